@@ -51,8 +51,9 @@ extern "C" {
 
 /* major * 1000 + minor.  2.0: tl_gemm_options gained raster_group and
  * force_split, and tl_plan gained tail_units, num_slots and raster_group; both
- * structs grew, so callers built against 1.x must be rebuilt.               */
-#define TL_VERSION 2000
+ * structs grew, so callers built against 1.x must be rebuilt.  2.1 added
+ * tl_attention_ex, tl_attention_bwd, tl_tree_attention and tl_rotary.         */
+#define TL_VERSION 2001
 
 #if defined(__GNUC__)
 #define TL_API __attribute__((visibility("default")))
@@ -211,6 +212,163 @@ TL_API tl_status tl_gemm_noalloc(const void *A, const void *B, const void *bias,
 TL_API tl_status tl_attention_fwd(const void *Q, const void *K, const void *V, void *O, float *lse,
                           int64_t batch, int64_t heads, int64_t seq_q, int64_t seq_k, int64_t head_dim,
                           tl_dtype dtype, int32_t causal, float softmax_scale, tl_stream stream);
+
+/*
+ * tl_attention_ex -- tl_attention_fwd for the attention of language models:
+ * shared key/value heads, capped scores, a bias that depends on distance,
+ * causal, document and prefix masks, strided tensors.
+ *
+ * With p_i = q_offset + i the place of query i among the keys, h its head and
+ * h' = h / (heads / kv_heads) the key/value head it shares,
+ *
+ *   u_ij     = scale Q[b,h,i,:] . K[b,h',j,:], with score_cap c > 0: c tanh(that / c)
+ *   y_ij     = u_ij - slopes[h] |p_i - j|
+ *   lse[i]   = log sum_j exp(y_ij),  O[i] = sum_j exp(y_ij - lse[i]) V[b,h',j,:]
+ *
+ * over the keys j that query i sees: with doc_offsets those of the document
+ * that holds p_i (documents cut the keys at ascending offsets
+ * o_0 <= o_1 <= ..., document d is [o_d, o_(d+1)), empty ones are fine;
+ * positions outside [o_0, o_num_docs) -- a padded end -- belong to none), with
+ * `causal` only j <= p_i and, with prefix_lens, the first prefix_lens keys of
+ * the document (of the sequence, without documents) besides.  A query that
+ * sees no key gets O = 0 and lse = -inf.  Offsets and prefixes live on the
+ * device and are not checked; out of order or out of range they leave some
+ * interval of valid keys.
+ *
+ *   Q, O   [batch][heads][seq_q][head_dim];  K, V [batch][kv_heads][seq_k][head_dim]
+ *   lse    batch * heads * seq_q floats, contiguous, or NULL
+ *
+ * head_dim is 64 or 128; seq_q, seq_k and q_offset + seq_q at most 2^31 - 257.
+ * Pointers are 16-byte aligned; strides are positive multiples of 8 elements,
+ * the last dimension is contiguous.  Rows of K and V that no query sees must
+ * still be finite (a weight of 0 times NaN is NaN).  Sums and softmax
+ * statistics are fp32; the weights are rounded to `dtype` before the product
+ * with V and O is rounded once.  Asynchronous on `stream`; allocates nothing;
+ * O must not overlap an input.
+ */
+typedef struct {
+    int32_t causal;              /* 1: query i sees keys j <= q_offset + i            */
+    float softmax_scale;         /* > 0, or 0 for 1 / sqrt(head_dim)                 */
+    float score_cap;             /* > 0: scores are capped by score_cap * tanh; 0: not */
+    int32_t reserved;            /* 0                                                */
+    const float *slopes;         /* [heads] floats on the device, or NULL: no bias    */
+    const int32_t *doc_offsets;  /* [batch][num_docs + 1] on the device, or NULL      */
+    int64_t num_docs;            /* documents of each batch entry; 0 without them     */
+    const int32_t *prefix_lens;  /* [batch][max(num_docs, 1)] on the device, or NULL; causal only */
+    int64_t q_offset;            /* >= 0: place of query 0 among the keys             */
+    int64_t kv_heads;            /* a divisor of heads; 0: heads                      */
+    /* strides of (batch, head, row) in elements; three zeros: contiguous             */
+    int64_t q_strides[3], k_strides[3], v_strides[3], o_strides[3];
+    int64_t do_strides[3], dq_strides[3], dk_strides[3], dv_strides[3];  /* tl_attention_bwd only */
+} tl_attention_options;
+
+TL_API tl_status tl_attention_ex(const void *Q, const void *K, const void *V, void *O, float *lse,
+                          int64_t batch, int64_t heads, int64_t seq_q, int64_t seq_k, int64_t head_dim,
+                          tl_dtype dtype, tl_stream stream, const tl_attention_options *options);
+
+/*
+ * tl_attention_bwd -- the gradients of tl_attention_ex: from dO, the inputs and
+ * the forward's O and lse (not NULL), dQ, dK and dV in `dtype`, written whole.
+ * The options are the forward's; slopes are constants and have no gradient.
+ *
+ *   P = exp(y - lse), dV = P^T dO, dX = P (dO V^T - rowsum(dO O)) (1 - (u / c)^2),
+ *   dQ = scale dX K, dK = scale dX^T Q, dK and dV summed over the heads that share them
+ *
+ * P and dX are rounded to `dtype` between the products (fp16 holds them scaled
+ * by powers of two, dX by one taken from the largest |dO|); every sum is fp32
+ * and has a fixed order, so results repeat bit for bit.  dO of queries that see
+ * no key does not count, but must be finite.  dQ, dK and dV must overlap
+ * neither the inputs nor one another.  The row sums and intervals live in a
+ * stream-ordered temporary (about 8 bytes a query and head).
+ */
+TL_API tl_status tl_attention_bwd(const void *dO, const void *Q, const void *K, const void *V, const void *O,
+                           const float *lse, void *dQ, void *dK, void *dV,
+                           int64_t batch, int64_t heads, int64_t seq_q, int64_t seq_k, int64_t head_dim,
+                           tl_dtype dtype, tl_stream stream, const tl_attention_options *options);
+
+/*
+ * tl_tree_attention -- attention of one or several new tokens of each request
+ * over a paged key/value cache: decoding (one token), a drafted chain, or a
+ * drafted tree that is being verified.
+ *
+ * Request b has context_lens[b] keys in the cache and, directly behind them,
+ * those of its `tokens` new tokens (tree_lens[b] of them when given; the caller
+ * has written them).  Key k of request b is row k % page_size of page
+ * block_table[b][k / page_size].  New token t sees the whole context, itself
+ * and its ancestors: parents[b][t] is the earlier token it hangs below, or -1
+ * for the context; parents NULL is the chain t - 1.  The formulas are
+ * tl_attention_ex's; for the distance bias a context key lies at its index and
+ * a new token at context_lens[b] + its depth.
+ *
+ *   Q, O         [batch][heads][tokens][head_dim]
+ *   K_cache, V_cache  [num_pages][page_size][kv_heads][head_dim]
+ *   block_table  [batch][max_pages] int32;  context_lens [batch] int32
+ *   parents      [batch][tokens] int32, or NULL
+ *   tree_lens    [batch] int32, or NULL; O and lse of tokens at or past it are
+ *                left as they were
+ *   lse          [batch][heads][tokens] floats, or NULL
+ *
+ * tokens at most 64, batch at most 4096, heads / kv_heads at most 128,
+ * page_size a multiple of 8, max_pages * page_size at most 2^31 - 257, head_dim
+ * 64 or 128.  Lengths on the device are held to what the table covers; a page
+ * index outside the cache reads as zeros, table entries behind a request's last
+ * key are not read, and rows of its last page behind that key may hold anything.
+ * Works with any lengths for one captured graph: the host reads none of them.
+ * Results repeat bit for bit on the same device.  The joined pieces of long
+ * requests live in a stream-ordered temporary.  Asynchronous on `stream`.
+ */
+typedef struct {
+    float softmax_scale;         /* > 0, or 0 for 1 / sqrt(head_dim)                 */
+    float score_cap;             /* as in tl_attention_options                       */
+    const float *slopes;         /* [heads], or NULL                                 */
+    int64_t table_stride;        /* block_table's row stride in entries; 0: max_pages */
+    int64_t q_strides[3], o_strides[3];   /* (batch, head, token); three zeros: contiguous */
+    int64_t k_strides[3], v_strides[3];   /* (page, row, head); three zeros: contiguous */
+} tl_tree_options;
+
+TL_API tl_status tl_tree_attention(const void *Q, const void *K_cache, const void *V_cache,
+                            const int32_t *block_table, const int32_t *context_lens, const int32_t *parents,
+                            const int32_t *tree_lens, void *O, float *lse,
+                            int64_t batch, int64_t heads, int64_t kv_heads, int64_t tokens,
+                            int64_t num_pages, int64_t page_size, int64_t max_pages, int64_t head_dim,
+                            tl_dtype dtype, tl_stream stream, const tl_tree_options *options);
+
+/*
+ * tl_rotary -- rotary positions of q and k in one launch:
+ *
+ *   (a, b) -> scale (a cos f - b sin f, a sin f + b cos f),  f = position * inv_freq[i]
+ *
+ * for the pairs i < rot_dim / 2 of each head: values (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) when interleaved; values from rot_dim on are copied.  With
+ * `inverse` the angle is -f: the inverse (for scale 1) and the backward of the
+ * same call.  Long contexts are served through inv_freq and scale.
+ *
+ *   Q, Q_out   [batch][heads][seq][head_dim];  K, K_out [batch][kv_heads][seq][head_dim],
+ *              or both NULL with kv_heads 0; an output may be its own input
+ *   positions  [batch][seq], or [seq] with positions_shared; int32 or int64
+ *   inv_freq   rot_dim / 2 floats on the device
+ *
+ * head_dim at most 1024, rot_dim even.  The angle is taken in double, sine and
+ * cosine in fp32, the result is rounded once.  Any 2-byte aligned tensors with
+ * positive strides and a contiguous last dimension; 16-byte aligned ones with
+ * strides and head_dim in multiples of 8 and rot_dim of 16 (8 interleaved) take
+ * the vectorised path.  Asynchronous on `stream`; allocates nothing.
+ */
+typedef struct {
+    int32_t interleaved;         /* 1: pairs (2 i, 2 i + 1)                          */
+    int32_t inverse;             /* 1: the negative angle                            */
+    float scale;                 /* > 0, or 0 for 1                                  */
+    int32_t positions_int64;     /* 1: positions are int64                           */
+    int32_t positions_shared;    /* 1: one row of positions for the whole batch       */
+    int32_t reserved;            /* 0                                                */
+    /* strides of (batch, head, token) in elements; three zeros: contiguous            */
+    int64_t q_strides[3], k_strides[3], qout_strides[3], kout_strides[3];
+} tl_rotary_options;
+
+TL_API tl_status tl_rotary(const void *Q, const void *K, void *Q_out, void *K_out, const void *positions,
+                    const float *inv_freq, int64_t batch, int64_t heads, int64_t kv_heads, int64_t seq,
+                    int64_t head_dim, int64_t rot_dim, tl_dtype dtype, tl_stream stream,
+                    const tl_rotary_options *options);
 
 /*
  * tl_softmax_rows -- Y[r, :] = softmax(X[r, :]) for each of `rows` rows of

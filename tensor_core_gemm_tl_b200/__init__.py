@@ -13,15 +13,17 @@ or library fallback.
 from __future__ import annotations
 
 from ._binding import (  # noqa: F401
-    LIB_PATH, Options, Plan, Status, TLError, TL_BF16, TL_EPI_BIAS, TL_EPI_BIAS_GELU, TL_EPI_GELU,
+    LIB_PATH, AttentionOptions, Options, Plan, RotaryOptions, Status, TLError, TreeOptions, TL_BF16, TL_EPI_BIAS, TL_EPI_BIAS_GELU, TL_EPI_GELU,
     TL_EPI_NONE, TL_EPI_BIAS_GELU_TANH, TL_EPI_GELU_TANH, TL_EPI_WITH_BIAS, TL_F16,
-    SIGNATURES, tl_attention_fwd, tl_check_device, tl_config_name, tl_gemm, tl_gemm_ex, tl_gemm_noalloc,
+    SIGNATURES, tl_attention_bwd, tl_attention_ex, tl_attention_fwd, tl_rotary, tl_tree_attention, tl_check_device, tl_config_name, tl_gemm, tl_gemm_ex, tl_gemm_noalloc,
     tl_gemm_plan, tl_num_configs, tl_softmax_rows, tl_vector_add,
     tl_status_string, tl_version,
 )
 
 __all__ = [
-    "gemm", "attention", "softmax", "vector_add", "check_device", "plan", "configs", "tl_attention_fwd",
+    "gemm", "attention", "attention_ex", "attention_backward", "tree_attention", "rotary", "rotary_frequencies",
+    "AttentionOptions", "TreeOptions", "RotaryOptions", "tl_attention_ex", "tl_attention_bwd", "tl_tree_attention",
+    "tl_rotary", "softmax", "vector_add", "check_device", "plan", "configs", "tl_attention_fwd",
     "tl_softmax_rows", "tl_vector_add", "Options", "Plan", "Status", "TLError",
     "tl_gemm", "tl_gemm_ex", "tl_gemm_noalloc", "tl_check_device", "tl_gemm_plan", "tl_num_configs", "tl_config_name",
     "tl_status_string", "tl_version", "TL_F16", "TL_BF16", "TL_EPI_NONE", "TL_EPI_BIAS_GELU",
@@ -155,6 +157,313 @@ def attention(q, k, v, causal: bool = False, scale: float = 0.0, out=None, lse=N
     if st != 0:
         raise TLError(st, "tl_attention_fwd")
     return out
+
+
+def _require_rows(name, t, device, dtype, shape):
+    """Raise ValueError unless `t` is a CUDA tensor on `device` of `dtype` and
+    `shape` whose rows the kernels can address: contiguous last dimension,
+    positive strides in multiples of 8 elements, a 16-byte aligned base."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 or any(n > 1 and (s <= 0 or s % 8) for n, s in zip(t.shape[:-1], st[:-1])):
+        raise ValueError(f"{name} must have a contiguous last dimension and positive strides in multiples of 8 "
+                         f"elements, got strides {tuple(st)}")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _strides3(t, order=(0, 1, 2)):
+    """Strides of a 4-D tensor's outer dimensions for the C ABI (any positive
+    value for a dimension of one element)."""
+    return tuple(max(t.stride(i), 1) if t.shape[i] > 1 else t.shape[-1] for i in order)
+
+
+def _require_ints(name, t, device, shape):
+    _require_device_tensor(name, t, device, shape=shape)
+    import torch
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name} must be int32, got {t.dtype}")
+
+
+def _score_arguments(scale, score_cap, slopes, heads, device):
+    """The softmax scale, cap and bias slopes, checked."""
+    import torch
+    if not (scale >= 0.0 and scale != float("inf")) or not (score_cap >= 0.0 and score_cap != float("inf")):
+        raise ValueError("scale and score_cap must be finite and not negative")
+    if slopes is not None:
+        _require_device_tensor("slopes", slopes, device, torch.float32, (heads,))
+        if getattr(slopes, "requires_grad", False):
+            raise ValueError("slopes are constants: they get no gradient")
+
+
+def _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset):
+    """Checks what attention_ex and attention_backward share; returns the options."""
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3] \
+            or k.shape[1] < 1 or q.shape[1] % k.shape[1]:
+        raise ValueError(f"shapes q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)} do not match")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    _dtype_code(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _require_rows(name, t, q.device, q.dtype, t.shape)
+    B, H = q.shape[:2]
+    _score_arguments(scale, score_cap, slopes, H, q.device)
+    docs = 0
+    if doc_offsets is not None:
+        if doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
+            raise ValueError(f"doc_offsets must be (batch, documents + 1), got {tuple(doc_offsets.shape)}")
+        docs = doc_offsets.shape[1] - 1
+        _require_ints("doc_offsets", doc_offsets, q.device, (B, docs + 1))
+    if prefix is not None:
+        if not causal:
+            raise ValueError("a prefix needs causal=True (without it every key is seen already)")
+        _require_ints("prefix", prefix, q.device, (B, max(docs, 1)))
+    if q_offset < 0:
+        raise ValueError("q_offset must not be negative")
+    return AttentionOptions(causal=int(bool(causal)), softmax_scale=scale, score_cap=score_cap,
+                            slopes=slopes.data_ptr() if slopes is not None else None,
+                            doc_offsets=doc_offsets.data_ptr() if docs else None, num_docs=docs,
+                            prefix_lens=prefix.data_ptr() if prefix is not None else None, q_offset=q_offset,
+                            kv_heads=k.shape[1], q_strides=_strides3(q), k_strides=_strides3(k),
+                            v_strides=_strides3(v))
+
+
+def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap: float = 0.0, slopes=None,
+                 doc_offsets=None, prefix=None, q_offset: int = 0, out=None, lse=None, stream=None):
+    """Attention forward of language models, for CUDA tensors q (B, H, Sq, D)
+    and k, v (B, Hkv, Sk, D), fp16 or bf16, D in {64, 128}, H a multiple of Hkv,
+    of any strides in multiples of 8 with a contiguous last dimension.
+
+    Scores are scale q.k (scale 0 = 1/sqrt(D)), capped as
+    score_cap * tanh(. / score_cap) when score_cap > 0, less
+    slopes[h] * |q_offset + i - j| when ``slopes`` (H floats) is given.  Query i
+    stands at key q_offset + i.  ``causal`` hides the keys behind it;
+    ``doc_offsets`` (B, docs + 1) int32, ascending, keeps each query inside its
+    document (positions outside the first to the last offset see nothing);
+    ``prefix`` (B, max(docs, 1)) int32 opens the first keys of each document (of
+    the sequence) to causal queries.  Queries that see nothing give 0 and lse
+    -inf.  Returns out, shaped and by default laid out like q; fills ``lse``
+    (B, H, Sq) float32 if given (attention_backward needs it)."""
+    import torch
+    opt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
+    B, H, Sq, D = q.shape
+    if lse is not None:
+        _require_device_tensor("lse", lse, q.device, torch.float32, (B, H, Sq))
+    if out is None:
+        out = torch.empty_like(q)
+    _require_rows("out", out, q.device, q.dtype, q.shape)
+    opt.o_strides = _strides3(out)
+    s = stream if stream is not None else torch.cuda.current_stream(q.device)
+    with torch.cuda.device(q.device):
+        st = tl_attention_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                             lse.data_ptr() if lse is not None else 0, B, H, Sq, k.shape[2], D, _dtype_code(q),
+                             s.cuda_stream, opt)
+    if st != 0:
+        raise TLError(st, "tl_attention_ex")
+    return out
+
+
+def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: float = 0.0, score_cap: float = 0.0,
+                       slopes=None, doc_offsets=None, prefix=None, q_offset: int = 0, dq=None, dk=None, dv=None,
+                       stream=None):
+    """Gradients (dq, dk, dv) of attention_ex, from its inputs, its ``out`` and
+    ``lse`` and the gradient ``dout`` of out; the options are the forward's.
+    dk and dv are summed over the heads that share them.  Results repeat bit
+    for bit."""
+    import torch
+    opt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
+    B, H, Sq, D = q.shape
+    _require_rows("dout", dout, q.device, q.dtype, q.shape)
+    _require_rows("out", out, q.device, q.dtype, q.shape)
+    _require_device_tensor("lse", lse, q.device, torch.float32, (B, H, Sq))
+    # every given tensor is checked before anything is allocated
+    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if g is not None:
+            _require_rows(name, g, q.device, q.dtype, like.shape)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for name, g in (("dq", dq), ("dk", dk), ("dv", dv)):
+        _require_rows(name, g, q.device, q.dtype, g.shape)
+    opt.o_strides, opt.do_strides = _strides3(out), _strides3(dout)
+    opt.dq_strides, opt.dk_strides, opt.dv_strides = _strides3(dq), _strides3(dk), _strides3(dv)
+    s = stream if stream is not None else torch.cuda.current_stream(q.device)
+    with torch.cuda.device(q.device):
+        st = tl_attention_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                              lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Sq, k.shape[2], D,
+                              _dtype_code(q), s.cuda_stream, opt)
+    if st != 0:
+        raise TLError(st, "tl_attention_bwd")
+    return dq, dk, dv
+
+
+def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None, *, tree_lens=None,
+                   scale: float = 0.0, score_cap: float = 0.0, slopes=None, out=None, lse=None, stream=None):
+    """Attention of the new tokens q (B, H, T, D), T up to 64, over paged caches
+    k_cache, v_cache (pages, page_size, Hkv, D): one token a request (decoding),
+    a drafted chain, or a drafted tree.
+
+    Request b has context_lens[b] keys in the cache and its new tokens' keys
+    directly behind them, already written; key n is row n % page_size of page
+    block_table[b, n // page_size] ((B, max_pages) int32).  Token t sees the
+    context, itself and its ancestors by ``parents`` (B, T) int32 (an earlier
+    token, or -1; None: a chain).  ``tree_lens`` (B,) int32 gives shorter trees:
+    out and lse of later tokens stay as they were.  Scale, cap and bias as in
+    attention_ex, a new token standing at context_lens[b] plus its depth.
+    Returns out, like q; fills ``lse`` (B, H, T) float32 if given."""
+    import torch
+    if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != q.shape[3] \
+            or k_cache.shape[2] < 1 or q.shape[1] % k_cache.shape[2]:
+        raise ValueError(f"shapes q{tuple(q.shape)} k_cache{tuple(k_cache.shape)} v_cache{tuple(v_cache.shape)} "
+                         "do not match")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dt = _dtype_code(q)
+    B, H, T, D = q.shape
+    pages, page_size, Hk, _ = k_cache.shape
+    _require_rows("q", q, q.device, q.dtype, q.shape)
+    _require_rows("k_cache", k_cache, q.device, q.dtype, k_cache.shape)
+    _require_rows("v_cache", v_cache, q.device, q.dtype, v_cache.shape)
+    if block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise ValueError(f"block_table must be (batch, pages), got {tuple(block_table.shape)}")
+    max_pages = block_table.shape[1]
+    _require_ints("block_table", block_table, q.device, (B, max_pages))
+    _require_ints("context_lens", context_lens, q.device, (B,))
+    if parents is not None:
+        _require_ints("parents", parents, q.device, (B, T))
+    if tree_lens is not None:
+        _require_ints("tree_lens", tree_lens, q.device, (B,))
+    _score_arguments(scale, score_cap, slopes, H, q.device)
+    if lse is not None:
+        _require_device_tensor("lse", lse, q.device, torch.float32, (B, H, T))
+    if out is None:
+        out = torch.empty_like(q)
+    _require_rows("out", out, q.device, q.dtype, q.shape)
+    opt = TreeOptions(softmax_scale=scale, score_cap=score_cap,
+                      slopes=slopes.data_ptr() if slopes is not None else None, q_strides=_strides3(q),
+                      o_strides=_strides3(out), k_strides=_strides3(k_cache), v_strides=_strides3(v_cache))
+    s = stream if stream is not None else torch.cuda.current_stream(q.device)
+    with torch.cuda.device(q.device):
+        st = tl_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                               context_lens.data_ptr(), parents.data_ptr() if parents is not None else 0,
+                               tree_lens.data_ptr() if tree_lens is not None else 0, out.data_ptr(),
+                               lse.data_ptr() if lse is not None else 0, B, H, Hk, T, pages, page_size, max_pages, D,
+                               dt, s.cuda_stream, opt)
+    if st != 0:
+        raise TLError(st, "tl_tree_attention")
+    return out
+
+
+def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
+           out_q=None, out_k=None, stream=None):
+    """Rotary positions of q (B, H, S, D) and k (B, Hkv, S, D) (or None), fp16 or
+    bf16, any positive strides with a contiguous last dimension; returns
+    (out_q, out_k).
+
+    ``positions`` is (B, S) or (S,), int32 or int64; ``inv_freq`` (float32, half
+    the rotated values) comes from rotary_frequencies or a model.  The first
+    2 * len(inv_freq) values of a head are rotated in pairs (i, i + half), or
+    (2 i, 2 i + 1) when ``interleaved``, and multiplied by ``scale``; the rest is
+    copied.  ``inverse`` turns back: it is the backward of the same call, on the
+    gradients.  ``out_q`` may be q and ``out_k`` may be k."""
+    import torch
+    if q.dim() != 4 or not q.is_cuda:
+        raise ValueError("q must be a 4-D CUDA tensor")
+    dt = _dtype_code(q)
+    B, H, S, D = q.shape
+
+    def rows(name, t, shape):
+        if not t.is_cuda or t.device != q.device or t.dtype != q.dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be a {q.dtype} CUDA tensor of shape {tuple(shape)} on {q.device}")
+        if t.stride(-1) != 1 or any(n > 1 and st <= 0 for n, st in zip(t.shape[:-1], t.stride()[:-1])):
+            raise ValueError(f"{name} must have a contiguous last dimension and positive strides")
+
+    rows("q", q, q.shape)
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must be 4-D")
+        rows("k", k, (B, k.shape[1], S, D))
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    shared = positions.dim() == 1
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
+    _require_device_tensor("positions", positions, q.device, shape=(S,) if shared else (B, S))
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be 1-D")
+    _require_device_tensor("inv_freq", inv_freq, q.device, torch.float32)
+    if not 2 <= 2 * inv_freq.shape[0] <= D:
+        raise ValueError(f"inv_freq has {inv_freq.shape[0]} frequencies for heads of {D} values")
+    if not (scale > 0.0 and scale != float("inf")):
+        raise ValueError("scale must be positive and finite")
+    for name, o, t in (("out_q", out_q, q), ("out_k", out_k, k)):
+        if o is not None:
+            rows(name, o, t.shape)
+    out_q = torch.empty_like(q) if out_q is None else out_q
+    if k is not None and out_k is None:
+        out_k = torch.empty_like(k)
+    opt = RotaryOptions(interleaved=int(bool(interleaved)), inverse=int(bool(inverse)), scale=scale,
+                        positions_int64=int(positions.dtype == torch.int64), positions_shared=int(shared),
+                        q_strides=_strides3(q), qout_strides=_strides3(out_q))
+    if k is not None:
+        opt.k_strides, opt.kout_strides = _strides3(k), _strides3(out_k)
+    s = stream if stream is not None else torch.cuda.current_stream(q.device)
+    with torch.cuda.device(q.device):
+        st = tl_rotary(q.data_ptr(), k.data_ptr() if k is not None else 0, out_q.data_ptr(),
+                       out_k.data_ptr() if k is not None else 0, positions.data_ptr(), inv_freq.data_ptr(), B, H,
+                       k.shape[1] if k is not None else 0, S, D, 2 * inv_freq.shape[0], dt, s.cuda_stream, opt)
+    if st != 0:
+        raise TLError(st, "tl_rotary")
+    return out_q, out_k
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                       original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(inv_freq, scale) for rotary: base^(-2 i / rot_dim), i < rot_dim / 2, as
+    float32 on ``device``, and the factor of the rotated values.
+
+    ``scaling`` serves contexts ``factor`` times the trained length: "linear"
+    divides every frequency by it; "ntk" raises the base by
+    factor^(rot_dim / (rot_dim - 2)), so that only the slow pairs stretch;
+    "yarn" divides the pairs that turn fewer than ``beta_slow`` times over
+    ``original_length`` positions, keeps those that turn more than ``beta_fast``
+    times, blends linearly in the pair's index in between, and returns the scale
+    0.1 ln(factor) + 1 (else the scale is 1)."""
+    import math
+
+    import torch
+    if rot_dim < 2 or rot_dim % 2 or not base > 0 or not factor >= 1.0:
+        raise ValueError("rot_dim must be even and positive, base positive, factor at least 1")
+    half = rot_dim // 2
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim of 4 at least")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * i / rot_dim) for i in range(half)]
+    scale = 1.0
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if original_length < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn needs original_length and beta_fast > beta_slow > 0")
+
+        def index(turns):  # the pair that turns so many times over original_length positions
+            return rot_dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo = min(max(math.floor(index(beta_fast)), 0), half - 1)
+        hi = min(max(math.ceil(index(beta_slow)), 0), half - 1)
+        for i in range(half):
+            blend = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)  # 0: kept, 1: divided
+            freq[i] = freq[i] * (1.0 - blend) + freq[i] / factor * blend
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.tensor(freq, dtype=torch.float32, device=device), scale
 
 
 def softmax(x, out=None, stream=None):

@@ -62,6 +62,40 @@ class Plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+_I64x3 = ctypes.c_int64 * 3
+
+
+class AttentionOptions(ctypes.Structure):
+    """tl_attention_options: causal, softmax_scale (0 = 1/sqrt(head_dim)),
+    score_cap (0 = none), slopes, doc_offsets with num_docs, prefix_lens (device
+    pointers or None), q_offset, kv_heads (0 = heads) and the tensors' strides of
+    (batch, head, row) in elements (three zeros = contiguous)."""
+    _fields_ = [("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("score_cap", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("doc_offsets", ctypes.c_void_p),
+                ("num_docs", ctypes.c_int64), ("prefix_lens", ctypes.c_void_p), ("q_offset", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("q_strides", _I64x3), ("k_strides", _I64x3), ("v_strides", _I64x3),
+                ("o_strides", _I64x3), ("do_strides", _I64x3), ("dq_strides", _I64x3), ("dk_strides", _I64x3),
+                ("dv_strides", _I64x3)]
+
+
+class TreeOptions(ctypes.Structure):
+    """tl_tree_options: softmax_scale, score_cap, slopes, table_stride (0 =
+    max_pages), strides of q and o (batch, head, token) and of the caches (page,
+    row, head)."""
+    _fields_ = [("softmax_scale", ctypes.c_float), ("score_cap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("q_strides", _I64x3), ("o_strides", _I64x3),
+                ("k_strides", _I64x3), ("v_strides", _I64x3)]
+
+
+class RotaryOptions(ctypes.Structure):
+    """tl_rotary_options: interleaved, inverse, scale (0 = 1), positions_int64,
+    positions_shared and the tensors' strides of (batch, head, token)."""
+    _fields_ = [("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("positions_int64", ctypes.c_int32), ("positions_shared", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("q_strides", _I64x3), ("k_strides", _I64x3),
+                ("qout_strides", _I64x3), ("kout_strides", _I64x3)]
+
+
 # name -> (restype, argtypes); every symbol include/tl_gemm.h declares
 _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 SIGNATURES = {
@@ -74,6 +108,10 @@ SIGNATURES = {
     "tl_vector_add": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
     "tl_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, ctypes.c_int, _I32,
                                         ctypes.c_float, _P]),
+    "tl_attention_ex": (ctypes.c_int, [_P] * 5 + [_I64] * 5 + [ctypes.c_int, _P, ctypes.POINTER(AttentionOptions)]),
+    "tl_attention_bwd": (ctypes.c_int, [_P] * 9 + [_I64] * 5 + [ctypes.c_int, _P, ctypes.POINTER(AttentionOptions)]),
+    "tl_tree_attention": (ctypes.c_int, [_P] * 9 + [_I64] * 8 + [ctypes.c_int, _P, ctypes.POINTER(TreeOptions)]),
+    "tl_rotary": (ctypes.c_int, [_P] * 6 + [_I64] * 6 + [ctypes.c_int, _P, ctypes.POINTER(RotaryOptions)]),
     "tl_gemm_plan": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _I32,
                                     ctypes.POINTER(Options), ctypes.POINTER(Plan)]),
     "tl_num_configs": (_I32, []),
@@ -125,6 +163,38 @@ def tl_attention_fwd(Q, K, V, O, lse, batch, heads, seq_q, seq_k, head_dim, dtyp
     """Attention forward on device pointers; returns the tl_status code."""
     return _lib.tl_attention_fwd(Q, K, V, O, lse or None, batch, heads, seq_q, seq_k, head_dim, dtype,
                                  int(bool(causal)), float(softmax_scale), stream or None)
+
+
+def tl_attention_ex(Q, K, V, O, lse, batch, heads, seq_q, seq_k, head_dim, dtype, stream=0,
+                    options: AttentionOptions | None = None) -> int:
+    """Attention forward with masks, caps, bias and shared heads on device pointers; returns the tl_status code."""
+    return _lib.tl_attention_ex(Q, K, V, O, lse or None, batch, heads, seq_q, seq_k, head_dim, dtype, stream or None,
+                                ctypes.byref(options) if options is not None else None)
+
+
+def tl_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, batch, heads, seq_q, seq_k, head_dim, dtype, stream=0,
+                     options: AttentionOptions | None = None) -> int:
+    """The gradients of tl_attention_ex on device pointers; returns the tl_status code."""
+    return _lib.tl_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, batch, heads, seq_q, seq_k, head_dim, dtype,
+                                 stream or None, ctypes.byref(options) if options is not None else None)
+
+
+def tl_tree_attention(Q, K_cache, V_cache, block_table, context_lens, parents, tree_lens, O, lse, batch, heads,
+                      kv_heads, tokens, num_pages, page_size, max_pages, head_dim, dtype, stream=0,
+                      options: TreeOptions | None = None) -> int:
+    """New tokens against a paged cache, on device pointers; returns the tl_status code."""
+    return _lib.tl_tree_attention(Q, K_cache, V_cache, block_table, context_lens, parents or None, tree_lens or None,
+                                  O, lse or None, batch, heads, kv_heads, tokens, num_pages, page_size, max_pages,
+                                  head_dim, dtype, stream or None,
+                                  ctypes.byref(options) if options is not None else None)
+
+
+def tl_rotary(Q, K, Q_out, K_out, positions, inv_freq, batch, heads, kv_heads, seq, head_dim, rot_dim, dtype,
+              stream=0, options: RotaryOptions | None = None) -> int:
+    """Rotary positions of q and k on device pointers; returns the tl_status code."""
+    return _lib.tl_rotary(Q, K or None, Q_out, K_out or None, positions, inv_freq, batch, heads, kv_heads, seq,
+                          head_dim, rot_dim, dtype, stream or None,
+                          ctypes.byref(options) if options is not None else None)
 
 
 def tl_softmax_rows(X, Y, rows, cols, dtype, stream=0) -> int:

@@ -14,6 +14,7 @@ import glob
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -47,14 +48,33 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(f) > t for f in inputs())
 
 
+def _compile(src: str, obj: str, force: bool, flags) -> None:
+    """One source to an object; kept when it is newer than everything the last
+    compile of it read (nvcc's own dependency list beside the object)."""
+    deps = obj + ".d"
+    if not force and os.path.exists(obj) and os.path.exists(deps):
+        with open(deps) as fh:
+            read = fh.read().split(":", 1)[1].replace("\\\n", " ").split()
+        t = os.path.getmtime(obj)
+        if all(os.path.exists(f) and os.path.getmtime(f) <= t for f in read):
+            return
+    tmp = obj + f".tmp{os.getpid()}"
+    subprocess.check_call([NVCC, *flags, "-MMD", "-MF", deps, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", tmp])
+    os.replace(tmp, obj)
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, out: str = LIB, extra=()) -> str:
     if not force and not stale(out):
         return out
+    objdir = os.path.join(ROOT, "build", os.path.basename(out))
+    os.makedirs(objdir, exist_ok=True)
+    flags = [f for f in NVCC_FLAGS if f != "-shared"] + list(extra) + (["-Xptxas", "-v"] if ptxas_verbose else [])
+    objs = [os.path.join(objdir, os.path.basename(s) + ".o") for s in sources()]
+    # the sources are independent: compile them side by side
+    with ThreadPoolExecutor(max_workers=len(objs)) as pool:
+        list(pool.map(lambda so: _compile(so[0], so[1], force, flags), zip(sources(), objs)))
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [NVCC, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *sources()]
-    if ptxas_verbose:
-        cmd[1:1] = ["-Xptxas", "-v"]
-    subprocess.check_call(cmd)
+    subprocess.check_call([NVCC, *NVCC_FLAGS, "-o", tmp, *objs])
     os.replace(tmp, out)
     return out
 

@@ -1,0 +1,123 @@
+// attention_common.cuh -- what the masked attention kernels share: 4- and 5-D
+// TMA loads, the interval of keys a query sees, and the score's capping and
+// distance bias.
+//
+// With a = q . k and p_i = q_offset + i (the place of query i among the keys),
+//
+//   u_ij = scale a                          or   cap tanh(scale a / cap)
+//   y_ij = u_ij - slope_h |p_i - j|
+//
+// and query i sees the keys lo_i <= j < hi_i: documents cut [0, seq_k) at
+// their offsets, a causal query sees nothing after p_i, and a prefix opens the
+// first keys of its document to everyone in it.  All three masks together are
+// one interval a query, which is why no mask is read for each score.
+#pragma once
+
+#include "device_common.cuh"
+#include "sm100.cuh"
+
+namespace tl {
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w, int32_t v)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+        : "memory");
+}
+
+// min that keeps a NaN
+__device__ __forceinline__ float fmin_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+struct MaskParams {
+    int32_t Sq, Sk, q_offset, causal;
+    const int32_t *doc_offsets;  // [batch][num_docs + 1], or null
+    int32_t num_docs;
+    const int32_t *prefix;       // [batch][max(num_docs, 1)], or null
+};
+
+// Document offsets kept in shared memory while rows look theirs up
+constexpr int kDocsInSmem = 512;
+
+// The keys query row `i` of batch entry `b` sees, [x, y); empty for rows past
+// the queries or outside every document.  `docs` are the batch entry's
+// offsets (shared or global memory).  Offsets out of order or out of range
+// give some interval inside [0, Sk], never an access outside it.
+__device__ __forceinline__ int2 visible_keys(const MaskParams &m, const int32_t *docs, int b, int i)
+{
+    if (i >= m.Sq)
+        return make_int2(0, 0);
+    const int pos = m.q_offset + i;
+    int lo = 0, hi = m.Sk, d = 0;
+    if (m.doc_offsets) {
+        // the last document that begins at or before pos (empty documents end where they begin)
+        int a = 0, n = m.num_docs;
+        while (a < n) {
+            const int mid = (a + n) >> 1;
+            if (docs[mid] <= pos)
+                a = mid + 1;
+            else
+                n = mid;
+        }
+        d = a - 1;
+        if (d < 0)
+            return make_int2(0, 0);
+        lo = docs[d];
+        hi = docs[d + 1];
+        if (pos >= hi)
+            return make_int2(0, 0);
+    }
+    if (m.causal) {
+        int64_t last = static_cast<int64_t>(pos) + 1;
+        if (m.prefix) {
+            const int64_t open = static_cast<int64_t>(lo) +
+                                 m.prefix[static_cast<int64_t>(b) * max(m.num_docs, 1) + d];
+            last = open > last ? open : last;
+        }
+        hi = static_cast<int>(last < hi ? last : hi);
+    }
+    lo = max(lo, 0);
+    hi = min(hi, m.Sk);
+    return hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+struct ScoreParams {
+    float scale_log2;  // scale * log2(e)
+    float cap_arg;     // 2 scale log2(e) / cap: e^(2 x) = 2^(cap_arg a) for x = scale a / cap
+    float cap_log2;    // cap * log2(e)
+    const float *slopes;  // [heads], or null
+};
+
+// tanh x = 1 - 2 / (1 + e^(2x)) of two scores at once: one reciprocal of the
+// product of the two denominators serves both, so a pair costs two 2^x and
+// one reciprocal.  The exponent is held below 2^60 (tanh is 1 to 2^-59 there)
+// so that the product stays finite.  The result is absolutely exact to about
+// 2^-22, which is what a score needs: cap 50 leaves 1e-5 in y.  r receives
+// 1 / (1 + e^(2x)): tanh x = 1 - 2 r and 1 - tanh^2 x = 4 r (1 - r).
+__device__ __forceinline__ float2 cap_reciprocals(float2 a, float cap_arg)
+{
+    const float2 z = fmul2(a, splat2(cap_arg));
+    const float2 d = fadd2(make_float2(exp2_approx_ftz(fmin_nan(z.x, 60.0f)), exp2_approx_ftz(fmin_nan(z.y, 60.0f))),
+                           splat2(1.0f));
+    const float r = rcp_approx(d.x * d.y);
+    return make_float2(r * d.y, r * d.x);
+}
+
+} // namespace tl

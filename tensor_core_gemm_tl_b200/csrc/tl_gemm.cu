@@ -17,14 +17,83 @@
 #include <unordered_map>
 
 #include "tl_gemm.h"
+#include "host_common.h"
 #include "gemm_kernel.cuh"
 #include "attention_kernel.cuh"
 #include "rowwise_kernels.cuh"
 
 namespace tl {
+
+// ------------------------------------------------------------------ shared with the other translation units
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+static std::mutex g_mu;
+static std::unordered_map<int, DeviceState> g_dev;
+
+tl_status device_state(DeviceState **out)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return TL_ERR_CUDA;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceState &d = g_dev[dev];
+    if (d.num_sms == 0) {
+        int sms = 0, major = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+            return TL_ERR_CUDA;
+        d.num_sms = sms;
+        d.cc_major = major;
+    }
+    *out = &d;
+    return TL_OK;
+}
+
+tl_status ensure_pool(DeviceState *d)
+{
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (d->pool)
+        return TL_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return TL_ERR_CUDA;
+    cudaMemPoolProps props{};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.handleTypes = cudaMemHandleTypeNone;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    if (cudaMemPoolCreate(&d->pool, &props) != cudaSuccess)
+        return TL_ERR_CUDA;
+    uint64_t keep = ~0ull;  // keep freed blocks for reuse by later calls
+    cudaMemPoolSetAttribute(d->pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    return TL_OK;
+}
+
+tl_status raise_smem_limit(DeviceState *d, const void *fn, int bytes)
+{
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto it = d->smem_set.find(fn);
+    if (it != d->smem_set.end())
+        return TL_OK;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return TL_ERR_CUDA;
+    d->smem_set[fn] = true;
+    return TL_OK;
+}
+
 namespace {
 
-constexpr uint64_t kDefaultTimeoutNs = 10ull * 1000 * 1000 * 1000;
 constexpr int kDefaultRasterGroup = 8;  // output-tile rows per rasterisation group
 
 using KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, GemmParams);
@@ -107,8 +176,6 @@ int config_index(const char *name)
             return i;
     return -1;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How the tiles of one launch are cut into work items.  Tiles fill whole
 // rounds of `units` (CTAs, or CTA pairs) first.  The tiles of a last, partial
@@ -218,8 +285,6 @@ int choose_config(int64_t M, int64_t N, int64_t K, int dtype, int epi, int num_s
     *group = 0;
     return model_config(M, N, K, num_sms);
 }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 struct Plan {
     tl_plan pub;
@@ -379,24 +444,6 @@ tl_status make_plan(const void *A, const void *B, const void *bias, void *C, int
     return TL_OK;
 }
 
-// ------------------------------------------------------------------ driver API
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<EncodeTiledFn>(nullptr);
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
 // 2-D row-major matrix of 16-bit values: `rows` x `cols`, row length `ld`;
 // box of box_cols (<= 64, 128 B) x box_rows, 128-byte swizzle.
 bool encode_2d(CUtensorMap *map, const void *base, int dtype, int64_t rows, int64_t cols, int64_t ld,
@@ -416,68 +463,6 @@ bool encode_2d(CUtensorMap *map, const void *base, int dtype, int64_t rows, int6
 }
 
 // ------------------------------------------------------------------ per-device state
-struct DeviceState {
-    int num_sms = 0;
-    int cc_major = 0;
-    cudaMemPool_t pool = nullptr;
-    std::unordered_map<const void *, bool> smem_set;  // kernels whose smem limit is raised
-    std::unordered_map<const void *, int> max_clusters;  // resident clusters of two, per kernel
-};
-
-std::mutex g_mu;
-std::unordered_map<int, DeviceState> g_dev;
-
-tl_status device_state(DeviceState **out)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return TL_ERR_CUDA;
-    std::lock_guard<std::mutex> lk(g_mu);
-    DeviceState &d = g_dev[dev];
-    if (d.num_sms == 0) {
-        int sms = 0, major = 0;
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-            return TL_ERR_CUDA;
-        d.num_sms = sms;
-        d.cc_major = major;
-    }
-    *out = &d;
-    return TL_OK;
-}
-
-tl_status ensure_pool(DeviceState *d)
-{
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (d->pool)
-        return TL_OK;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return TL_ERR_CUDA;
-    cudaMemPoolProps props{};
-    props.allocType = cudaMemAllocationTypePinned;
-    props.handleTypes = cudaMemHandleTypeNone;
-    props.location.type = cudaMemLocationTypeDevice;
-    props.location.id = dev;
-    if (cudaMemPoolCreate(&d->pool, &props) != cudaSuccess)
-        return TL_ERR_CUDA;
-    uint64_t keep = ~0ull;  // keep freed blocks for reuse by later calls
-    cudaMemPoolSetAttribute(d->pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    return TL_OK;
-}
-
-tl_status raise_smem_limit(DeviceState *d, KernelFn fn, int bytes)
-{
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto it = d->smem_set.find(reinterpret_cast<const void *>(fn));
-    if (it != d->smem_set.end())
-        return TL_OK;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return TL_ERR_CUDA;
-    d->smem_set[reinterpret_cast<const void *>(fn)] = true;
-    return TL_OK;
-}
-
 tl_status max_active_clusters(DeviceState *d, KernelFn fn, const cudaLaunchConfig_t &cfg, int *out)
 {
     {
@@ -554,7 +539,7 @@ tl_status launch_gemm(const Plan &p, const void *A, const void *B, const void *b
     const bool tma_store = store == STORE_TMA;
     const int bt = (opt && opt->b_layout == 1) ? 1 : 0;
     KernelFn fn = c.fn[dtype][epi != 0][store][bt];
-    tl_status st = raise_smem_limit(d, fn, c.smem_bytes);
+    tl_status st = raise_smem_limit(d, reinterpret_cast<const void *>(fn), c.smem_bytes);
     if (st != TL_OK)
         return st;
 
@@ -643,7 +628,7 @@ tl_status device_plan(DeviceState *d, const void *A, const void *B, const void *
     if (c.ctas != 2)
         return TL_OK;
     KernelFn fn = c.fn[dtype][epi != 0][store_mode(p->pub, opt)][(opt && opt->b_layout == 1) ? 1 : 0];
-    if ((st = raise_smem_limit(d, fn, c.smem_bytes)) != TL_OK)
+    if ((st = raise_smem_limit(d, reinterpret_cast<const void *>(fn), c.smem_bytes)) != TL_OK)
         return st;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
@@ -802,7 +787,7 @@ tl_status attention_impl(const void *Q, const void *K, const void *V, void *O, f
         if (fa.numRegs < e.launch_regs)
             return TL_ERR_UNSUPPORTED;
     }
-    if ((st = raise_smem_limit(d, reinterpret_cast<KernelFn>(fn), e.smem_bytes)) != TL_OK)
+    if ((st = raise_smem_limit(d, reinterpret_cast<const void *>(fn), e.smem_bytes)) != TL_OK)
         return st;
     const int64_t BH = batch * heads;
     CUtensorMap tq, tk, tv;
@@ -939,7 +924,7 @@ tl_status softmax_impl(const void *X, void *Y, int64_t rows, int64_t cols, int d
         // boundary as x (then every row's x and y do)
         const int y_vec = ((reinterpret_cast<uintptr_t>(X) - reinterpret_cast<uintptr_t>(Y)) & 15) == 0;
         auto launch = [&](auto fn) -> tl_status {
-            tl_status r = raise_smem_limit(d, reinterpret_cast<KernelFn>(fn), static_cast<int>(kSoftmaxSmemMax));
+            tl_status r = raise_smem_limit(d, reinterpret_cast<const void *>(fn), static_cast<int>(kSoftmaxSmemMax));
             if (r != TL_OK)
                 return r;
             const dim3 g(static_cast<unsigned>(resident_grid(d, fn, 512, static_cast<size_t>(smem), rows)));
@@ -1021,7 +1006,7 @@ tl_status noalloc_setup(DeviceState *d, void **scratch)
                     for (int st = 0; st < 2; ++st)
                         for (int bt = 0; bt < 2; ++bt) {
                             KernelFn fn = c.fn[dt][epi][st][bt];
-                            tl_status r = raise_smem_limit(d, fn, c.smem_bytes);
+                            tl_status r = raise_smem_limit(d, reinterpret_cast<const void *>(fn), c.smem_bytes);
                             if (r != TL_OK)
                                 return r;
                             if (c.ctas == 2) {
@@ -1135,11 +1120,15 @@ tl_status tl_check_device(tl_stream stream, uint32_t *detail)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return TL_ERR_CUDA;
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&v, tl::g_device_error, sizeof(v)) != cudaSuccess)
-        return TL_ERR_CUDA;
-    if (v && cudaMemcpyToSymbol(tl::g_device_error, &zero, sizeof(zero)) != cudaSuccess)
-        return TL_ERR_CUDA;
+    unsigned int v = 0;
+    bool (*const words[])(unsigned int *) = {tl::take_device_error, tl::take_error_attention_ex,
+                                             tl::take_error_attention_bwd, tl::take_error_tree_attention};
+    for (auto take : words) {
+        unsigned int w = 0;
+        if (!take(&w))
+            return TL_ERR_CUDA;
+        v |= w;
+    }
     if (detail)
         *detail = v;
     return v ? TL_ERR_DEVICE_TIMEOUT : TL_OK;

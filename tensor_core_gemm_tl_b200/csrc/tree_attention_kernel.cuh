@@ -1,0 +1,799 @@
+// tree_attention_kernel.cuh -- one or several drafted tokens of each request
+// against its paged key/value cache.
+//
+// Request b has context_b keys in the cache and, behind them, those of its
+// drafted tokens; token t sees every key of the context, itself and the tokens
+// it hangs below (its ancestors in the draft's tree):
+//
+//     O_t = sum_j w_tj V_j,  w_tj = exp(y_tj - lse_t)   over the keys j that t sees
+//
+// with y as in attention_common.cuh; a context key lies at its index, a drafted
+// token at context_b + its depth in the tree.
+//
+// Bound by reading the cache once (4 D bytes a key and key/value head).  All
+// query heads that share a key/value head and all tokens become rows of one
+// 128-row tile (token-major), so the cache is read once for all of them; the
+// products are those of 128 rows whatever the number of rows is, which costs
+// nothing while the reads bound: a 128-key block is 64 KB (D = 128), about
+// 2800 clocks of one SM's share of the HBM, against about 512 for the products.
+//
+// Split over the keys: the blocks of all requests and heads are laid end to
+// end and cut into equal runs, one for each CTA, from the lengths on the device
+// (the host never reads them).  A run that holds all blocks of a tile writes
+// the result; the others leave fp32 sums with their maximum, which
+// tree_combine_kernel joins.  A CTA prefetches across the ends of its pieces.
+//
+// Inside a CTA consecutive blocks alternate between two sets of Tensor Memory
+// columns (scores and sums) and two softmax warpgroups, joined at the end of
+// the piece, so that one block's exponentials overlap the next one's products.
+//
+// Warps: 0 TMA producer, 1 TMEM allocator and MMA issuer, 2..3 the tree's
+// masks and zeros for V rows behind the last key (a page's unused rows may
+// hold anything, and 0 times NaN is NaN), 4..7 and 8..11 softmax.
+#pragma once
+
+#include "attention_common.cuh"
+
+namespace tl {
+
+constexpr int kTreeMaxTokens = 64;
+constexpr int kTreeMaxBatch = 4096;
+
+struct TreeParams {
+    ScoreParams score;
+    int32_t B, H, Hk, group, T;
+    int32_t tile_tokens, row_tiles;   // tokens a 128-row tile holds, tiles a request
+    int32_t units;                    // Hk * row_tiles
+    int32_t page_size, box_rows;      // box_rows: rows a TMA box loads, a divisor of page_size and of 128
+    int32_t capacity;                 // keys a block table row covers
+    int64_t table_row;                // block table's row stride in entries
+    const int32_t *block_table, *context, *parents, *tree_lens;  // parents, tree_lens: may be null
+    uint16_t *O;
+    int64_t o_batch, o_head, o_row;
+    float *lse;                       // [B][H][T], or null
+    float *part_o;                    // [2 CTAs][128][D]
+    float2 *part_ml;                  // [2 CTAs][128]: maximum (log2 units), sum
+    uint64_t timeout_ns;
+};
+
+// A request's lengths: drafted tokens, keys of the context and all keys
+struct TreeRequest {
+    int tokens, context, keys;
+    __device__ __forceinline__ int blocks() const { return tokens > 0 ? (keys + 127) / 128 : 0; }
+};
+
+__device__ __forceinline__ TreeRequest tree_request(const TreeParams &p, int b)
+{
+    TreeRequest r;
+    r.tokens = p.tree_lens ? min(max(p.tree_lens[b], 0), p.T) : p.T;
+    r.context = min(max(p.context[b], 0), p.capacity);
+    r.keys = min(r.context, p.capacity - r.tokens) + r.tokens;
+    r.keys = max(min(r.keys, p.capacity), 0);
+    return r;
+}
+
+// How many CTAs share `work` blocks
+__device__ __forceinline__ int tree_ctas(int grid, int work) { return min(grid, work); }
+
+template <int D_>
+struct TreeConfig {
+    static constexpr int D = D_;
+    static constexpr int BN = 128;
+    static constexpr int KS = D == 128 ? 2 : 4;
+    static constexpr int ATOM_BYTES = 128 * 128;
+    static constexpr int D_ATOMS = D / 64;
+    static constexpr int TILE_BYTES = D_ATOMS * ATOM_BYTES;  // a Q tile, a K block, a V block
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
+    static constexpr int OFF_V = OFF_K + KS * TILE_BYTES;
+    static constexpr int OFF_BAR = OFF_V + KS * TILE_BYTES;
+    static constexpr int BAR_QF = 0, BAR_QE = 2, BAR_KF = 4, BAR_KE = 4 + KS, BAR_VF = 4 + 2 * KS, BAR_VE = 4 + 3 * KS;
+    static constexpr int BAR_SF = 4 + 4 * KS;     // [stream]: scores in Tensor Memory
+    static constexpr int BAR_PF = BAR_SF + 2;     // [stream]: weights in Tensor Memory (4 warps arrive)
+    static constexpr int BAR_DONE = BAR_PF + 2;   // [stream]: O += P V completed
+    static constexpr int BAR_OE = BAR_DONE + 2;   // [piece & 1]: the piece's sums have been read (8 warps)
+    static constexpr int BAR_TF = BAR_OE + 2;     // [piece & 1]: the tree's masks are there (2 warps)
+    static constexpr int BAR_VZ = BAR_TF + 2;     // [V slot]: rows behind the last key are zero (2 warps)
+    static constexpr int BAR_ZR = BAR_VZ + KS;    // a block with rows behind the last key has landed
+    static constexpr int BAR_ML = BAR_ZR + 1;     // both streams of a piece are complete, their statistics in shared memory (8 warps)
+    static constexpr int BAR_DRAIN = BAR_ML + 1;
+    static constexpr int NUM_BARS = BAR_DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int OFF_ML = (OFF_MISC + 16 + 15) / 16 * 16;         // [piece & 1][stream][128] float2
+    static constexpr int OFF_TREE = OFF_ML + 2 * 2 * 128 * 8;             // [piece & 1][64] masks, then depths
+    static constexpr int OFF_PARENT = OFF_TREE + 2 * kTreeMaxTokens * 12;  // [warp][64]
+    static constexpr int OFF_CUM = OFF_PARENT + 2 * kTreeMaxTokens * 4;   // [batch]: blocks of the requests before
+    static constexpr int SMEM_FIXED = OFF_CUM + 1024;                     // + 4 (batch + 1)
+    static constexpr int THREADS = 384;
+    static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 216;
+    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
+    static constexpr int TMEM_S = 0, TMEM_O = 256;
+    static constexpr float RESCALE_LOG2 = 8.0f;
+    static_assert(SMEM_FIXED + 4 * (kTreeMaxBatch + 1) <= 232448, "shared memory");
+};
+
+// A piece: consecutive blocks of one tile (request, key/value head, row tile)
+struct TreePiece {
+    int b, unit, first, len, blocks;  // blocks: the tile's
+};
+
+// The piece of the run [g, g1) that begins at block g of the laid-out work
+__device__ __forceinline__ TreePiece tree_piece(const int32_t *cum, int B, int units, int g, int g1)
+{
+    int lo = 0, hi = B - 1;  // the last request that begins at or before g (empty ones begin where the next does)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] * units <= g)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    TreePiece s;
+    s.b = lo;
+    s.blocks = cum[lo + 1] - cum[lo];
+    const int o = g - cum[lo] * units;
+    s.unit = o / s.blocks;
+    s.first = o - s.unit * s.blocks;
+    s.len = min(s.blocks - s.first, g1 - g);
+    return s;
+}
+
+template <class CF, int DT, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(384, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                          const __grid_constant__ CUtensorMap tmap_v, const TreeParams p)
+{
+    constexpr int D = CF::D, KS = CF::KS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t sQ = smem_addr(smem + CF::OFF_Q);
+    const uint32_t sK = smem_addr(smem + CF::OFF_K);
+    const uint32_t sV = smem_addr(smem + CF::OFF_V);
+    const uint32_t bar0 = smem_addr(smem + CF::OFF_BAR);
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CF::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float2 *ml = reinterpret_cast<float2 *>(smem + CF::OFF_ML);
+    uint64_t *tree_mask = reinterpret_cast<uint64_t *>(smem + CF::OFF_TREE);
+    int32_t *tree_depth = reinterpret_cast<int32_t *>(smem + CF::OFF_TREE + 2 * kTreeMaxTokens * 8);
+    int32_t *parent_smem = reinterpret_cast<int32_t *>(smem + CF::OFF_PARENT);
+    int32_t *cum = reinterpret_cast<int32_t *>(smem + CF::OFF_CUM);
+
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(CF::BAR_QF + i), 1);
+            mbar_init(bar(CF::BAR_QE + i), 1);
+            mbar_init(bar(CF::BAR_SF + i), 1);
+            mbar_init(bar(CF::BAR_PF + i), 4);
+            mbar_init(bar(CF::BAR_DONE + i), 1);
+            mbar_init(bar(CF::BAR_OE + i), 8);
+            mbar_init(bar(CF::BAR_TF + i), 2);
+        }
+        for (int s = 0; s < KS; ++s) {
+            mbar_init(bar(CF::BAR_KF + s), 1);
+            mbar_init(bar(CF::BAR_KE + s), 1);
+            mbar_init(bar(CF::BAR_VF + s), 1);
+            mbar_init(bar(CF::BAR_VE + s), 1);
+            mbar_init(bar(CF::BAR_VZ + s), 2);
+        }
+        mbar_init(bar(CF::BAR_ZR), 1);
+        mbar_init(bar(CF::BAR_ML), 8);
+        mbar_init(bar(CF::BAR_DRAIN), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (threadIdx.x == 64) {
+        tma_prefetch_map(&tmap_q);
+        tma_prefetch_map(&tmap_k);
+        tma_prefetch_map(&tmap_v);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (warp == 0) {
+        // blocks of the requests before each one
+        int before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int x = b < p.B ? tree_request(p, b).blocks() : 0;
+            const int own = x;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off)
+                    x += y;
+            }
+            if (b < p.B)
+                cum[b] = before + x - own;
+            before += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0)
+            cum[p.B] = before;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint64_t timeout = p.timeout_ns;
+    const int work = cum[p.B] * p.units;
+    const int ctas = tree_ctas(static_cast<int>(gridDim.x), work);
+    const int cta = static_cast<int>(blockIdx.x);
+    const int g0 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta) * work / ctas) : 0;
+    const int g1 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta + 1) * work / ctas) : 0;
+
+    uint32_t issued = 0, parity = 0;  // bits: Q buffers 0..1, K slots 8.., V slots 16..
+    if (warp < 4) {
+        regs_decrease<CF::REGS_CONTROL>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer (the whole warp, a box a lane)
+            const int boxes = CF::BN / p.box_rows;
+            const uint32_t q_bytes = static_cast<uint32_t>(CF::D_ATOMS * 128 * p.group * p.tile_tokens);
+            bool ok = true;
+            int st = 0, seg = 0;
+            uint32_t ph = 0;
+            auto mark = [&](int bit, uint32_t par) {
+                issued |= 1u << bit;
+                parity = (parity & ~(1u << bit)) | (par << bit);
+            };
+            auto wait_w = [&](int id, uint32_t par) {
+                return __all_sync(0xffffffffu, wait_bounded(bar(id), par, abort_flag, timeout, ERR_PRODUCER)) != 0;
+            };
+            for (int g = g0; ok && g < g1; ++seg) {
+                const TreePiece s = tree_piece(cum, p.B, p.units, g, g1);
+                const TreeRequest rq = tree_request(p, s.b);
+                const int hk = s.unit / p.row_tiles, rt = s.unit - hk * p.row_tiles;
+                const int32_t *table = p.block_table + s.b * p.table_row;
+                // this lane's box of block j: its page and the row in it
+                auto page_of = [&](int j) {
+                    const int k = j * CF::BN + lane * p.box_rows;
+                    return lane < boxes && k < rq.keys ? table[k / p.page_size] : -1;
+                };
+                int page = page_of(s.first);
+                const int qi = seg & 1;
+                const uint32_t qp = static_cast<uint32_t>(seg >> 1) & 1u;
+                if (!(ok = wait_w(CF::BAR_QE + qi, qp ^ 1u)))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(CF::BAR_QF + qi), q_bytes);
+#pragma unroll
+                    for (int a = 0; a < CF::D_ATOMS; ++a)
+                        tma_load_5d(sQ + qi * CF::TILE_BYTES + a * CF::ATOM_BYTES, &tmap_q, bar(CF::BAR_QF + qi), 64 * a,
+                                    0, hk, rt * p.tile_tokens, s.b);
+                }
+                mark(qi, qp);
+                for (int j = s.first; j < s.first + s.len; ++j) {
+                    const int k = j * CF::BN + lane * p.box_rows;
+                    const bool load = lane < boxes && k < rq.keys;
+                    const int row = k % p.page_size;
+                    const int this_page = page;
+                    page = j + 1 < s.first + s.len ? page_of(j + 1) : -1;
+                    const uint32_t bytes = static_cast<uint32_t>(
+                        __popc(__ballot_sync(0xffffffffu, load)) * p.box_rows * 128 * CF::D_ATOMS);
+                    const uint32_t off = static_cast<uint32_t>(lane * p.box_rows * 128);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int full = (kv ? CF::BAR_VF : CF::BAR_KF) + st;
+                        if (!(ok = wait_w((kv ? CF::BAR_VE : CF::BAR_KE) + st, ph ^ 1u)))
+                            break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(bar(full), bytes);
+                        __syncwarp();
+                        if (load) {
+#pragma unroll
+                            for (int a = 0; a < CF::D_ATOMS; ++a)
+                                tma_load_4d((kv ? sV : sK) + st * CF::TILE_BYTES + a * CF::ATOM_BYTES + off,
+                                            kv ? &tmap_v : &tmap_k, bar(full), 64 * a, row, hk, this_page);
+                        }
+                        mark((kv ? 16 : 8) + st, ph);
+                    }
+                    if (!ok)
+                        break;
+                    if (++st == KS) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                g += s.len;
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0 && g0 < g1) {
+                constexpr uint32_t IDESC_QK = mma_idesc_f16(DT, 128, 128, 0, 0);
+                constexpr uint32_t IDESC_PV = mma_idesc_f16(DT, 128, D, 0, 1);
+                const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024);
+                const uint64_t k_desc = smem_desc_sw128(sK, 16, 1024);
+                const uint64_t v_desc = smem_desc_sw128(sV, CF::ATOM_BYTES, 1024);
+                auto kmaj = [](int k) { return static_cast<uint64_t>(((k >> 2) * CF::ATOM_BYTES + (k & 3) * 32) >> 4); };
+                auto wait = [&](int id, uint32_t par) {
+                    return wait_bounded(bar(id), par, abort_flag, timeout, ERR_MMA_DATA);
+                };
+                const int total = g1 - g0;
+                TreePiece s1 = tree_piece(cum, p.B, p.units, g0, g1), s2 = s1;  // of block n + 1, of block n
+                int seg1 = 0, seg2 = 0, i1 = 0, i2 = 0;                          // their numbers, blocks done in them
+                int keys2 = tree_request(p, s2.b).keys;
+                int st1 = 0, st2 = 0;
+                uint32_t ph1 = 0, ph2 = 0, zeroed = 0;  // zeroed: parity of each V slot's zeroings
+                for (int n = -1; n < total; ++n) {
+                    if (n + 1 < total) {
+                        const int w1 = (n + 1) & 1;
+                        if (i1 == 0 && !wait(CF::BAR_QF + (seg1 & 1), static_cast<uint32_t>(seg1 >> 1) & 1u))
+                            break;
+                        if (!wait(CF::BAR_KF + st1, ph1))
+                            break;
+                        if (n >= 1 && !wait(CF::BAR_DONE + w1, static_cast<uint32_t>((n - 1) >> 1) & 1u))
+                            break;
+                        tc_fence_after_sync();
+                        const uint64_t qd = q_desc + (((seg1 & 1) * CF::TILE_BYTES) >> 4);
+                        const uint64_t kd = k_desc + ((st1 * CF::TILE_BYTES) >> 4);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            tc_mma_f16(tmem_base + CF::TMEM_S + 128 * w1, qd + kmaj(k), kd + kmaj(k), IDESC_QK,
+                                       k != 0 ? 1u : 0u);
+                        tc_commit(bar(CF::BAR_SF + w1));
+                        tc_commit(bar(CF::BAR_KE + st1));
+                        if (++st1 == KS) {
+                            st1 = 0;
+                            ph1 ^= 1u;
+                        }
+                        if (++i1 == s1.len) {
+                            tc_commit(bar(CF::BAR_QE + (seg1 & 1)));
+                            if (n + 2 < total)
+                                s1 = tree_piece(cum, p.B, p.units, g0 + n + 2, g1);
+                            ++seg1;
+                            i1 = 0;
+                        }
+                    }
+                    if (n >= 0) {
+                        const int w = n & 1;
+                        if (!wait(CF::BAR_VF + st2, ph2))
+                            break;
+                        if ((s2.first + i2 + 1) * CF::BN > keys2) {
+                            mbar_arrive(bar(CF::BAR_ZR));
+                            if (!wait(CF::BAR_VZ + st2, (zeroed >> st2) & 1u))
+                                break;
+                            zeroed ^= 1u << st2;
+                        }
+                        // the previous piece's sums have left Tensor Memory
+                        if (i2 == 0 && seg2 > 0 &&
+                            !wait(CF::BAR_OE + ((seg2 - 1) & 1), static_cast<uint32_t>((seg2 - 1) >> 1) & 1u))
+                            break;
+                        if (!wait(CF::BAR_PF + w, static_cast<uint32_t>(n >> 1) & 1u))
+                            break;
+                        tc_fence_after_sync();
+                        const uint64_t vd = v_desc + ((st2 * CF::TILE_BYTES) >> 4);
+#pragma unroll
+                        for (int k = 0; k < CF::BN / 16; ++k)
+                            tc_mma_f16_ts(tmem_base + CF::TMEM_O + D * w, tmem_base + CF::TMEM_S + 128 * w + 8 * k,
+                                          vd + ((2048 * k) >> 4), IDESC_PV, (i2 >= 2 || k > 0) ? 1u : 0u);
+                        tc_commit(bar(CF::BAR_DONE + w));
+                        tc_commit(bar(CF::BAR_VE + st2));
+                        if (++st2 == KS) {
+                            st2 = 0;
+                            ph2 ^= 1u;
+                        }
+                        if (++i2 == s2.len && n + 1 < total) {
+                            s2 = tree_piece(cum, p.B, p.units, g0 + n + 1, g1);
+                            keys2 = tree_request(p, s2.b).keys;
+                            ++seg2;
+                            i2 = 0;
+                        }
+                    }
+                }
+                tc_commit(bar(CF::BAR_DRAIN));
+                wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ the tree's masks; zeros behind the last key
+            const int t = threadIdx.x - 64;  // token
+            bool ok = true;
+            int seg = 0, n = 0;
+            uint32_t tails = 0;
+            for (int g = g0; ok && g < g1; ++seg) {
+                const TreePiece s = tree_piece(cum, p.B, p.units, g, g1);
+                const TreeRequest rq = tree_request(p, s.b);
+                const int buf = seg & 1;
+                if (seg >= 2 && !(ok = __all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_OE + buf),
+                                                                            static_cast<uint32_t>((seg >> 1) - 1) & 1u,
+                                                                            abort_flag, timeout, ERR_EPILOGUE))))
+                    break;
+                // bit u: token t sees drafted token u; only tokens that have a key
+                uint64_t mask = ~0ull >> (63 - t);
+                int depth = t;
+                if (p.parents) {
+                    // each warp keeps its own copy, so neither waits for the other
+                    int32_t *par = parent_smem + (warp - 2) * kTreeMaxTokens;
+                    __syncwarp();
+                    for (int i = lane; i < kTreeMaxTokens; i += 32)
+                        par[i] = i < p.T ? p.parents[static_cast<int64_t>(s.b) * p.T + i] : -1;
+                    __syncwarp();
+                    mask = 1ull << t;
+                    depth = 0;
+                    for (int a = t, up = par[t]; up >= 0 && up < a; up = par[a]) {
+                        a = up;
+                        mask |= 1ull << a;
+                        ++depth;
+                    }
+                }
+                const int live = rq.keys - rq.context;  // drafted tokens with a key
+                if (live < kTreeMaxTokens)
+                    mask &= live > 0 ? (1ull << live) - 1 : 0ull;
+                tree_mask[buf * kTreeMaxTokens + t] = mask;
+                tree_depth[buf * kTreeMaxTokens + t] = depth;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(CF::BAR_TF + buf));
+                // the tile's last block, where the keys end inside it
+                const int end = s.first + s.len;
+                if (end * CF::BN > rq.keys) {
+                    // the MMA warp says when it has landed: it follows every phase of the V slots, this warp does not
+                    const int st = (n + s.len - 1) % KS;
+                    if (!(ok = __all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_ZR), tails & 1u, abort_flag, timeout,
+                                                                    ERR_EPILOGUE))))
+                        break;
+                    ++tails;
+                    const int from = rq.keys - (end - 1) * CF::BN;  // first row behind the keys
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int a = 0; a < CF::D_ATOMS; ++a) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(smem + CF::OFF_V + st * CF::TILE_BYTES + a * CF::ATOM_BYTES);
+                        for (int i = from * 8 + t; i < CF::BN * 8; i += 64)
+                            dst[i] = zero;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(CF::BAR_VZ + st));
+                }
+                n += s.len;
+                g += s.len;
+            }
+            __syncwarp();
+        }
+    } else {
+        regs_increase<CF::REGS_SOFTMAX>();
+        // ------------------------------------------------------------ softmax of every other block, output of a piece
+        const int w = (warp - 4) >> 2;
+        const int r = (warp & 3) * 32 + lane;
+        const int r_token = r / p.group, r_head = r - r_token * p.group;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + 128 * w);
+        const uint32_t o_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + D * w);
+        auto wait_warp = [&](int id, uint32_t par) -> bool {
+            return __all_sync(0xffffffffu, wait_bounded(bar(id), par, abort_flag, timeout, ERR_EPILOGUE));
+        };
+        bool ok = true;
+        int seg = 0, n0 = 0;
+        for (int g = g0; ok && g < g1; ++seg) {
+            const TreePiece s = tree_piece(cum, p.B, p.units, g, g1);
+            const TreeRequest rq = tree_request(p, s.b);
+            const int hk = s.unit / p.row_tiles, rt = s.unit - hk * p.row_tiles;
+            const int tok = rt * p.tile_tokens + r_token;
+            const bool valid = r_token < p.tile_tokens && tok < rq.tokens;
+            const bool active = __any_sync(0xffffffffu, valid);  // warps without a row only keep the barriers going
+            const int head = hk * p.group + r_head;
+            const int buf = seg & 1;
+            if (!(ok = wait_warp(CF::BAR_TF + buf, static_cast<uint32_t>(seg >> 1) & 1u)))
+                break;
+            const uint64_t mask = valid ? tree_mask[buf * kTreeMaxTokens + tok] : 0ull;
+            float slope2 = 0.0f;
+            int pos = 0;
+            if constexpr (BIAS) {
+                if (valid) {
+                    slope2 = __ldg(p.score.slopes + head) * 1.4426950408889634f;
+                    pos = rq.context + tree_depth[buf * kTreeMaxTokens + tok];
+                }
+            }
+            float m = -INFINITY, l = 0.0f;
+            const int i_first = (w - n0) & 1;  // first block of the piece that is this stream's
+            for (int i = i_first; ok && i < s.len; i += 2) {
+                const int n = n0 + i;
+                if (!(ok = wait_warp(CF::BAR_SF + w, static_cast<uint32_t>(n >> 1) & 1u)))
+                    break;
+                tc_fence_after_sync();
+                if (active) {
+                    const int key0 = (s.first + i) * CF::BN;
+                    uint32_t sv[128];
+                    tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                    tmem_load_32cols(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
+                    tmem_load_32cols(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
+                    tmem_load_wait();
+                    const bool context_only = key0 + CF::BN <= rq.context;
+                    if constexpr (CAP || BIAS) {
+                        const float dist0 = static_cast<float>(pos - key0);
+#pragma unroll
+                        for (int e = 0; e < 128; e += 2) {
+                            float2 x = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                            if constexpr (CAP) {
+                                const float2 c = cap_reciprocals(x, p.score.cap_arg);
+                                x = ffma2(c, splat2(-2.0f * p.score.cap_log2), splat2(p.score.cap_log2));
+                            } else {
+                                x = fmul2(x, splat2(p.score.scale_log2));
+                            }
+                            if constexpr (BIAS) {
+                                float2 dist = make_float2(dist0 - static_cast<float>(e), dist0 - static_cast<float>(e + 1));
+                                if (!context_only) {
+                                    // a drafted key lies at the context's end plus its depth
+                                    const int a = key0 + e - rq.context;
+                                    const int32_t *dep = tree_depth + buf * kTreeMaxTokens;
+                                    if (a >= 0)
+                                        dist.x = static_cast<float>(pos - rq.context - dep[min(a, kTreeMaxTokens - 1)]);
+                                    if (a + 1 >= 0)
+                                        dist.y = static_cast<float>(pos - rq.context - dep[min(a + 1, kTreeMaxTokens - 1)]);
+                                }
+                                x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
+                            }
+                            sv[e] = __float_as_uint(x.x);
+                            sv[e + 1] = __float_as_uint(x.y);
+                        }
+                    }
+                    if (!context_only) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int a = key0 + 32 * q - rq.context;  // the word's first key among the drafted
+                            uint32_t see;
+                            if (a <= -32)
+                                see = 0xFFFFFFFFu;
+                            else if (a < 0)
+                                see = (static_cast<uint32_t>(mask) << -a) | ((1u << -a) - 1u);
+                            else
+                                see = a < 64 ? static_cast<uint32_t>(mask >> a) : 0u;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e)))
+                                    sv[32 * q + e] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    float t[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float *f = reinterpret_cast<const float *>(&sv[8 * q]);
+                        t[q] = fmax3(fmax3(f[0], f[1], f[2]), fmax3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        t[q] = fmaxf(t[q], t[q + 8]);
+                    float mx = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
+                    if constexpr (!CAP && !BIAS)
+                        mx *= p.score.scale_log2;
+                    const bool resc = mx > m + CF::RESCALE_LOG2;
+                    const float m_new = resc ? mx : m;
+                    const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
+                    const float alpha = resc ? exp2_approx_ftz(m - m_ref) : 1.0f;
+                    const float2 negm2 = splat2(-m_ref);
+                    float2 part[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e2 = 0; e2 < 32; ++e2) {
+                            const int e = 64 * q + 2 * e2;
+                            const float2 v = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                            const float2 x = CAP || BIAS ? fadd2(v, negm2) : ffma2(v, splat2(p.score.scale_log2), negm2);
+                            const float2 e2v = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
+                            part[e2 & 3] = fadd2(part[e2 & 3], e2v);
+                            pk[e2] = pack2<DT>(e2v.x, e2v.y);
+                        }
+                        tmem_store_32cols(s_addr + 32 * q, pk);
+                    }
+                    const float2 ps = fadd2(fadd2(part[0], part[1]), fadd2(part[2], part[3]));
+                    l = l * alpha + (ps.x + ps.y);
+                    m = m_new;
+                    // S(n) was issued after this stream's last P V had completed, so O is whole here
+                    if (i > i_first && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_load_32cols(o_addr + 32 * c, o);
+                            tmem_load_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_store_32cols(o_addr + 32 * c, o);
+                        }
+                    }
+                    tmem_store_wait();
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(CF::BAR_PF + w));
+            }
+            if (!ok)
+                break;
+            // the two streams' sums of the piece, joined: this warpgroup takes half the columns
+            float2 *mls = ml + buf * 2 * 128;
+            mls[w * 128 + r] = make_float2(m, l);
+            const int n1 = n0 + s.len;
+            // this stream's last P V (the ones before it have completed, S(n) being issued behind them), then the other's
+            if (i_first < s.len)
+                ok = wait_warp(CF::BAR_DONE + w, static_cast<uint32_t>((n1 - w + 1) / 2 - 1) & 1u);
+            if (!ok)
+                break;
+            tc_fence_after_sync();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(CF::BAR_ML));
+            if (!(ok = wait_warp(CF::BAR_ML, static_cast<uint32_t>(seg) & 1u)))
+                break;
+            tc_fence_after_sync();
+            const bool whole = s.len == s.blocks;
+            if (active) {
+                const float2 a = mls[r], c = mls[128 + r];
+                const float M = fmaxf(a.x, c.x);
+                const float f0 = a.x == -INFINITY ? 0.0f : exp2_approx_ftz(a.x - M);
+                const float f1 = c.x == -INFINITY ? 0.0f : exp2_approx_ftz(c.x - M);
+                const float L = a.y * f0 + c.y * f1;
+                const bool use0 = ((0 - n0) & 1) < s.len, use1 = ((1 - n0) & 1) < s.len;
+                const float inv = whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
+                const int slot = 2 * cta + (s.first == 0 ? 1 : 0);
+                uint16_t *orow = p.O + s.b * p.o_batch + head * p.o_head + static_cast<int64_t>(tok) * p.o_row;
+                float *prow = p.part_o + (static_cast<int64_t>(slot) * 128 + r) * D;
+#pragma unroll 1
+                for (int c0 = w * (D / 2); c0 < (w + 1) * (D / 2); c0 += 32) {
+                    uint32_t o0[32], o1[32];
+                    if (use0)
+                        tmem_load_32cols(tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + c0), o0);
+                    if (use1)
+                        tmem_load_32cols(tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + D + c0), o1);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float v = 0.0f;
+                        if (use0)
+                            v = __uint_as_float(o0[e]) * f0;
+                        if (use1)
+                            v = fmaf(__uint_as_float(o1[e]), f1, v);
+                        o0[e] = __float_as_uint(v * inv);
+                    }
+                    if (valid) {
+                        if (whole) {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                uint4 x;
+                                x.x = pack2<DT>(__uint_as_float(o0[8 * v]), __uint_as_float(o0[8 * v + 1]));
+                                x.y = pack2<DT>(__uint_as_float(o0[8 * v + 2]), __uint_as_float(o0[8 * v + 3]));
+                                x.z = pack2<DT>(__uint_as_float(o0[8 * v + 4]), __uint_as_float(o0[8 * v + 5]));
+                                x.w = pack2<DT>(__uint_as_float(o0[8 * v + 6]), __uint_as_float(o0[8 * v + 7]));
+                                reinterpret_cast<uint4 *>(orow + c0)[v] = x;
+                            }
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < 8; ++v)
+                                reinterpret_cast<uint4 *>(prow + c0)[v] =
+                                    make_uint4(o0[4 * v], o0[4 * v + 1], o0[4 * v + 2], o0[4 * v + 3]);
+                        }
+                    }
+                }
+                if (valid && w == 0) {
+                    if (!whole)
+                        p.part_ml[static_cast<int64_t>(slot) * 128 + r] = make_float2(M, L);
+                    else if (p.lse)
+                        p.lse[(static_cast<int64_t>(s.b) * p.H + head) * p.T + tok] =
+                            L == 0.0f ? -INFINITY : M * 0.69314718055994531f + logf(L);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(CF::BAR_OE + buf));
+            n0 = n1;
+            g += s.len;
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        for (int i = 0; i < 2; ++i)
+            if (issued & (1u << i))
+                wait_drain(bar(CF::BAR_QF + i), (parity >> i) & 1u, timeout);
+        for (int s = 0; s < KS; ++s) {
+            if (issued & (1u << (8 + s)))
+                wait_drain(bar(CF::BAR_KF + s), (parity >> (8 + s)) & 1u, timeout);
+            if (issued & (1u << (16 + s)))
+                wait_drain(bar(CF::BAR_VF + s), (parity >> (16 + s)) & 1u, timeout);
+        }
+    }
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 1)
+        tmem_dealloc(tmem_base, 512);
+}
+
+// Joins the pieces of each tile whose blocks fell to several CTAs: one CTA (4
+// warps) a tile, a warp a row.  The pieces are added in the order of the keys.
+template <int DT, int D>
+__global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p, int grid)
+{
+    constexpr int V = D / 32;  // values a lane
+    __shared__ int sums[2];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int unit = static_cast<int>(blockIdx.x % p.units), b = static_cast<int>(blockIdx.x / p.units);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < 2)
+        sums[threadIdx.x] = 0;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = threadIdx.x; i < p.B; i += 128) {
+        const int x = tree_request(p, i).blocks();
+        all += x;
+        before += i < b ? x : 0;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) {
+        atomicAdd(&sums[0], before);
+        atomicAdd(&sums[1], all);
+    }
+    __syncthreads();
+    const TreeRequest rq = tree_request(p, b);
+    const int blocks = rq.blocks();
+    if (blocks == 0)
+        return;
+    const int64_t work = static_cast<int64_t>(sums[1]) * p.units;
+    const int64_t first = static_cast<int64_t>(sums[0]) * p.units + static_cast<int64_t>(unit) * blocks;
+    const int ctas = tree_ctas(grid, static_cast<int>(work));
+    // the CTA whose run [c work / ctas, (c + 1) work / ctas) holds block g
+    auto owner = [&](int64_t g) { return static_cast<int>(((g + 1) * ctas - 1) / work); };
+    const int c0 = owner(first), c1 = owner(first + blocks - 1);
+    if (c0 == c1)
+        return;
+    const int hk = unit / p.row_tiles, rt = unit - hk * p.row_tiles;
+    const int rows = min(p.tile_tokens, rq.tokens - rt * p.tile_tokens) * p.group;
+    for (int r = warp; r < rows; r += 4) {
+        auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * 128 + r; };
+        float M = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32)
+            M = fmaxf(M, p.part_ml[slot(c)].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        float L = 0.0f, acc[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            acc[v] = 0.0f;
+        for (int c = c0; c <= c1; ++c) {
+            const float2 x = p.part_ml[slot(c)];
+            const float f = x.x == -INFINITY ? 0.0f : exp2_approx_ftz(x.x - M);
+            L = fmaf(x.y, f, L);
+            const float *o = p.part_o + slot(c) * D + lane * V;
+            if constexpr (V == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(o);
+                acc[0] = fmaf(w.x, f, acc[0]);
+                acc[1] = fmaf(w.y, f, acc[1]);
+                acc[2] = fmaf(w.z, f, acc[2]);
+                acc[3] = fmaf(w.w, f, acc[3]);
+            } else {
+                const float2 w = *reinterpret_cast<const float2 *>(o);
+                acc[0] = fmaf(w.x, f, acc[0]);
+                acc[1] = fmaf(w.y, f, acc[1]);
+            }
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int tok = rt * p.tile_tokens + r / p.group, head = hk * p.group + r % p.group;
+        uint16_t *orow = p.O + b * p.o_batch + head * p.o_head + static_cast<int64_t>(tok) * p.o_row + lane * V;
+        if constexpr (V == 4)
+            *reinterpret_cast<uint2 *>(orow) =
+                make_uint2(pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(orow) = pack2<DT>(acc[0] * inv, acc[1] * inv);
+        if (p.lse && lane == 0)
+            p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + tok] =
+                L == 0.0f ? -INFINITY : M * 0.69314718055994531f + logf(L);
+    }
+}
+
+} // namespace tl
