@@ -424,14 +424,14 @@ __global__ void __launch_bounds__(384, 1)
         };
         // fp16: P times 2^p_shift, dX times x_mul over P's factor; x_undo takes dX's factor out again
         constexpr float p_shift = DT == 0 ? 10.0f : 0.0f;
-        float x_mul = 1.0f, x_undo = CAP ? 4.0f : 1.0f;  // capped: 1 - tanh^2 = 4 r (1 - r), the 4 left for the end
+        float x_mul = 1.0f, x_undo = CAP ? 4.0f : 1.0f;  // capped: 1 - tanh^2 = 4 r (1 - r), bf16 leaves the 4 for the end
         if constexpr (DT == 0) {
             const unsigned bits = __ldg(p.amax);
             // 2^-e with 2^(e-1) <= largest |dO| < 2^e, kept where both 2^e and 2^-e are normal; 1 for 0, inf, NaN
             int e = static_cast<int>(bits >> 23) - 126;
             e = bits == 0 || bits >= 0x7F800000u ? 0 : min(max(e, -100), 100);
-            x_mul = exp2f(static_cast<float>(-e) + 4.0f - p_shift);
-            x_undo *= exp2f(static_cast<float>(e) - 4.0f);
+            x_mul = exp2f(static_cast<float>(-e) + 4.0f - p_shift) * x_undo;  // the capped 4 goes in here
+            x_undo = exp2f(static_cast<float>(e) - 4.0f);
         }
         float row_lse = INFINITY, row_delta = 0.0f;
         float2 eps[2] = {splat2(0.0f), splat2(0.0f)};  // dQ: this warpgroup's part of e (times P's factor)

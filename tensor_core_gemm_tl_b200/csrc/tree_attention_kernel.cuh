@@ -509,6 +509,27 @@ __global__ void __launch_bounds__(384, 1)
                     tmem_load_32cols(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
                     tmem_load_wait();
                     const bool context_only = key0 + CF::BN <= rq.context;
+                    // put `value` in the place of the keys the row does not see
+                    auto hide = [&](float value) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int a = key0 + 32 * q - rq.context;  // the word's first key among the drafted
+                            uint32_t see;
+                            if (a <= -32)
+                                see = 0xFFFFFFFFu;
+                            else if (a < 0)
+                                see = (static_cast<uint32_t>(mask) << -a) | ((1u << -a) - 1u);
+                            else
+                                see = a < 64 ? static_cast<uint32_t>(mask >> a) : 0u;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e)))
+                                    sv[32 * q + e] = __float_as_uint(value);
+                        }
+                    };
+                    // a page's unused rows may hold anything, and the cap's shared reciprocal takes two keys at once
+                    if (CAP && !context_only)
+                        hide(0.0f);
                     if constexpr (CAP || BIAS) {
                         const float dist0 = static_cast<float>(pos - key0);
 #pragma unroll
@@ -537,23 +558,8 @@ __global__ void __launch_bounds__(384, 1)
                             sv[e + 1] = __float_as_uint(x.y);
                         }
                     }
-                    if (!context_only) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int a = key0 + 32 * q - rq.context;  // the word's first key among the drafted
-                            uint32_t see;
-                            if (a <= -32)
-                                see = 0xFFFFFFFFu;
-                            else if (a < 0)
-                                see = (static_cast<uint32_t>(mask) << -a) | ((1u << -a) - 1u);
-                            else
-                                see = a < 64 ? static_cast<uint32_t>(mask >> a) : 0u;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see & (1u << e)))
-                                    sv[32 * q + e] = __float_as_uint(-INFINITY);
-                        }
-                    }
+                    if (!context_only)
+                        hide(-INFINITY);
                     float t[16];
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
