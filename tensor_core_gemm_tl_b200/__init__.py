@@ -13,7 +13,7 @@ or library fallback.
 from __future__ import annotations
 
 from ._binding import (  # noqa: F401
-    LIB_PATH, AttentionOptions, Options, Plan, RotaryOptions, Status, TLError, TreeOptions, TL_BF16, TL_EPI_BIAS, TL_EPI_BIAS_GELU, TL_EPI_GELU,
+    ATTENTION_OPTIONS, LIB_PATH, ROTARY_OPTIONS, TREE_OPTIONS, AttentionOptions, Options, Plan, RotaryOptions, Status, TLError, TreeOptions, TL_BF16, TL_EPI_BIAS, TL_EPI_BIAS_GELU, TL_EPI_GELU,
     TL_EPI_NONE, TL_EPI_BIAS_GELU_TANH, TL_EPI_GELU_TANH, TL_EPI_WITH_BIAS, TL_F16,
     SIGNATURES, tl_attention_bwd, tl_attention_ex, tl_attention_fwd, tl_rotary, tl_tree_attention, tl_check_device, tl_config_name, tl_gemm, tl_gemm_ex, tl_gemm_noalloc,
     tl_gemm_plan, tl_num_configs, tl_softmax_rows, tl_vector_add,
@@ -159,78 +159,109 @@ def attention(q, k, v, causal: bool = False, scale: float = 0.0, out=None, lse=N
     return out
 
 
-def _require_rows(name, t, device, dtype, shape):
-    """Raise ValueError unless `t` is a CUDA tensor on `device` of `dtype` and
-    `shape` whose rows the kernels can address: contiguous last dimension,
-    positive strides in multiples of 8 elements, a 16-byte aligned base."""
-    if not t.is_cuda or t.device != device:
+# The calls below run as often as a model has layers and tokens, so their checks
+# are written to cost little: each tensor's strides are read once, the option
+# structs are packed in one go, the device is only switched when it has to be.
+
+def _rows(name, t, device, dtype, shape):
+    """The strides of (outer, middle, row) of a 4-D CUDA tensor, for the C ABI;
+    ValueError unless it lies on `device`, has `dtype` and `shape`, a contiguous
+    last dimension, positive strides in multiples of 8 elements and a 16-byte
+    aligned base."""
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
-    if st[-1] != 1 or any(n > 1 and (s <= 0 or s % 8) for n, s in zip(t.shape[:-1], st[:-1])):
-        raise ValueError(f"{name} must have a contiguous last dimension and positive strides in multiples of 8 "
-                         f"elements, got strides {tuple(st)}")
-    if t.data_ptr() % 16:
+    s0, s1, s2, s3 = st
+    if s3 != 1 or s0 <= 0 or s1 <= 0 or s2 <= 0 or (s0 | s1 | s2) & 7:
+        # a dimension of one element takes any stride
+        n = t.shape
+        s0, s1, s2 = (s if n[i] > 1 else n[3] for i, s in enumerate((s0, s1, s2)))
+        if s3 != 1 or s0 <= 0 or s1 <= 0 or s2 <= 0 or (s0 | s1 | s2) & 7:
+            raise ValueError(f"{name} must have a contiguous last dimension and positive strides in multiples of 8 "
+                             f"elements, got strides {tuple(st)}")
+    if t.data_ptr() & 15:
         raise ValueError(f"{name} must be 16-byte aligned")
+    return s0, s1, s2
 
 
-def _strides3(t, order=(0, 1, 2)):
-    """Strides of a 4-D tensor's outer dimensions for the C ABI (any positive
-    value for a dimension of one element)."""
-    return tuple(max(t.stride(i), 1) if t.shape[i] > 1 else t.shape[-1] for i in order)
-
-
-def _require_ints(name, t, device, shape):
-    _require_device_tensor(name, t, device, shape=shape)
-    import torch
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name} must be int32, got {t.dtype}")
+def _flat(name, t, device, dtype, shape):
+    """ValueError unless `t` is a contiguous CUDA tensor on `device` of `dtype` and `shape`."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _score_arguments(scale, score_cap, slopes, heads, device):
-    """The softmax scale, cap and bias slopes, checked."""
-    import torch
-    if not (scale >= 0.0 and scale != float("inf")) or not (score_cap >= 0.0 and score_cap != float("inf")):
+    """The softmax scale, cap and bias slopes, checked; returns the slopes' pointer."""
+    if not 0.0 <= scale < float("inf") or not 0.0 <= score_cap < float("inf"):
         raise ValueError("scale and score_cap must be finite and not negative")
-    if slopes is not None:
-        _require_device_tensor("slopes", slopes, device, torch.float32, (heads,))
-        if getattr(slopes, "requires_grad", False):
-            raise ValueError("slopes are constants: they get no gradient")
+    if slopes is None:
+        return 0
+    import torch
+    _flat("slopes", slopes, device, torch.float32, (heads,))
+    if slopes.requires_grad:
+        raise ValueError("slopes are constants: they get no gradient")
+    return slopes.data_ptr()
+
+
+def _launch(device, stream, call, what):
+    """Runs call(raw stream) with `device` current, on `stream` or torch's current one; raises TLError."""
+    import torch
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        st = call(raw)
+    else:
+        with torch.cuda.device(device):
+            st = call(raw)
+    if st != 0:
+        raise TLError(st, what)
 
 
 def _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset):
-    """Checks what attention_ex and attention_backward share; returns the options."""
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3] \
-            or k.shape[1] < 1 or q.shape[1] % k.shape[1]:
+    """Checks what attention_ex and attention_backward share; returns the leading
+    option fields, the strides of q, k and v, and the dtype code."""
+    import torch
+    dims = q.dim()
+    if dims != 4 or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError(f"shapes q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)} do not match")
+    B, H, _, D = q.shape
+    Bk, Hk, _, Dk = k.shape
+    if B != Bk or D != Dk or Hk < 1 or H % Hk:
         raise ValueError(f"shapes q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)} do not match")
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    _dtype_code(q)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _require_rows(name, t, q.device, q.dtype, t.shape)
-    B, H = q.shape[:2]
-    _score_arguments(scale, score_cap, slopes, H, q.device)
-    docs = 0
+    dt = _dtype_code(q)
+    dev, dtype = q.device, q.dtype
+    strides = _rows("q", q, dev, dtype, q.shape) + _rows("k", k, dev, dtype, k.shape) + \
+        _rows("v", v, dev, dtype, v.shape)
+    slopes_ptr = _score_arguments(scale, score_cap, slopes, H, dev)
+    docs = docs_ptr = prefix_ptr = 0
     if doc_offsets is not None:
         if doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
             raise ValueError(f"doc_offsets must be (batch, documents + 1), got {tuple(doc_offsets.shape)}")
         docs = doc_offsets.shape[1] - 1
-        _require_ints("doc_offsets", doc_offsets, q.device, (B, docs + 1))
+        _flat("doc_offsets", doc_offsets, dev, torch.int32, (B, docs + 1))
+        docs_ptr = doc_offsets.data_ptr()
     if prefix is not None:
         if not causal:
             raise ValueError("a prefix needs causal=True (without it every key is seen already)")
-        _require_ints("prefix", prefix, q.device, (B, max(docs, 1)))
+        _flat("prefix", prefix, dev, torch.int32, (B, max(docs, 1)))
+        prefix_ptr = prefix.data_ptr()
     if q_offset < 0:
         raise ValueError("q_offset must not be negative")
-    return AttentionOptions(causal=int(bool(causal)), softmax_scale=scale, score_cap=score_cap,
-                            slopes=slopes.data_ptr() if slopes is not None else None,
-                            doc_offsets=doc_offsets.data_ptr() if docs else None, num_docs=docs,
-                            prefix_lens=prefix.data_ptr() if prefix is not None else None, q_offset=q_offset,
-                            kv_heads=k.shape[1], q_strides=_strides3(q), k_strides=_strides3(k),
-                            v_strides=_strides3(v))
+    return (1 if causal else 0, scale, score_cap, 0, slopes_ptr, docs_ptr, docs, prefix_ptr, q_offset, Hk), strides, dt
+
+
+_DENSE = (0, 0, 0)
 
 
 def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap: float = 0.0, slopes=None,
@@ -250,21 +281,19 @@ def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap
     -inf.  Returns out, shaped and by default laid out like q; fills ``lse``
     (B, H, Sq) float32 if given (attention_backward needs it)."""
     import torch
-    opt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
+    head, strides, dt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
     B, H, Sq, D = q.shape
+    dev = q.device
+    lse_ptr = 0
     if lse is not None:
-        _require_device_tensor("lse", lse, q.device, torch.float32, (B, H, Sq))
+        _flat("lse", lse, dev, torch.float32, (B, H, Sq))
+        lse_ptr = lse.data_ptr()
     if out is None:
         out = torch.empty_like(q)
-    _require_rows("out", out, q.device, q.dtype, q.shape)
-    opt.o_strides = _strides3(out)
-    s = stream if stream is not None else torch.cuda.current_stream(q.device)
-    with torch.cuda.device(q.device):
-        st = tl_attention_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                             lse.data_ptr() if lse is not None else 0, B, H, Sq, k.shape[2], D, _dtype_code(q),
-                             s.cuda_stream, opt)
-    if st != 0:
-        raise TLError(st, "tl_attention_ex")
+    so = _rows("out", out, dev, q.dtype, q.shape)
+    opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *_DENSE, *_DENSE, *_DENSE, *_DENSE)
+    _launch(dev, stream, lambda s: tl_attention_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_ptr, B,
+                                                   H, Sq, k.shape[2], D, dt, s, opt), "tl_attention_ex")
     return out
 
 
@@ -276,30 +305,30 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: 
     dk and dv are summed over the heads that share them.  Results repeat bit
     for bit."""
     import torch
-    opt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
+    head, strides, dt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
     B, H, Sq, D = q.shape
-    _require_rows("dout", dout, q.device, q.dtype, q.shape)
-    _require_rows("out", out, q.device, q.dtype, q.shape)
-    _require_device_tensor("lse", lse, q.device, torch.float32, (B, H, Sq))
+    dev, dtype = q.device, q.dtype
+    sdo = _rows("dout", dout, dev, dtype, q.shape)
+    so = _rows("out", out, dev, dtype, q.shape)
+    _flat("lse", lse, dev, torch.float32, (B, H, Sq))
     # every given tensor is checked before anything is allocated
+    grads = []
     for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        if g is not None:
-            _require_rows(name, g, q.device, q.dtype, like.shape)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    for name, g in (("dq", dq), ("dk", dk), ("dv", dv)):
-        _require_rows(name, g, q.device, q.dtype, g.shape)
-    opt.o_strides, opt.do_strides = _strides3(out), _strides3(dout)
-    opt.dq_strides, opt.dk_strides, opt.dv_strides = _strides3(dq), _strides3(dk), _strides3(dv)
-    s = stream if stream is not None else torch.cuda.current_stream(q.device)
-    with torch.cuda.device(q.device):
-        st = tl_attention_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                              lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Sq, k.shape[2], D,
-                              _dtype_code(q), s.cuda_stream, opt)
-    if st != 0:
-        raise TLError(st, "tl_attention_bwd")
+        grads.append((g, None if g is None else _rows(name, g, dev, dtype, like.shape), name, like))
+    grads = [(g, sg) if g is not None else _new_rows(name, like) for g, sg, name, like in grads]
+    (dq, sdq), (dk, sdk), (dv, sdv) = grads
+    opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *sdo, *sdq, *sdk, *sdv)
+    _launch(dev, stream, lambda s: tl_attention_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                                    out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                                    dv.data_ptr(), B, H, Sq, k.shape[2], D, dt, s, opt),
+            "tl_attention_bwd")
     return dq, dk, dv
+
+
+def _new_rows(name, like):
+    import torch
+    g = torch.empty_like(like)
+    return g, _rows(name, g, like.device, like.dtype, like.shape)
 
 
 def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None, *, tree_lens=None,
@@ -317,46 +346,59 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
     attention_ex, a new token standing at context_lens[b] plus its depth.
     Returns out, like q; fills ``lse`` (B, H, T) float32 if given."""
     import torch
-    if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != q.shape[3] \
-            or k_cache.shape[2] < 1 or q.shape[1] % k_cache.shape[2]:
+    if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError(f"shapes q{tuple(q.shape)} k_cache{tuple(k_cache.shape)} v_cache{tuple(v_cache.shape)} "
                          "do not match")
+    B, H, T, D = q.shape
+    pages, page_size, Hk, Dk = k_cache.shape
+    if D != Dk or Hk < 1 or H % Hk:
+        raise ValueError(f"shapes q{tuple(q.shape)} k_cache{tuple(k_cache.shape)} do not match")
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
     dt = _dtype_code(q)
-    B, H, T, D = q.shape
-    pages, page_size, Hk, _ = k_cache.shape
-    _require_rows("q", q, q.device, q.dtype, q.shape)
-    _require_rows("k_cache", k_cache, q.device, q.dtype, k_cache.shape)
-    _require_rows("v_cache", v_cache, q.device, q.dtype, v_cache.shape)
+    dev, dtype, i32 = q.device, q.dtype, torch.int32
+    sq = _rows("q", q, dev, dtype, q.shape)
+    sk = _rows("k_cache", k_cache, dev, dtype, k_cache.shape)
+    sv = _rows("v_cache", v_cache, dev, dtype, v_cache.shape)
     if block_table.dim() != 2 or block_table.shape[1] < 1:
         raise ValueError(f"block_table must be (batch, pages), got {tuple(block_table.shape)}")
     max_pages = block_table.shape[1]
-    _require_ints("block_table", block_table, q.device, (B, max_pages))
-    _require_ints("context_lens", context_lens, q.device, (B,))
+    _flat("block_table", block_table, dev, i32, (B, max_pages))
+    _flat("context_lens", context_lens, dev, i32, (B,))
+    parents_ptr = lens_ptr = lse_ptr = 0
     if parents is not None:
-        _require_ints("parents", parents, q.device, (B, T))
+        _flat("parents", parents, dev, i32, (B, T))
+        parents_ptr = parents.data_ptr()
     if tree_lens is not None:
-        _require_ints("tree_lens", tree_lens, q.device, (B,))
-    _score_arguments(scale, score_cap, slopes, H, q.device)
+        _flat("tree_lens", tree_lens, dev, i32, (B,))
+        lens_ptr = tree_lens.data_ptr()
+    slopes_ptr = _score_arguments(scale, score_cap, slopes, H, dev)
     if lse is not None:
-        _require_device_tensor("lse", lse, q.device, torch.float32, (B, H, T))
+        _flat("lse", lse, dev, torch.float32, (B, H, T))
+        lse_ptr = lse.data_ptr()
     if out is None:
         out = torch.empty_like(q)
-    _require_rows("out", out, q.device, q.dtype, q.shape)
-    opt = TreeOptions(softmax_scale=scale, score_cap=score_cap,
-                      slopes=slopes.data_ptr() if slopes is not None else None, q_strides=_strides3(q),
-                      o_strides=_strides3(out), k_strides=_strides3(k_cache), v_strides=_strides3(v_cache))
-    s = stream if stream is not None else torch.cuda.current_stream(q.device)
-    with torch.cuda.device(q.device):
-        st = tl_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                               context_lens.data_ptr(), parents.data_ptr() if parents is not None else 0,
-                               tree_lens.data_ptr() if tree_lens is not None else 0, out.data_ptr(),
-                               lse.data_ptr() if lse is not None else 0, B, H, Hk, T, pages, page_size, max_pages, D,
-                               dt, s.cuda_stream, opt)
-    if st != 0:
-        raise TLError(st, "tl_tree_attention")
+    so = _rows("out", out, dev, dtype, q.shape)
+    opt = TREE_OPTIONS.pack(scale, score_cap, slopes_ptr, 0, *sq, *so, *sk, *sv)
+    _launch(dev, stream, lambda s: tl_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                                     block_table.data_ptr(), context_lens.data_ptr(), parents_ptr,
+                                                     lens_ptr, out.data_ptr(), lse_ptr, B, H, Hk, T, pages, page_size,
+                                                     max_pages, D, dt, s, opt), "tl_tree_attention")
     return out
+
+
+def _rotary_rows(name, t, device, dtype, shape):
+    """The strides of a 4-D tensor for rotary, any positive ones with a contiguous last dimension."""
+    if t.device != device or not t.is_cuda or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    s0, s1, s2, s3 = t.stride()
+    if s0 <= 0 or s1 <= 0 or s2 <= 0:  # a dimension of one element takes any stride
+        n = t.shape
+        s0, s1, s2 = (s if n[i] > 1 else n[3] for i, s in enumerate((s0, s1, s2)))
+    if s3 != 1 or s0 <= 0 or s1 <= 0 or s2 <= 0:
+        raise ValueError(f"{name} must have a contiguous last dimension and positive strides")
+    return s0, s1, s2
 
 
 def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
@@ -376,49 +418,46 @@ def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float
         raise ValueError("q must be a 4-D CUDA tensor")
     dt = _dtype_code(q)
     B, H, S, D = q.shape
-
-    def rows(name, t, shape):
-        if not t.is_cuda or t.device != q.device or t.dtype != q.dtype or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be a {q.dtype} CUDA tensor of shape {tuple(shape)} on {q.device}")
-        if t.stride(-1) != 1 or any(n > 1 and st <= 0 for n, st in zip(t.shape[:-1], t.stride()[:-1])):
-            raise ValueError(f"{name} must have a contiguous last dimension and positive strides")
-
-    rows("q", q, q.shape)
+    dev, dtype = q.device, q.dtype
+    sq, sk, sok, Hk = _rotary_rows("q", q, dev, dtype, q.shape), _DENSE, _DENSE, 0
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k must be 4-D")
-        rows("k", k, (B, k.shape[1], S, D))
+        Hk = k.shape[1]
+        sk = _rotary_rows("k", k, dev, dtype, (B, Hk, S, D))
     elif out_k is not None:
         raise ValueError("out_k without k")
     shared = positions.dim() == 1
     if positions.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
-    _require_device_tensor("positions", positions, q.device, shape=(S,) if shared else (B, S))
+    _flat("positions", positions, dev, positions.dtype, (S,) if shared else (B, S))
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be 1-D")
-    _require_device_tensor("inv_freq", inv_freq, q.device, torch.float32)
-    if not 2 <= 2 * inv_freq.shape[0] <= D:
-        raise ValueError(f"inv_freq has {inv_freq.shape[0]} frequencies for heads of {D} values")
-    if not (scale > 0.0 and scale != float("inf")):
+    half = inv_freq.shape[0]
+    _flat("inv_freq", inv_freq, dev, torch.float32, (half,))
+    if not 2 <= 2 * half <= D:
+        raise ValueError(f"inv_freq has {half} frequencies for heads of {D} values")
+    if not 0.0 < scale < float("inf"):
         raise ValueError("scale must be positive and finite")
-    for name, o, t in (("out_q", out_q, q), ("out_k", out_k, k)):
-        if o is not None:
-            rows(name, o, t.shape)
-    out_q = torch.empty_like(q) if out_q is None else out_q
-    if k is not None and out_k is None:
-        out_k = torch.empty_like(k)
-    opt = RotaryOptions(interleaved=int(bool(interleaved)), inverse=int(bool(inverse)), scale=scale,
-                        positions_int64=int(positions.dtype == torch.int64), positions_shared=int(shared),
-                        q_strides=_strides3(q), qout_strides=_strides3(out_q))
+    soq = sq
+    # every given tensor is checked before anything is allocated
+    if out_q is not None:
+        soq = _rotary_rows("out_q", out_q, dev, dtype, q.shape)
+    if out_k is not None:
+        sok = _rotary_rows("out_k", out_k, dev, dtype, k.shape)
+    if out_q is None:
+        out_q = torch.empty_like(q)
+        soq = _rotary_rows("out_q", out_q, dev, dtype, q.shape)
+    k_ptr = ok_ptr = 0
     if k is not None:
-        opt.k_strides, opt.kout_strides = _strides3(k), _strides3(out_k)
-    s = stream if stream is not None else torch.cuda.current_stream(q.device)
-    with torch.cuda.device(q.device):
-        st = tl_rotary(q.data_ptr(), k.data_ptr() if k is not None else 0, out_q.data_ptr(),
-                       out_k.data_ptr() if k is not None else 0, positions.data_ptr(), inv_freq.data_ptr(), B, H,
-                       k.shape[1] if k is not None else 0, S, D, 2 * inv_freq.shape[0], dt, s.cuda_stream, opt)
-    if st != 0:
-        raise TLError(st, "tl_rotary")
+        if out_k is None:
+            out_k = torch.empty_like(k)
+            sok = _rotary_rows("out_k", out_k, dev, dtype, k.shape)
+        k_ptr, ok_ptr = k.data_ptr(), out_k.data_ptr()
+    opt = ROTARY_OPTIONS.pack(1 if interleaved else 0, 1 if inverse else 0, scale, positions.dtype == torch.int64, shared,
+                              0, *sq, *sk, *soq, *sok)
+    _launch(dev, stream, lambda s: tl_rotary(q.data_ptr(), k_ptr, out_q.data_ptr(), ok_ptr, positions.data_ptr(),
+                                             inv_freq.data_ptr(), B, H, Hk, S, D, 2 * half, dt, s, opt), "tl_rotary")
     return out_q, out_k
 
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import enum
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtlgemm.so")
@@ -96,6 +97,12 @@ class RotaryOptions(ctypes.Structure):
                 ("qout_strides", _I64x3), ("kout_strides", _I64x3)]
 
 
+# The same structs as packed bytes: one call fills all fields, several times
+# faster than setting a Structure's arrays.
+ATTENTION_OPTIONS = struct.Struct("=iffiQQqQqq24q")
+TREE_OPTIONS = struct.Struct("=ffQq12q")
+ROTARY_OPTIONS = struct.Struct("=iifiii12q")
+
 # name -> (restype, argtypes); every symbol include/tl_gemm.h declares
 _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 SIGNATURES = {
@@ -108,10 +115,10 @@ SIGNATURES = {
     "tl_vector_add": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
     "tl_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, ctypes.c_int, _I32,
                                         ctypes.c_float, _P]),
-    "tl_attention_ex": (ctypes.c_int, [_P] * 5 + [_I64] * 5 + [ctypes.c_int, _P, ctypes.POINTER(AttentionOptions)]),
-    "tl_attention_bwd": (ctypes.c_int, [_P] * 9 + [_I64] * 5 + [ctypes.c_int, _P, ctypes.POINTER(AttentionOptions)]),
-    "tl_tree_attention": (ctypes.c_int, [_P] * 9 + [_I64] * 8 + [ctypes.c_int, _P, ctypes.POINTER(TreeOptions)]),
-    "tl_rotary": (ctypes.c_int, [_P] * 6 + [_I64] * 6 + [ctypes.c_int, _P, ctypes.POINTER(RotaryOptions)]),
+    "tl_attention_ex": (ctypes.c_int, [_P] * 5 + [_I64] * 5 + [ctypes.c_int, _P, _P]),
+    "tl_attention_bwd": (ctypes.c_int, [_P] * 9 + [_I64] * 5 + [ctypes.c_int, _P, _P]),
+    "tl_tree_attention": (ctypes.c_int, [_P] * 9 + [_I64] * 8 + [ctypes.c_int, _P, _P]),
+    "tl_rotary": (ctypes.c_int, [_P] * 6 + [_I64] * 6 + [ctypes.c_int, _P, _P]),
     "tl_gemm_plan": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _I32,
                                     ctypes.POINTER(Options), ctypes.POINTER(Plan)]),
     "tl_num_configs": (_I32, []),
@@ -133,6 +140,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 _lib = load()
+
+
+def _options(o):
+    """An options argument: a Structure, packed bytes, or None."""
+    return ctypes.byref(o) if isinstance(o, ctypes.Structure) else o
 
 
 def _check(st: int, what: str) -> None:
@@ -166,35 +178,35 @@ def tl_attention_fwd(Q, K, V, O, lse, batch, heads, seq_q, seq_k, head_dim, dtyp
 
 
 def tl_attention_ex(Q, K, V, O, lse, batch, heads, seq_q, seq_k, head_dim, dtype, stream=0,
-                    options: AttentionOptions | None = None) -> int:
+                    options: AttentionOptions | bytes | None = None) -> int:
     """Attention forward with masks, caps, bias and shared heads on device pointers; returns the tl_status code."""
     return _lib.tl_attention_ex(Q, K, V, O, lse or None, batch, heads, seq_q, seq_k, head_dim, dtype, stream or None,
-                                ctypes.byref(options) if options is not None else None)
+                                _options(options))
 
 
 def tl_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, batch, heads, seq_q, seq_k, head_dim, dtype, stream=0,
-                     options: AttentionOptions | None = None) -> int:
+                     options: AttentionOptions | bytes | None = None) -> int:
     """The gradients of tl_attention_ex on device pointers; returns the tl_status code."""
     return _lib.tl_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, batch, heads, seq_q, seq_k, head_dim, dtype,
-                                 stream or None, ctypes.byref(options) if options is not None else None)
+                                 stream or None, _options(options))
 
 
 def tl_tree_attention(Q, K_cache, V_cache, block_table, context_lens, parents, tree_lens, O, lse, batch, heads,
                       kv_heads, tokens, num_pages, page_size, max_pages, head_dim, dtype, stream=0,
-                      options: TreeOptions | None = None) -> int:
+                      options: TreeOptions | bytes | None = None) -> int:
     """New tokens against a paged cache, on device pointers; returns the tl_status code."""
     return _lib.tl_tree_attention(Q, K_cache, V_cache, block_table, context_lens, parents or None, tree_lens or None,
                                   O, lse or None, batch, heads, kv_heads, tokens, num_pages, page_size, max_pages,
                                   head_dim, dtype, stream or None,
-                                  ctypes.byref(options) if options is not None else None)
+                                  _options(options))
 
 
 def tl_rotary(Q, K, Q_out, K_out, positions, inv_freq, batch, heads, kv_heads, seq, head_dim, rot_dim, dtype,
-              stream=0, options: RotaryOptions | None = None) -> int:
+              stream=0, options: RotaryOptions | bytes | None = None) -> int:
     """Rotary positions of q and k on device pointers; returns the tl_status code."""
     return _lib.tl_rotary(Q, K or None, Q_out, K_out or None, positions, inv_freq, batch, heads, kv_heads, seq,
                           head_dim, rot_dim, dtype, stream or None,
-                          ctypes.byref(options) if options is not None else None)
+                          _options(options))
 
 
 def tl_softmax_rows(X, Y, rows, cols, dtype, stream=0) -> int:

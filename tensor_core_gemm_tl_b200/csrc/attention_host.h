@@ -96,12 +96,15 @@ tl_status launch_overlapped(void (*fn)(P...), int64_t grid, int threads, int sme
 template <class Fn>
 tl_status ready_kernel(DeviceState *d, Fn fn, int smem, int launch_regs)
 {
+    const void *f = reinterpret_cast<const void *>(fn);
+    if (smem_limit_raised(d, f))  // done before, the registers included
+        return TL_OK;
     cudaFuncAttributes fa{};
     if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess)
         return TL_ERR_CUDA;
     if (fa.numRegs < launch_regs)
         return TL_ERR_UNSUPPORTED;
-    return raise_smem_limit(d, reinterpret_cast<const void *>(fn), smem);
+    return raise_smem_limit(d, f, smem);
 }
 
 inline bool score_values_ok(float scale, float cap)

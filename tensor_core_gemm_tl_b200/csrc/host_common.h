@@ -44,6 +44,9 @@ tl_status ensure_pool(DeviceState *d);
 // Raise a kernel's dynamic shared-memory limit once per device
 tl_status raise_smem_limit(DeviceState *d, const void *fn, int bytes);
 
+// Whether raise_smem_limit has been through for the kernel on this device
+bool smem_limit_raised(DeviceState *d, const void *fn);
+
 // Read and clear the error word of the kernels of one translation unit (each
 // has its own; defined there); false when a CUDA call failed
 bool take_error_attention_ex(unsigned int *word);

@@ -80,6 +80,12 @@ tl_status ensure_pool(DeviceState *d)
     return TL_OK;
 }
 
+bool smem_limit_raised(DeviceState *d, const void *fn)
+{
+    std::lock_guard<std::mutex> lk(g_mu);
+    return d->smem_set.find(fn) != d->smem_set.end();
+}
+
 tl_status raise_smem_limit(DeviceState *d, const void *fn, int bytes)
 {
     std::lock_guard<std::mutex> lk(g_mu);

@@ -273,6 +273,16 @@ def test_structs_match_the_header():
     assert ctypes.sizeof(tg.AttentionOptions) == 16 + 6 * 8 + 8 * 24
     assert ctypes.sizeof(tg.TreeOptions) == 8 + 2 * 8 + 4 * 24
     assert ctypes.sizeof(tg.RotaryOptions) == 24 + 4 * 24
+    for packed, cls in ((tg.ATTENTION_OPTIONS, tg.AttentionOptions), (tg.TREE_OPTIONS, tg.TreeOptions),
+                        (tg.ROTARY_OPTIONS, tg.RotaryOptions)):
+        n = sum(3 if name.endswith("strides") else 1 for name, _ in cls._fields_)
+        given = [i + 1 for i in range(n)]
+        o = cls.from_buffer_copy(packed.pack(*given))
+        flat = []
+        for name, _ in cls._fields_:
+            v = getattr(o, name)
+            flat += list(v) if name.endswith("strides") else [v]
+        assert packed.size == ctypes.sizeof(cls) and flat == given
     header = open(os.path.join(os.path.dirname(__file__), "..", "include", "tl_gemm.h")).read()
     header = re.sub(r"/\*.*?\*/", "", header, flags=re.S)
     for struct, cls in (("tl_attention_options", tg.AttentionOptions), ("tl_tree_options", tg.TreeOptions),
