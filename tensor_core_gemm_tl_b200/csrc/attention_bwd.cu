@@ -92,7 +92,7 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
 
     const int64_t nqb = ceil_div(seq_q, kBwdCols);
     const int64_t rows_bytes = round256(batch * heads * nqb * 2 * kBwdCols * 4);
-    const int64_t interval_bytes = round256(batch * nqb * 2 * kBwdCols * 4);
+    const int64_t interval_bytes = round256(batch * nqb * 3 * kBwdCols * 4);
     const int64_t range_bytes = round256(batch * nqb * 16);
     if ((st = ensure_pool(d)) != TL_OK)
         return st;

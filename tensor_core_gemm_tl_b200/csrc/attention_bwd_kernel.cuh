@@ -40,11 +40,15 @@
 // are powers of two and leave with the fp32 sums.
 #pragma once
 
+#include <type_traits>
+
 #include "attention_common.cuh"
 
 namespace tl {
 
 constexpr int kBwdCols = 64;  // queries (DKV) or keys a step takes
+template <int DT>
+constexpr float kPShift = DT == 0 ? 10.0f : 0.0f;  // fp16 holds P times 2^10
 
 struct AttnBwdParams {
     MaskParams mask;
@@ -53,8 +57,9 @@ struct AttnBwdParams {
     int32_t nqb;               // blocks of 64 queries
     int32_t tiles;             // 128-row tiles a CTA each: of the keys (DKV) or of the queries
     float scale;               // softmax scale
-    float *rows;               // [B][H][nqb][2][64]: lse in log2 units (+inf where the row sees nothing), delta
-    const int32_t *intervals;  // [B][nqb][2][64]: first and end key of each query
+    float *rows;               // [B][H][nqb][2][64]: -lse in log2 units (-inf where the row sees nothing) plus the
+                               // exponent of P's factor, -delta
+    const int32_t *intervals;  // [B][nqb][3][64]: first and end key of each query; 0.0f where it sees one key, else 1.0f
     const int4 *ranges;        // [B][nqb]: least first, largest end, largest first, least end of the block's queries
     const unsigned *amax;      // fp16: bits of the largest |dO|, else null
     uint16_t *out0, *out1;     // dK, dV (DKV) or dQ, null
@@ -101,9 +106,10 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
         __syncthreads();
         if (threadIdx.x < kBwdCols) {
             const int2 seen = visible_keys(p.mask, docs, b, qb * kBwdCols + threadIdx.x);
-            int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + qb) * 2 * kBwdCols;
+            int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + qb) * 3 * kBwdCols;
             iv[threadIdx.x] = seen.x;
             iv[kBwdCols + threadIdx.x] = seen.y;
+            iv[2 * kBwdCols + threadIdx.x] = __float_as_int(seen.y - seen.x == 1 ? 0.0f : 1.0f);
             if (seen.y > seen.x) {
                 atomicMin(&red[0], seen.x);
                 atomicMax(&red[1], seen.y);
@@ -146,8 +152,8 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
         if (sub == 0) {
             const float l = i < p.mask.Sq ? p.lse[static_cast<int64_t>(bh) * p.mask.Sq + i] : -INFINITY;
             float *rows = p.rows + (static_cast<int64_t>(bh) * p.nqb + qb) * 2 * kBwdCols;
-            rows[r] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-            rows[kBwdCols + r] = l == -INFINITY ? 0.0f : sum;
+            rows[r] = l == -INFINITY ? -INFINITY : kPShift<DT> - l * 1.4426950408889634f;
+            rows[kBwdCols + r] = l == -INFINITY ? 0.0f : -sum;
         }
     }
     if constexpr (DT == 0) {
@@ -166,9 +172,9 @@ struct AttnBwdConfig {
     static constexpr int D_ATOMS = D / 64;
     static constexpr int XATOM = 128 * 128, YATOM = BN * 128;  // bytes of 64 columns of a tile
     static constexpr int X_BYTES = D_ATOMS * XATOM, Y_BYTES = D_ATOMS * YATOM;
-    static constexpr int INFO_BYTES = 2 * 2 * BN * 4;  // rows' lse and delta, intervals
+    static constexpr int ROWS_BYTES = 2 * BN * 4, INTERVAL_BYTES = 3 * BN * 4;  // of a block of queries
     static constexpr int STAGES = 4;
-    static constexpr int STAGE_BYTES = 2 * Y_BYTES + 1024;  // Y1, Y2, info
+    static constexpr int STAGE_BYTES = 2 * Y_BYTES + 2048;  // Y1, Y2, rows, intervals
     static constexpr int OFF_X = 0;
     static constexpr int OFF_Y = 2 * X_BYTES;
     static constexpr int OFF_BAR = OFF_Y + STAGES * STAGE_BYTES;
@@ -187,7 +193,7 @@ struct AttnBwdConfig {
     static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
     // Tensor Memory columns: S and dP of buffer w, the accumulators
     static constexpr int TMEM_S = 0, TMEM_DP = 128, TMEM_A0 = 256, TMEM_A1 = 256 + D;
-    static_assert(INFO_BYTES <= 1024 && SMEM_BYTES <= 232448, "shared memory");
+    static_assert(ROWS_BYTES + INTERVAL_BYTES <= 2048 && SMEM_BYTES <= 232448, "shared memory");
 };
 
 // X1, X2: the CTA's 128 rows (K and V, or Q and dO); Y1, Y2: the blocks of 64
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(384, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);  // uniform for the compiler too
     const int lane = threadIdx.x & 31;
     // the tile and its head.  Causal: the heaviest tiles first (the first keys,
     // the last queries); else one head's tiles together.
@@ -279,7 +285,7 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp >= 4) {
         const int i = x0 + r;
         if (i < p.mask.Sq) {
-            const int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + i / CF::BN) * 2 * CF::BN + i % CF::BN;
+            const int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + i / CF::BN) * 3 * CF::BN + i % CF::BN;
             seen = make_int2(iv[0], iv[CF::BN]);
         }
         const int lo = __reduce_min_sync(0xffffffffu, seen.y > seen.x ? seen.x / CF::BN : 0x7FFFFFFF);
@@ -316,17 +322,17 @@ __global__ void __launch_bounds__(384, 1)
                         break;
                     const uint32_t full = bar(CF::BAR_YF + st);
                     const uint32_t dst = sY + st * CF::STAGE_BYTES;
-                    mbar_arrive_expect_tx(full, 2 * CF::Y_BYTES + (DKV ? CF::INFO_BYTES : 0));
+                    mbar_arrive_expect_tx(full, 2 * CF::Y_BYTES + (DKV ? CF::ROWS_BYTES + CF::INTERVAL_BYTES : 0));
 #pragma unroll
                     for (int a = 0; a < CF::D_ATOMS; ++a)
                         tma_load_4d(dst + a * CF::YATOM, &map_y1, full, 64 * a, yb * CF::BN, yh, b);
                     if constexpr (DKV) {
                         bulk_load_g2s(dst + 2 * CF::Y_BYTES,
                                       p.rows + ((static_cast<int64_t>(b) * p.H + yh) * p.nqb + yb) * 2 * CF::BN,
-                                      CF::INFO_BYTES / 2, full);
-                        bulk_load_g2s(dst + 2 * CF::Y_BYTES + CF::INFO_BYTES / 2,
-                                      p.intervals + (static_cast<int64_t>(b) * p.nqb + yb) * 2 * CF::BN,
-                                      CF::INFO_BYTES / 2, full);
+                                      CF::ROWS_BYTES, full);
+                        bulk_load_g2s(dst + 2 * CF::Y_BYTES + CF::ROWS_BYTES,
+                                      p.intervals + (static_cast<int64_t>(b) * p.nqb + yb) * 3 * CF::BN,
+                                      CF::INTERVAL_BYTES, full);
                     }
 #pragma unroll
                     for (int a = 0; a < CF::D_ATOMS; ++a)
@@ -346,7 +352,9 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
-            if (lane == 0 && n_total > 0) {
+            // the whole warp walks the loop and one elected lane issues: what the
+            // instructions are made from stays uniform across the warp
+            if (n_total > 0) {
                 constexpr uint32_t IDESC_1 = mma_idesc_f16(DT, 128, CF::BN, 0, 0);  // both K-major
                 constexpr uint32_t IDESC_2 = mma_idesc_f16(DT, 128, D, 0, 1);       // A from Tensor Memory, Y N-major
                 const uint64_t x_desc = smem_desc_sw128(sX, 16, 1024);
@@ -381,33 +389,40 @@ __global__ void __launch_bounds__(384, 1)
                 };
                 int st = 0, st1 = 0;  // stages of block n and of block n + 1
                 uint32_t ph1 = 0;
-                bool ok = wait_bounded(bar(CF::BAR_X), 0, abort_flag, timeout, ERR_MMA_DATA);
+                auto wait = [&](int id, uint32_t par, unsigned code) {
+                    return __all_sync(0xffffffffu, wait_bounded(bar(id), par, abort_flag, timeout, code)) != 0;
+                };
+                bool ok = wait(CF::BAR_X, 0, ERR_MMA_DATA);
                 for (int n = -1; ok && n < n_total; ++n) {
                     if (n + 1 < n_total) {
                         const int w1 = (n + 1) & 1;
                         // the buffer's previous P and dX (block n - 1) have been read
-                        if (!wait_bounded(bar(CF::BAR_YF + st1), ph1, abort_flag, timeout, ERR_MMA_DATA) ||
-                            (n >= 1 && !wait_bounded(bar(CF::BAR_DONE + w1), static_cast<uint32_t>((n - 1) >> 1) & 1u,
-                                                     abort_flag, timeout, ERR_MMA_ACC)))
+                        if (!wait(CF::BAR_YF + st1, ph1, ERR_MMA_DATA) ||
+                            (n >= 1 && !wait(CF::BAR_DONE + w1, static_cast<uint32_t>((n - 1) >> 1) & 1u, ERR_MMA_ACC)))
                             break;
                         tc_fence_after_sync();
-                        first_products(w1, st1);
+                        if (elect_one())
+                            first_products(w1, st1);
+                        __syncwarp();
                         if (++st1 == STAGES) {
                             st1 = 0;
                             ph1 ^= 1u;
                         }
                     }
                     if (n >= 0) {
-                        if (!wait_bounded(bar(CF::BAR_PF + (n & 1)), static_cast<uint32_t>(n >> 1) & 1u, abort_flag,
-                                          timeout, ERR_MMA_ACC))
+                        if (!wait(CF::BAR_PF + (n & 1), static_cast<uint32_t>(n >> 1) & 1u, ERR_MMA_ACC))
                             break;
                         tc_fence_after_sync();
-                        second_products(n & 1, st, n == 0);
+                        if (elect_one())
+                            second_products(n & 1, st, n == 0);
+                        __syncwarp();
                         if (++st == STAGES)
                             st = 0;
                     }
                 }
-                tc_commit(bar(CF::BAR_DRAIN));
+                if (elect_one())
+                    tc_commit(bar(CF::BAR_DRAIN));
+                __syncwarp();
                 wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
             }
             __syncwarp();
@@ -423,7 +438,7 @@ __global__ void __launch_bounds__(384, 1)
             return __all_sync(0xffffffffu, w);
         };
         // fp16: P times 2^p_shift, dX times x_mul over P's factor; x_undo takes dX's factor out again
-        constexpr float p_shift = DT == 0 ? 10.0f : 0.0f;
+        constexpr float p_shift = kPShift<DT>;
         float x_mul = 1.0f, x_undo = CAP ? 4.0f : 1.0f;  // capped: 1 - tanh^2 = 4 r (1 - r), bf16 leaves the 4 for the end
         if constexpr (DT == 0) {
             const unsigned bits = __ldg(p.amax);
@@ -433,15 +448,15 @@ __global__ void __launch_bounds__(384, 1)
             x_mul = exp2f(static_cast<float>(-e) + 4.0f - p_shift) * x_undo;  // the capped 4 goes in here
             x_undo = exp2f(static_cast<float>(e) - 4.0f);
         }
-        float row_lse = INFINITY, row_delta = 0.0f;
+        float row_nlse = -INFINITY, row_ndelta = 0.0f;
         float2 eps[2] = {splat2(0.0f), splat2(0.0f)};  // dQ: this warpgroup's part of e (times P's factor)
         if constexpr (!DKV) {
             const int i = x0 + r;
             if (i < p.mask.Sq) {
                 const float *rows = p.rows + ((static_cast<int64_t>(b) * p.H + head) * p.nqb + i / CF::BN) * 2 * CF::BN +
                                     i % CF::BN;
-                row_lse = rows[0] - p_shift;
-                row_delta = rows[CF::BN];
+                row_nlse = rows[0];
+                row_ndelta = rows[CF::BN];
             }
         }
         bool ok = true;
@@ -476,8 +491,10 @@ __global__ void __launch_bounds__(384, 1)
             tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
             tmem_load_32cols(dp_addr, *reinterpret_cast<uint32_t(*)[32]>(&dp[0]));
             tmem_load_32cols(dp_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&dp[32]));
+            // DKV: -lse, -delta, first key, end key and "sees more than one key" of the block's queries
             const float4 *info = reinterpret_cast<const float4 *>(smem + CF::OFF_Y + st * CF::STAGE_BYTES + 2 * CF::Y_BYTES);
-            const int *iv = reinterpret_cast<const int *>(info + 2 * CF::BN / 4);
+            const int4 *iv = reinterpret_cast<const int4 *>(info + 2 * CF::BN / 4);
+            const float4 *many = info + 4 * CF::BN / 4;
             // |p_i - j|: the column's step away from the first column's distance
             const float dist0 = DKV ? static_cast<float>(p.mask.q_offset + yb * CF::BN - (x0 + r))
                                     : static_cast<float>(p.mask.q_offset + x0 + r - yb * CF::BN);
@@ -486,72 +503,78 @@ __global__ void __launch_bounds__(384, 1)
             bool whole = DKV ? rg.z <= x0 && rg.w >= x0 + CF::BM : nlo <= 0 && nhi >= CF::BN;
             whole = __all_sync(0xffffffffu, whole);
             tmem_load_wait();
+            // scores and dP to P and dX, in place and packed in pairs; only blocks that cut an interval are masked
+            auto block = [&](auto masked) {
+                constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
-            for (int e = 0; e < CF::BN; e += 4) {
-                float4 l4, d4;
-                if constexpr (DKV) {
-                    l4 = info[e / 4];
-                    d4 = info[CF::BN / 4 + e / 4];
-                    if constexpr (DT == 0) {
-                        l4.x -= p_shift;
-                        l4.y -= p_shift;
-                        l4.z -= p_shift;
-                        l4.w -= p_shift;
-                    }
-                } else {
-                    l4 = make_float4(row_lse, row_lse, row_lse, row_lse);
-                    d4 = make_float4(row_delta, row_delta, row_delta, row_delta);
-                }
-#pragma unroll
-                for (int c = 0; c < 4; c += 2) {
-                    const float2 s = make_float2(__uint_as_float(sv[e + c]), __uint_as_float(sv[e + c + 1]));
-                    const float2 nl = c ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y);
-                    const float2 nd = c ? make_float2(-d4.z, -d4.w) : make_float2(-d4.x, -d4.y);
-                    float2 x, cap_r;
-                    if constexpr (CAP) {
-                        cap_r = cap_reciprocals(s, p.score.cap_arg);
-                        x = fadd2(ffma2(cap_r, splat2(-2.0f * p.score.cap_log2), splat2(p.score.cap_log2)), nl);
-                    } else {
-                        x = ffma2(s, splat2(p.score.scale_log2), nl);
-                    }
-                    if constexpr (BIAS) {
-                        const float f = static_cast<float>(e + c);
-                        const float2 dist = DKV ? make_float2(dist0 + f, dist0 + f + 1.0f)
-                                                : make_float2(dist0 - f, dist0 - f - 1.0f);
-                        x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
-                    }
-                    float2 w = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
-                    if (!whole) {
-                        if constexpr (DKV) {
-                            w.x = key >= iv[e + c] && key < iv[CF::BN + e + c] ? w.x : 0.0f;
-                            w.y = key >= iv[e + c + 1] && key < iv[CF::BN + e + c + 1] ? w.y : 0.0f;
-                        } else {
-                            w.x = e + c >= nlo && e + c < nhi ? w.x : 0.0f;
-                            w.y = e + c + 1 >= nlo && e + c + 1 < nhi ? w.y : 0.0f;
-                        }
-                    }
-                    const float2 g = fadd2(make_float2(__uint_as_float(dp[e + c]), __uint_as_float(dp[e + c + 1])), nd);
-                    float2 ds = fmul2(w, g);
-                    if constexpr (!DKV)
-                        eps[c / 2] = fadd2(eps[c / 2], ds);
-                    if constexpr (CAP) {
-                        const float2 t = ffma2(make_float2(-cap_r.x, -cap_r.y), cap_r, cap_r);
-                        ds = fmul2(ds, t);
-                        if constexpr (!DKV)
-                            w = fmul2(w, t);
-                    }
-                    if constexpr (DT == 0)
-                        ds = fmul2(ds, splat2(x_mul));
+                for (int e = 0; e < CF::BN; e += 4) {
+                    float4 l4 = make_float4(row_nlse, row_nlse, row_nlse, row_nlse);
+                    float4 d4 = make_float4(row_ndelta, row_ndelta, row_ndelta, row_ndelta);
+                    float4 m4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                    int4 lo4 = make_int4(0, 0, 0, 0), hi4 = lo4;
                     if constexpr (DKV) {
-                        if (!whole) {  // a query that sees one key
-                            ds.x = iv[CF::BN + e + c] - iv[e + c] == 1 ? 0.0f : ds.x;
-                            ds.y = iv[CF::BN + e + c + 1] - iv[e + c + 1] == 1 ? 0.0f : ds.y;
+                        l4 = info[e / 4];
+                        d4 = info[CF::BN / 4 + e / 4];
+                        if constexpr (MASKED) {
+                            lo4 = iv[e / 4];
+                            hi4 = iv[CF::BN / 4 + e / 4];
+                            m4 = many[e / 4];
                         }
                     }
-                    sv[(e + c) / 2] = pack2<DT>(w.x, w.y);
-                    dp[(e + c) / 2] = pack2<DT>(ds.x, ds.y);
+#pragma unroll
+                    for (int c = 0; c < 4; c += 2) {
+                        const float2 s = make_float2(__uint_as_float(sv[e + c]), __uint_as_float(sv[e + c + 1]));
+                        const float2 nl = c ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+                        const float2 nd = c ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
+                        float2 x, cap_r;
+                        if constexpr (CAP) {
+                            cap_r = cap_reciprocals(s, p.score.cap_arg);
+                            x = ffma2(cap_r, splat2(-2.0f * p.score.cap_log2), fadd2(nl, splat2(p.score.cap_log2)));
+                        } else {
+                            x = ffma2(s, splat2(p.score.scale_log2), nl);
+                        }
+                        if constexpr (BIAS) {
+                            const float f = static_cast<float>(e + c);
+                            const float2 dist = DKV ? fadd2(splat2(dist0), make_float2(f, f + 1.0f))
+                                                    : fadd2(splat2(dist0), make_float2(-f, -f - 1.0f));
+                            x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
+                        }
+                        float2 w = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
+                        const float2 dpv = make_float2(__uint_as_float(dp[e + c]), __uint_as_float(dp[e + c + 1]));
+                        float2 g;
+                        if constexpr (MASKED && DKV) {
+                            w.x = key >= (c ? lo4.z : lo4.x) && key < (c ? hi4.z : hi4.x) ? w.x : 0.0f;
+                            w.y = key >= (c ? lo4.w : lo4.y) && key < (c ? hi4.w : hi4.y) ? w.y : 0.0f;
+                            // a query that sees one key gets dX = 0 exactly
+                            const float2 m = c ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y);
+                            g = fmul2(fadd2(dpv, nd), m);
+                        } else {
+                            if constexpr (MASKED) {
+                                w.x = e + c >= nlo && e + c < nhi ? w.x : 0.0f;
+                                w.y = e + c + 1 >= nlo && e + c + 1 < nhi ? w.y : 0.0f;
+                            }
+                            g = fadd2(dpv, nd);
+                        }
+                        float2 ds = fmul2(w, g);
+                        if constexpr (!DKV)
+                            eps[c / 2] = fadd2(eps[c / 2], ds);
+                        if constexpr (CAP) {
+                            const float2 t = ffma2(make_float2(-cap_r.x, -cap_r.y), cap_r, cap_r);
+                            ds = fmul2(ds, t);
+                            if constexpr (!DKV)
+                                w = fmul2(w, t);
+                        }
+                        if constexpr (DT == 0)
+                            ds = fmul2(ds, splat2(x_mul));
+                        sv[(e + c) / 2] = pack2<DT>(w.x, w.y);
+                        dp[(e + c) / 2] = pack2<DT>(ds.x, ds.y);
+                    }
                 }
-            }
+            };
+            if (whole)
+                block(std::false_type{});
+            else
+                block(std::true_type{});
             tmem_store_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
             tmem_store_32cols(dp_addr, *reinterpret_cast<uint32_t(*)[32]>(&dp[0]));
             tmem_store_wait();
@@ -595,7 +618,7 @@ __global__ void __launch_bounds__(384, 1)
             if constexpr (!DKV) {
                 if (wg == 0 && live)
                     p.rows[((static_cast<int64_t>(b) * p.H + head) * p.nqb + row / CF::BN) * 2 * CF::BN + CF::BN +
-                           row % CF::BN] = row_delta + e_row;
+                           row % CF::BN] = row_ndelta - e_row;
             }
             const int c0 = DKV ? 0 : wg * (D / 64), c1 = DKV ? D / 32 : (wg + 1) * (D / 64);
 #pragma unroll 1

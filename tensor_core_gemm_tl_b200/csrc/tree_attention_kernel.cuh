@@ -718,8 +718,8 @@ __global__ void __launch_bounds__(384, 1)
         tmem_dealloc(tmem_base, 512);
 }
 
-// Joins the pieces of each tile whose blocks fell to several CTAs: one CTA (4
-// warps) a tile, a warp a row.  The pieces are added in the order of the keys.
+// Joins the pieces of each tile whose blocks fell to several CTAs: a warp a
+// row.  The pieces are added in the order of the keys.
 template <int DT, int D>
 __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p, int grid)
 {
@@ -727,7 +727,9 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p, i
     __shared__ int sums[2];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int unit = static_cast<int>(blockIdx.x % p.units), b = static_cast<int>(blockIdx.x / p.units);
+    const int row_blocks = (p.tile_tokens * p.group + 3) / 4;
+    const int rb = static_cast<int>(blockIdx.x % row_blocks), bu = static_cast<int>(blockIdx.x / row_blocks);
+    const int unit = bu % p.units, b = bu / p.units;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x < 2)
         sums[threadIdx.x] = 0;
@@ -759,7 +761,8 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p, i
         return;
     const int hk = unit / p.row_tiles, rt = unit - hk * p.row_tiles;
     const int rows = min(p.tile_tokens, rq.tokens - rt * p.tile_tokens) * p.group;
-    for (int r = warp; r < rows; r += 4) {
+    const int r = 4 * rb + warp;
+    if (r < rows) {
         auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * 128 + r; };
         float M = -INFINITY;
         for (int c = c0 + lane; c <= c1; c += 32)
@@ -771,6 +774,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p, i
 #pragma unroll
         for (int v = 0; v < V; ++v)
             acc[v] = 0.0f;
+#pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
             const float2 x = p.part_ml[slot(c)];
             const float f = x.x == -INFINITY ? 0.0f : exp2_approx_ftz(x.x - M);
