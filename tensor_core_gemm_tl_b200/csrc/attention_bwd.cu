@@ -12,7 +12,7 @@ using RowsFn = void (*)(AttnBwdRowsParams);
 struct BwdEntry {
     BwdFn fn[2][2][2][2];  // [dtype][dK and dV][capped][biased]
     RowsFn rows[2];        // [dtype]
-    int smem, launch_regs;
+    int smem, threads, launch_regs;
 };
 
 template <class CF, int DT>
@@ -37,6 +37,7 @@ BwdEntry make_bwd()
     fill_bwd<CF, 0>(e);
     fill_bwd<CF, 1>(e);
     e.smem = CF::SMEM_BYTES;
+    e.threads = CF::THREADS;
     e.launch_regs = CF::LAUNCH_REGS;
     return e;
 }
@@ -147,10 +148,10 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     if (st == TL_OK)
         st = launch_overlapped(e.rows[dtype], nqb * batch * heads, 256, 0, stream, rp);
     if (st == TL_OK)
-        st = launch_overlapped(dq, pq.tiles * batch * heads, 384, e.smem, stream, q_tile, do_tile, k_block, v_block,
+        st = launch_overlapped(dq, pq.tiles * batch * heads, e.threads, e.smem, stream, q_tile, do_tile, k_block, v_block,
                                pq);
     if (st == TL_OK)
-        st = launch_overlapped(dkv, pk.tiles * batch * c.kv_heads, 384, e.smem, stream, k_tile, v_tile, q_block,
+        st = launch_overlapped(dkv, pk.tiles * batch * c.kv_heads, e.threads, e.smem, stream, k_tile, v_tile, q_block,
                                do_block, pk);
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == TL_OK)
         st = TL_ERR_CUDA;

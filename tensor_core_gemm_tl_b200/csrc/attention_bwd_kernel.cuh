@@ -31,8 +31,11 @@
 // from there; nothing of size queries x keys leaves the SM.
 //
 // Pipeline: blocks of 64 columns alternate between two sets of Tensor Memory
-// columns and two softmax warpgroups, so the first products of block n + 1 run
-// while block n is turned into P and dX.
+// columns, so the first products of block n + 1 run while block n is turned
+// into P and dX.  Two warpgroups share each set, 32 columns a thread: sixteen
+// warps hide the latencies of one another's loads, exponentials and
+// conversions, which with two warpgroups of 64 columns a thread set the pace
+// (2560 clocks a block of 128 x 64 against 1280 of products).
 //
 // 16-bit range: bf16 takes P and dX as they are.  fp16 holds P times 2^10 and
 // dX times 2^4 over the power of two above the largest |dO| (P of long rows
@@ -180,17 +183,17 @@ struct AttnBwdConfig {
     static constexpr int OFF_BAR = OFF_Y + STAGES * STAGE_BYTES;
     static constexpr int BAR_X = 0, BAR_YF = 1, BAR_YE = 1 + STAGES;
     static constexpr int BAR_SF = 1 + 2 * STAGES;  // [buffer]: S and dP in Tensor Memory
-    static constexpr int BAR_PF = BAR_SF + 2;      // [buffer]: P and dX in Tensor Memory (4 warps arrive)
+    static constexpr int BAR_PF = BAR_SF + 2;      // [buffer]: P and dX in Tensor Memory (8 warps arrive)
     static constexpr int BAR_DONE = BAR_PF + 2;    // [buffer]: the second products have read them
-    static constexpr int BAR_EPS = BAR_DONE + 2;   // dQ: both warpgroups' parts of e are in shared memory (8 warps)
+    static constexpr int BAR_EPS = BAR_DONE + 2;   // dQ: the warpgroups' parts of e are in shared memory (16 warps)
     static constexpr int BAR_DRAIN = BAR_EPS + 1;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_EPS = OFF_MISC + 32;   // [warpgroup][128] floats
-    static constexpr int SMEM_BYTES = OFF_EPS + 1024 + 1024;
-    static constexpr int THREADS = 384;
-    static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 216;
-    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
+    static constexpr int SMEM_BYTES = OFF_EPS + 2048 + 1024;
+    static constexpr int THREADS = 640;  // 4 control warps, 4 warpgroups for P and dX
+    static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 104;
+    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 512 * REGS_SOFTMAX + THREADS - 1) / THREADS;
     // Tensor Memory columns: S and dP of buffer w, the accumulators
     static constexpr int TMEM_S = 0, TMEM_DP = 128, TMEM_A0 = 256, TMEM_A1 = 256 + D;
     static_assert(ROWS_BYTES + INTERVAL_BYTES <= 2048 && SMEM_BYTES <= 232448, "shared memory");
@@ -199,7 +202,7 @@ struct AttnBwdConfig {
 // X1, X2: the CTA's 128 rows (K and V, or Q and dO); Y1, Y2: the blocks of 64
 // it runs over (Q and dO, or K and V)
 template <class CF, int DT, bool DKV, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x1, const __grid_constant__ CUtensorMap map_x2,
                          const __grid_constant__ CUtensorMap map_y1, const __grid_constant__ CUtensorMap map_y2,
                          const AttnBwdParams p)
@@ -236,10 +239,10 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(CF::BAR_SF + i), 1);
-            mbar_init(bar(CF::BAR_PF + i), 4);
+            mbar_init(bar(CF::BAR_PF + i), 8);
             mbar_init(bar(CF::BAR_DONE + i), 1);
         }
-        mbar_init(bar(CF::BAR_EPS), 8);
+        mbar_init(bar(CF::BAR_EPS), 16);
         mbar_init(bar(CF::BAR_DRAIN), 1);
         *abort_flag = 0;
         range[0] = 0x7FFFFFFF;
@@ -262,7 +265,8 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const int wg = warp >= 4 ? (warp - 4) >> 2 : 0;       // softmax warpgroup
+    const int group = warp >= 4 ? (warp - 4) >> 2 : 0;    // warpgroup
+    const int wg = group & 1, half = group >> 1;          // its buffer, and which 32 of the 64 columns
     const int r = (warp & 3) * 32 + lane;                 // row of the tile (Tensor Memory lane)
     int2 seen = make_int2(0, 0);                          // dQ: the row's interval
     if constexpr (DKV) {
@@ -373,16 +377,18 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     tc_commit(bar(CF::BAR_SF + w));
                 };
+                // 16 values of P or dX take 8 columns; each half of the block's lies where its half of the scores was
+                auto p_col = [](int k) { return (k >> 1) * (CF::BN / 2) + (k & 1) * 8; };
                 auto second_products = [&](int w, int st, bool first) {
                     const uint64_t yd = yt_desc + ((st * CF::STAGE_BYTES) >> 4);
 #pragma unroll
                     for (int k = 0; k < CF::BN / 16; ++k)  // dV += P^T dO, or B += P c K
-                        tc_mma_f16_ts(tmem_base + CF::TMEM_A0, tmem_base + CF::TMEM_S + CF::BN * w + 8 * k,
+                        tc_mma_f16_ts(tmem_base + CF::TMEM_A0, tmem_base + CF::TMEM_S + CF::BN * w + p_col(k),
                                       yd + (((DKV ? CF::Y_BYTES : 0) + 2048 * k) >> 4), IDESC_2,
                                       (!first || k > 0) ? 1u : 0u);
 #pragma unroll
                     for (int k = 0; k < CF::BN / 16; ++k)  // dK += dX^T Q, or dQ += dX K
-                        tc_mma_f16_ts(tmem_base + CF::TMEM_A1, tmem_base + CF::TMEM_DP + CF::BN * w + 8 * k,
+                        tc_mma_f16_ts(tmem_base + CF::TMEM_A1, tmem_base + CF::TMEM_DP + CF::BN * w + p_col(k),
                                       yd + ((2048 * k) >> 4), IDESC_2, (!first || k > 0) ? 1u : 0u);
                     tc_commit(bar(CF::BAR_DONE + w));
                     tc_commit(bar(CF::BAR_YE + st));
@@ -433,6 +439,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + CF::BN * wg);
         const uint32_t dp_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_DP + CF::BN * wg);
+        constexpr int HN = CF::BN / 2;  // columns a thread
         auto wait_warp = [&](int id, uint32_t parity) -> bool {
             const bool w = wait_bounded(bar(id), parity, abort_flag, timeout, ERR_EPILOGUE);
             return __all_sync(0xffffffffu, w);
@@ -486,28 +493,28 @@ __global__ void __launch_bounds__(384, 1)
             if (!(ok = wait_warp(CF::BAR_SF + wg, static_cast<uint32_t>(n >> 1) & 1u)))
                 break;
             tc_fence_after_sync();
-            uint32_t sv[64], dp[64];
-            tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-            tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-            tmem_load_32cols(dp_addr, *reinterpret_cast<uint32_t(*)[32]>(&dp[0]));
-            tmem_load_32cols(dp_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&dp[32]));
+            uint32_t sv[HN], dp[HN];
+            tmem_load_32cols(s_addr + HN * half, sv);
+            tmem_load_32cols(dp_addr + HN * half, dp);
             // DKV: -lse, -delta, first key, end key and "sees more than one key" of the block's queries
-            const float4 *info = reinterpret_cast<const float4 *>(smem + CF::OFF_Y + st * CF::STAGE_BYTES + 2 * CF::Y_BYTES);
+            const float4 *info = reinterpret_cast<const float4 *>(smem + CF::OFF_Y + st * CF::STAGE_BYTES + 2 * CF::Y_BYTES) +
+                                 half * (HN / 4);
             const int4 *iv = reinterpret_cast<const int4 *>(info + 2 * CF::BN / 4);
             const float4 *many = info + 4 * CF::BN / 4;
             // |p_i - j|: the column's step away from the first column's distance
-            const float dist0 = DKV ? static_cast<float>(p.mask.q_offset + yb * CF::BN - (x0 + r))
-                                    : static_cast<float>(p.mask.q_offset + x0 + r - yb * CF::BN);
-            const int key = x0 + r;                                              // DKV
-            const int nlo = seen.x - yb * CF::BN, nhi = seen.y - yb * CF::BN;     // dQ
-            bool whole = DKV ? rg.z <= x0 && rg.w >= x0 + CF::BM : nlo <= 0 && nhi >= CF::BN;
+            const int y0 = yb * CF::BN + HN * half;  // the thread's first column
+            const float dist0 = DKV ? static_cast<float>(p.mask.q_offset + y0 - (x0 + r))
+                                    : static_cast<float>(p.mask.q_offset + x0 + r - y0);
+            const int key = x0 + r;                             // DKV
+            const int nlo = seen.x - y0, nhi = seen.y - y0;     // dQ
+            bool whole = DKV ? rg.z <= x0 && rg.w >= x0 + CF::BM : nlo <= 0 && nhi >= HN;
             whole = __all_sync(0xffffffffu, whole);
             tmem_load_wait();
             // scores and dP to P and dX, in place and packed in pairs; only blocks that cut an interval are masked
             auto block = [&](auto masked) {
                 constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
-                for (int e = 0; e < CF::BN; e += 4) {
+                for (int e = 0; e < HN; e += 4) {
                     float4 l4 = make_float4(row_nlse, row_nlse, row_nlse, row_nlse);
                     float4 d4 = make_float4(row_ndelta, row_ndelta, row_ndelta, row_ndelta);
                     float4 m4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
@@ -575,8 +582,9 @@ __global__ void __launch_bounds__(384, 1)
                 block(std::false_type{});
             else
                 block(std::true_type{});
-            tmem_store_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-            tmem_store_32cols(dp_addr, *reinterpret_cast<uint32_t(*)[32]>(&dp[0]));
+            // over the first half of the columns this thread read itself (the other warpgroup may still read its own)
+            tmem_store_16cols(s_addr + HN * half, sv);
+            tmem_store_16cols(dp_addr + HN * half, dp);
             tmem_store_wait();
             tc_fence_before_sync();
             __syncwarp();
@@ -593,21 +601,22 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (!DKV) {
             float *eps_smem = reinterpret_cast<float *>(smem + CF::OFF_EPS);
             const float2 mine = fadd2(eps[0], eps[1]);
-            eps_smem[wg * 128 + r] = mine.x + mine.y;
+            eps_smem[group * 128 + r] = mine.x + mine.y;
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar(CF::BAR_EPS));
             ok = ok && wait_warp(CF::BAR_EPS, 0);
             if (ok)
-                e_row = (eps_smem[r] + eps_smem[128 + r]) * (DT == 0 ? 1.0f / 1024.0f : 1.0f);
+                e_row = ((eps_smem[r] + eps_smem[128 + r]) + (eps_smem[256 + r] + eps_smem[384 + r])) *
+                        (DT == 0 ? 1.0f / 1024.0f : 1.0f);
         }
         if (ok) {
             tc_fence_after_sync();
             const int row = x0 + r;
             const bool live = row < (DKV ? p.mask.Sk : p.mask.Sq);
             constexpr float p_undo = DT == 0 ? 1.0f / 1024.0f : 1.0f;
-            // DKV: warpgroup 0 writes dK, 1 writes dV; dQ: half the columns each
-            uint16_t *out = DKV && wg ? p.out1 : p.out0;
+            // DKV: buffer 0's warpgroups write dK, buffer 1's dV, half the columns each; dQ: a quarter each
+            uint16_t *out = DKV && wg ? p.out1 : p.out0;  // (batch, head, row) strides below
             const int64_t *sd = DKV && wg ? p.s1 : p.s0;
             const float mul = DKV && wg ? p_undo : p.scale * x_undo;
             out += b * sd[0] + head * sd[1] + static_cast<int64_t>(row) * sd[2];
@@ -616,44 +625,44 @@ __global__ void __launch_bounds__(384, 1)
             const float e_mul = -e_row * p.scale * p_undo * (CAP ? 4.0f : 1.0f);
             const bool none = n_total == 0 || (!DKV && seen.y - seen.x <= 1);  // nothing comes through
             if constexpr (!DKV) {
-                if (wg == 0 && live)
+                if (group == 0 && live)
                     p.rows[((static_cast<int64_t>(b) * p.H + head) * p.nqb + row / CF::BN) * 2 * CF::BN + CF::BN +
                            row % CF::BN] = row_ndelta - e_row;
             }
-            const int c0 = DKV ? 0 : wg * (D / 64), c1 = DKV ? D / 32 : (wg + 1) * (D / 64);
+            const int c0 = DKV ? half * (D / 32) : group * (D / 64), c1 = c0 + (DKV ? D / 32 : D / 64);  // of 16 columns
 #pragma unroll 1
             for (int c = c0; c < c1; ++c) {
-                uint32_t o[32];
+                uint32_t o[16];
                 if (n_total > 0) {
-                    tmem_load_32cols(acc + 32 * c, o);
+                    tmem_load_16cols(acc + 16 * c, o);
                     if constexpr (!DKV) {
-                        uint32_t o0[32];
-                        tmem_load_32cols(acc0 + 32 * c, o0);
+                        uint32_t o0[16];
+                        tmem_load_16cols(acc0 + 16 * c, o0);
                         tmem_load_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             o[e] = __float_as_uint(fmaf(__uint_as_float(o0[e]), e_mul, __uint_as_float(o[e]) * mul));
                     } else {
                         tmem_load_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * mul);
                     }
                 }
                 if (none) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 16; ++e)
                         o[e] = 0;
                 }
                 if (live) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
+                    for (int v = 0; v < 2; ++v) {
                         uint4 w;
                         w.x = pack2<DT>(__uint_as_float(o[8 * v]), __uint_as_float(o[8 * v + 1]));
                         w.y = pack2<DT>(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3]));
                         w.z = pack2<DT>(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5]));
                         w.w = pack2<DT>(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7]));
-                        reinterpret_cast<uint4 *>(out + 32 * c)[v] = w;
+                        reinterpret_cast<uint4 *>(out + 16 * c)[v] = w;
                     }
                 }
             }
