@@ -6,7 +6,7 @@
 namespace tl {
 namespace {
 
-using BwdFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnBwdParams);
+using BwdFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnBwdParams);
 using RowsFn = void (*)(AttnBwdRowsParams);
 
 struct BwdEntry {
@@ -79,16 +79,15 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     if ((st = ready_kernel(d, dkv, e.smem, e.launch_regs)) != TL_OK ||
         (st = ready_kernel(d, dq, e.smem, e.launch_regs)) != TL_OK)
         return st;
-    // X: 128-row tiles, Y: blocks of 64 rows; dK and dV hold the keys, dQ the queries
-    CUtensorMap k_tile, v_tile, q_tile, do_tile, k_block, v_block, q_block, do_block;
-    if (!encode_heads(&k_tile, K, dtype, batch, c.kv_heads, seq_k, head_dim, c.k, 128) ||
-        !encode_heads(&v_tile, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, 128) ||
-        !encode_heads(&q_tile, Q, dtype, batch, heads, seq_q, head_dim, c.q, 128) ||
-        !encode_heads(&do_tile, dO, dtype, batch, heads, seq_q, head_dim, sdo, 128) ||
-        !encode_heads(&k_block, K, dtype, batch, c.kv_heads, seq_k, head_dim, c.k, kBwdCols) ||
-        !encode_heads(&v_block, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, kBwdCols) ||
-        !encode_heads(&q_block, Q, dtype, batch, heads, seq_q, head_dim, c.q, kBwdCols) ||
-        !encode_heads(&do_block, dO, dtype, batch, heads, seq_q, head_dim, sdo, kBwdCols))
+    // one box of 128 rows serves both passes
+    CUtensorMap tk, tv, tq, tdo, out_q, out_k, out_v;
+    if (!encode_heads(&tk, K, dtype, batch, c.kv_heads, seq_k, head_dim, c.k, 128) ||
+        !encode_heads(&tv, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, 128) ||
+        !encode_heads(&tq, Q, dtype, batch, heads, seq_q, head_dim, c.q, 128) ||
+        !encode_heads(&tdo, dO, dtype, batch, heads, seq_q, head_dim, sdo, 128) ||
+        !encode_heads_out(&out_q, dQ, dtype, batch, heads, seq_q, head_dim, sdq, 32, 16) ||
+        !encode_heads_out(&out_k, dK, dtype, batch, c.kv_heads, seq_k, head_dim, sdk, 32, 16) ||
+        !encode_heads_out(&out_v, dV, dtype, batch, c.kv_heads, seq_k, head_dim, sdv, 32, 16))
         return TL_ERR_CUDA;
 
     const int64_t nqb = ceil_div(seq_q, kBwdCols);
@@ -114,6 +113,7 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     rp.rows = reinterpret_cast<float *>(at);
     rp.intervals = reinterpret_cast<int32_t *>(at + rows_bytes);
     rp.ranges = reinterpret_cast<int4 *>(at + rows_bytes + interval_bytes);
+    rp.next = reinterpret_cast<int32_t *>(at + rows_bytes + interval_bytes + range_bytes + 16);
     rp.amax = dtype == TL_F16 ? reinterpret_cast<unsigned *>(at + rows_bytes + interval_bytes + range_bytes) : nullptr;
     AttnBwdParams p{};
     p.mask = c.mask;
@@ -130,29 +130,29 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     p.amax = rp.amax;
     p.timeout_ns = kDefaultTimeoutNs;
     AttnBwdParams pk = p, pq = p;
+    pq.next = rp.next;
+    pk.next = rp.next + 1;
     pk.tiles = static_cast<int32_t>(ceil_div(seq_k, 128));
-    pk.out0 = static_cast<uint16_t *>(dK);
-    pk.out1 = static_cast<uint16_t *>(dV);
     pq.tiles = static_cast<int32_t>(ceil_div(seq_q, 128));
-    pq.out0 = static_cast<uint16_t *>(dQ);
-    pq.out1 = nullptr;
     for (int i = 0; i < 3; ++i) {
         rp.so[i] = c.o.s[i];
         rp.sdo[i] = sdo.s[i];
-        pk.s0[i] = sdk.s[i];
-        pk.s1[i] = sdv.s[i];
-        pq.s0[i] = sdq.s[i];
     }
     if (rp.amax && cudaMemsetAsync(rp.amax, 0, sizeof(unsigned), stream) != cudaSuccess)
         st = TL_ERR_CUDA;
     if (st == TL_OK)
         st = launch_overlapped(e.rows[dtype], nqb * batch * heads, 256, 0, stream, rp);
+    // persistent CTAs, one an SM; they take tiles from the passes' counters
+    auto launch = [&](BwdFn fn, const CUtensorMap &x1, const CUtensorMap &x2, const CUtensorMap &y1,
+                      const CUtensorMap &y2, const CUtensorMap &o0, const CUtensorMap &o1, int64_t items,
+                      const AttnBwdParams &a) {
+        return launch_overlapped(fn, items < d->num_sms ? items : d->num_sms, e.threads, e.smem, stream, x1, x2, y1, y2,
+                                 o0, o1, a);
+    };
     if (st == TL_OK)
-        st = launch_overlapped(dq, pq.tiles * batch * heads, e.threads, e.smem, stream, q_tile, do_tile, k_block, v_block,
-                               pq);
+        st = launch(dq, tq, tdo, tk, tv, out_q, out_q, pq.tiles * batch * heads, pq);
     if (st == TL_OK)
-        st = launch_overlapped(dkv, pk.tiles * batch * c.kv_heads, e.threads, e.smem, stream, k_tile, v_tile, q_block,
-                               do_block, pk);
+        st = launch(dkv, tk, tv, tq, tdo, out_k, out_v, pk.tiles * batch * c.kv_heads, pk);
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == TL_OK)
         st = TL_ERR_CUDA;
     return st;

@@ -30,12 +30,20 @@
 // as 16-bit values over the scores they came from and feed the second products
 // from there; nothing of size queries x keys leaves the SM.
 //
-// Pipeline: blocks of 64 columns alternate between two sets of Tensor Memory
-// columns, so the first products of block n + 1 run while block n is turned
-// into P and dX.  Two warpgroups share each set, 32 columns a thread: sixteen
-// warps hide the latencies of one another's loads, exponentials and
-// conversions, which with two warpgroups of 64 columns a thread set the pace
-// (2560 clocks a block of 128 x 64 against 1280 of products).
+// Pipeline (a block is 128 x 128 scores): sixteen warps, 32 columns a thread, turn
+// S(n) into P(n) and dP(n) into dX(n) in two steps, written over the scores they
+// came from.  The products go out as dV(n), S(n + 1), dK(n), dP(n + 1): S(n + 1) is
+// there when dX(n) is done, and dP(n + 1) when P(n + 1) is.  With D = 128 Tensor
+// Memory is full (S, dP and the two sums are 512 columns), so S(n + 1) waits until
+// dV(n) has read P(n); with D = 64 S has two sets of columns and does not.  The
+// CTAs are persistent and take tiles from a counter; the next tile's operands load
+// while this one's sums leave through shared memory and TMA stores (stores of a
+// row a thread held up every other memory operation of the SM, the products'
+// issue included: 5000 clocks a tile).
+//
+// What bounds it: 4 products of 128 x 128 x D a block, 2048 clocks with D = 128
+// at 4096 multiply-adds a clock and SM, against one 2^x a score (1024 clocks;
+// 2.5 times that with capped scores).
 //
 // 16-bit range: bf16 takes P and dX as they are.  fp16 holds P times 2^10 and
 // dX times 2^4 over the power of two above the largest |dO| (P of long rows
@@ -49,7 +57,7 @@
 
 namespace tl {
 
-constexpr int kBwdCols = 64;  // queries (DKV) or keys a step takes
+constexpr int kBwdCols = 128;  // rows and columns of a block of scores
 template <int DT>
 constexpr float kPShift = DT == 0 ? 10.0f : 0.0f;  // fp16 holds P times 2^10
 
@@ -57,16 +65,15 @@ struct AttnBwdParams {
     MaskParams mask;
     ScoreParams score;
     int32_t B, H, Hk, group;
-    int32_t nqb;               // blocks of 64 queries
-    int32_t tiles;             // 128-row tiles a CTA each: of the keys (DKV) or of the queries
+    int32_t nqb;               // blocks of 128 queries
+    int32_t tiles;             // 128-row tiles of the keys (DKV) or of the queries
     float scale;               // softmax scale
-    float *rows;               // [B][H][nqb][2][64]: -lse in log2 units (-inf where the row sees nothing) plus the
+    float *rows;               // [B][H][nqb][2][128]: -lse in log2 units (-inf where the row sees nothing) plus the
                                // exponent of P's factor, -delta
-    const int32_t *intervals;  // [B][nqb][3][64]: first and end key of each query; 0.0f where it sees one key, else 1.0f
+    const int32_t *intervals;  // [B][nqb][3][128]: first and end key of each query; 0.0f where it sees one key, else 1.0f
     const int4 *ranges;        // [B][nqb]: least first, largest end, largest first, least end of the block's queries
     const unsigned *amax;      // fp16: bits of the largest |dO|, else null
-    uint16_t *out0, *out1;     // dK, dV (DKV) or dQ, null
-    int64_t s0[3], s1[3];      // their strides (batch, head, row) in elements
+    int32_t *next;             // counter that tiles are taken from, 0 at the start
     uint64_t timeout_ns;
 };
 
@@ -80,9 +87,10 @@ struct AttnBwdRowsParams {
     int32_t *intervals;
     int4 *ranges;
     unsigned *amax;
+    int32_t *next;             // the two passes' tile counters
 };
 
-// One CTA (256 threads) per 64 queries of a head: 8 lanes a row.  Bound by
+// One CTA (256 threads) per 128 queries of a head: 8 lanes a row.  Bound by
 // reading O and dO once.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRowsParams p)
@@ -94,6 +102,8 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
     const int qb = static_cast<int>(blockIdx.x % p.nqb);
     const int bh = static_cast<int>(blockIdx.x / p.nqb);
     const int b = bh / p.H, h = bh % p.H;
+    if (blockIdx.x == 0 && threadIdx.x < 2)
+        p.next[threadIdx.x] = 0;
     const int32_t *docs = p.mask.doc_offsets
                               ? p.mask.doc_offsets + static_cast<int64_t>(b) * (p.mask.num_docs + 1) : nullptr;
     if (h == 0) {
@@ -173,38 +183,49 @@ struct AttnBwdConfig {
     static constexpr int D = D_;
     static constexpr int BM = 128, BN = kBwdCols;
     static constexpr int D_ATOMS = D / 64;
-    static constexpr int XATOM = 128 * 128, YATOM = BN * 128;  // bytes of 64 columns of a tile
-    static constexpr int X_BYTES = D_ATOMS * XATOM, Y_BYTES = D_ATOMS * YATOM;
+    static constexpr int ATOM = 128 * 128;  // bytes of 64 columns of a tile
+    static constexpr int TILE_BYTES = D_ATOMS * ATOM;
     static constexpr int ROWS_BYTES = 2 * BN * 4, INTERVAL_BYTES = 3 * BN * 4;  // of a block of queries
-    static constexpr int STAGES = 4;
-    static constexpr int STAGE_BYTES = 2 * Y_BYTES + 2048;  // Y1, Y2, rows, intervals
+    static constexpr int STAGES = D == 128 ? 2 : 4;
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES + 3072;  // Y1, Y2, rows, intervals
     static constexpr int OFF_X = 0;
-    static constexpr int OFF_Y = 2 * X_BYTES;
+    static constexpr int OFF_Y = 2 * TILE_BYTES;
     static constexpr int OFF_BAR = OFF_Y + STAGES * STAGE_BYTES;
-    static constexpr int BAR_X = 0, BAR_YF = 1, BAR_YE = 1 + STAGES;
-    static constexpr int BAR_SF = 1 + 2 * STAGES;  // [buffer]: S and dP in Tensor Memory
-    static constexpr int BAR_PF = BAR_SF + 2;      // [buffer]: P and dX in Tensor Memory (8 warps arrive)
-    static constexpr int BAR_DONE = BAR_PF + 2;    // [buffer]: the second products have read them
-    static constexpr int BAR_EPS = BAR_DONE + 2;   // dQ: the warpgroups' parts of e are in shared memory (16 warps)
-    static constexpr int BAR_DRAIN = BAR_EPS + 1;
+    static constexpr int BAR_XF = 0, BAR_XE = 1, BAR_YF = 2, BAR_YE = 2 + STAGES;
+    static constexpr int BAR_SF = 2 + 2 * STAGES;  // [set]: S in Tensor Memory
+    static constexpr int BAR_DPF = BAR_SF + 2;     // dP in Tensor Memory
+    static constexpr int BAR_PF = BAR_DPF + 1;     // [set]: P in Tensor Memory (16 warps arrive)
+    static constexpr int BAR_DXF = BAR_PF + 2;     // dX in Tensor Memory (16 warps)
+    static constexpr int BAR_PE = BAR_DXF + 1;     // [set]: P has been read
+    static constexpr int BAR_DXE = BAR_PE + 2;     // dX has been read
+    static constexpr int BAR_ACCF = BAR_DXE + 1;   // a tile's sums are complete
+    static constexpr int BAR_ACCE = BAR_ACCF + 1;  // and have been read (16 warps)
+    static constexpr int BAR_EPS = BAR_ACCE + 1;   // dQ: the warpgroups' parts of e are in shared memory (16 warps)
+    static constexpr int BAR_TF = BAR_EPS + 1;     // [slot]: a tile's description is in shared memory
+    static constexpr int BAR_TE = BAR_TF + 2;      // [slot]: and has been read (18: producer, MMA issuer, 16 warps)
+    static constexpr int BAR_DRAIN = BAR_TE + 2;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-    static constexpr int OFF_EPS = OFF_MISC + 32;   // [warpgroup][128] floats
-    static constexpr int SMEM_BYTES = OFF_EPS + 2048 + 1024;
+    static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
+    static constexpr int OFF_TILES = OFF_MISC + 16;  // [slot] x0, batch entry * heads + head, first block, blocks
+    static constexpr int OFF_EPS = OFF_TILES + 32;   // [tile & 1][warpgroup][128] floats
+    static constexpr int OFF_OUT = (OFF_EPS + 4096 + 127) / 128 * 128;  // [warp] 32 rows x 16 columns on their way out
+    static constexpr int SMEM_BYTES = OFF_OUT + 16 * 1024 + 1024;
     static constexpr int THREADS = 640;  // 4 control warps, 4 warpgroups for P and dX
     static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 104;
     static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 512 * REGS_SOFTMAX + THREADS - 1) / THREADS;
-    // Tensor Memory columns: S and dP of buffer w, the accumulators
-    static constexpr int TMEM_S = 0, TMEM_DP = 128, TMEM_A0 = 256, TMEM_A1 = 256 + D;
-    static_assert(ROWS_BYTES + INTERVAL_BYTES <= 2048 && SMEM_BYTES <= 232448, "shared memory");
+    static constexpr int S_SETS = D == 128 ? 1 : 2;  // sets of columns S alternates between
+    static constexpr int TMEM_S = 0, TMEM_DP = 128 * S_SETS, TMEM_A0 = TMEM_DP + 128, TMEM_A1 = TMEM_A0 + D;
+    static_assert(TMEM_A1 + D <= 512, "Tensor Memory columns");
+    static_assert(ROWS_BYTES + INTERVAL_BYTES <= 3072 && SMEM_BYTES <= 232448, "shared memory");
 };
 
-// X1, X2: the CTA's 128 rows (K and V, or Q and dO); Y1, Y2: the blocks of 64
-// it runs over (Q and dO, or K and V)
+// X1, X2: the CTA's 128 rows (K and V, or Q and dO); Y1, Y2: the blocks it runs
+// over (Q and dO, or K and V); out0, out1: dK and dV, or dQ twice
 template <class CF, int DT, bool DKV, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(640, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap map_x1, const __grid_constant__ CUtensorMap map_x2,
                          const __grid_constant__ CUtensorMap map_y1, const __grid_constant__ CUtensorMap map_y2,
+                         const __grid_constant__ CUtensorMap map_out0, const __grid_constant__ CUtensorMap map_out1,
                          const AttnBwdParams p)
 {
     constexpr int D = CF::D, STAGES = CF::STAGES;
@@ -213,15 +234,9 @@ __global__ void __launch_bounds__(640, 1)
                                                 ~static_cast<uintptr_t>(1023));
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);  // uniform for the compiler too
     const int lane = threadIdx.x & 31;
-    // the tile and its head.  Causal: the heaviest tiles first (the first keys,
-    // the last queries); else one head's tiles together.
     const int heads = DKV ? p.Hk : p.H;
     const int BH = p.B * heads;
-    const int bx = static_cast<int>(blockIdx.x);
-    const int tile = p.mask.causal ? (DKV ? bx / BH : p.tiles - 1 - bx / BH) : bx % p.tiles;
-    const int bh = p.mask.causal ? bx % BH : bx / p.tiles;
-    const int b = bh / heads, head = bh % heads;
-    const int x0 = tile * CF::BM;
+    const int items = p.tiles * BH;
 
     const uint32_t sX = smem_addr(smem + CF::OFF_X);
     const uint32_t sY = smem_addr(smem + CF::OFF_Y);
@@ -229,24 +244,33 @@ __global__ void __launch_bounds__(640, 1)
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CF::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *range = reinterpret_cast<int *>(tmem_slot + 2);  // first and end block of 64
+    int4 *tile_slots = reinterpret_cast<int4 *>(smem + CF::OFF_TILES);
+    float *eps_smem = reinterpret_cast<float *>(smem + CF::OFF_EPS);
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(CF::BAR_X), 1);
+        mbar_init(bar(CF::BAR_XF), 1);
+        mbar_init(bar(CF::BAR_XE), 1);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(bar(CF::BAR_YF + s), 1);
             mbar_init(bar(CF::BAR_YE + s), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(CF::BAR_SF + i), 1);
-            mbar_init(bar(CF::BAR_PF + i), 8);
-            mbar_init(bar(CF::BAR_DONE + i), 1);
+            mbar_init(bar(CF::BAR_PF + i), 16);
+            mbar_init(bar(CF::BAR_PE + i), 1);
         }
+        mbar_init(bar(CF::BAR_DPF), 1);
+        mbar_init(bar(CF::BAR_DXF), 16);
+        mbar_init(bar(CF::BAR_DXE), 1);
+        mbar_init(bar(CF::BAR_ACCF), 1);
+        mbar_init(bar(CF::BAR_ACCE), 16);
         mbar_init(bar(CF::BAR_EPS), 16);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(CF::BAR_TF + i), 1);
+            mbar_init(bar(CF::BAR_TE + i), 18);
+        }
         mbar_init(bar(CF::BAR_DRAIN), 1);
         *abort_flag = 0;
-        range[0] = 0x7FFFFFFF;
-        range[1] = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -255,389 +279,493 @@ __global__ void __launch_bounds__(640, 1)
         tma_prefetch_map(&map_x2);
         tma_prefetch_map(&map_y1);
         tma_prefetch_map(&map_y2);
+        tma_prefetch_map(&map_out0);
+        tma_prefetch_map(&map_out1);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), 512);
         tmem_relinquish();
     }
-    grid_dependency_wait();
-    grid_launch_dependents();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const int group = warp >= 4 ? (warp - 4) >> 2 : 0;    // warpgroup
-    const int wg = group & 1, half = group >> 1;          // its buffer, and which 32 of the 64 columns
-    const int r = (warp & 3) * 32 + lane;                 // row of the tile (Tensor Memory lane)
-    int2 seen = make_int2(0, 0);                          // dQ: the row's interval
-    if constexpr (DKV) {
-        // the blocks of queries that see some key of the tile
-        const int4 *rg = p.ranges + static_cast<int64_t>(b) * p.nqb;
-        int first = 0x7FFFFFFF, end = 0;
-        for (int q = threadIdx.x; q < p.nqb; q += CF::THREADS) {
-            const int4 v = __ldg(rg + q);
-            if (v.x < x0 + CF::BM && v.y > x0) {
-                first = min(first, q);
-                end = max(end, q + 1);
-            }
-        }
-        first = __reduce_min_sync(0xffffffffu, first);
-        end = __reduce_max_sync(0xffffffffu, end);
-        if (lane == 0) {
-            atomicMin(&range[0], first);
-            atomicMax(&range[1], end);
-        }
-    } else if (warp >= 4) {
-        const int i = x0 + r;
-        if (i < p.mask.Sq) {
-            const int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + i / CF::BN) * 3 * CF::BN + i % CF::BN;
-            seen = make_int2(iv[0], iv[CF::BN]);
-        }
-        const int lo = __reduce_min_sync(0xffffffffu, seen.y > seen.x ? seen.x / CF::BN : 0x7FFFFFFF);
-        const int hi = __reduce_max_sync(0xffffffffu, (seen.y + CF::BN - 1) / CF::BN);
-        if (lane == 0) {
-            atomicMin(&range[0], lo);
-            atomicMax(&range[1], hi);
-        }
-    }
-    __syncthreads();
     const uint32_t tmem_base = *tmem_slot;
     const uint64_t timeout = p.timeout_ns;
-    const int y_first = range[0];
-    const int y_count = range[1] > y_first ? range[1] - y_first : 0;
-    const int n_total = DKV ? y_count * p.group : y_count;  // DKV: over the heads that share the keys, one after another
+    grid_dependency_wait();
+    grid_launch_dependents();
 
-    uint32_t x_issued = 0, y_issued = 0, y_par = 0;
+    // The tiles this CTA takes, one after another: every role reads the same
+    // descriptions, two of them ahead at most.
+    auto take_tile = [&](int t, int4 *out) {
+        const bool w = __all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_TF + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u,
+                                                            abort_flag, timeout, ERR_EPILOGUE));
+        if (!w)
+            return false;
+        *out = tile_slots[t & 1];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar(CF::BAR_TE + (t & 1)));
+        return out->x >= 0;
+    };
+
+    uint32_t issued = 0, parity = 0;  // bit 0: X, bits 8..: stages
     if (warp < 4) {
         regs_decrease<CF::REGS_CONTROL>();
         if (warp == 0) {
             // ------------------------------------------------------------ producer
-            if (lane == 0 && n_total > 0) {
-                mbar_arrive_expect_tx(bar(CF::BAR_X), 2 * CF::X_BYTES);
+            int st = 0;
+            uint32_t ph = 0, xph = 0;
+            int4 tl;
+            bool ok = true;
+            for (int t = 0; ok && take_tile(t, &tl); ++t) {
+                if (tl.w == 0)
+                    continue;
+                const int b = tl.y / heads, head = tl.y - b * heads;
+                if (lane == 0) {
+                    ok = wait_bounded(bar(CF::BAR_XE), xph ^ 1u, abort_flag, timeout, ERR_PRODUCER);
+                    if (ok) {
+                        mbar_arrive_expect_tx(bar(CF::BAR_XF), 2 * CF::TILE_BYTES);
 #pragma unroll
-                for (int a = 0; a < CF::D_ATOMS; ++a) {
-                    tma_load_4d(sX + a * CF::XATOM, &map_x1, bar(CF::BAR_X), 64 * a, x0, head, b);
-                    tma_load_4d(sX + CF::X_BYTES + a * CF::XATOM, &map_x2, bar(CF::BAR_X), 64 * a, x0, head, b);
+                        for (int a = 0; a < CF::D_ATOMS; ++a) {
+                            tma_load_4d(sX + a * CF::ATOM, &map_x1, bar(CF::BAR_XF), 64 * a, tl.x, head, b);
+                            tma_load_4d(sX + CF::TILE_BYTES + a * CF::ATOM, &map_x2, bar(CF::BAR_XF), 64 * a, tl.x, head, b);
+                        }
+                        issued |= 1u;
+                        parity = (parity & ~1u) | xph;
+                    }
+                    // DKV: over the heads that share the keys, one after another
+                    int yb = tl.z, yh = DKV ? head * p.group : head / p.group;
+                    const int n_total = DKV ? tl.w * p.group : tl.w;
+                    for (int n = 0; ok && n < n_total; ++n) {
+                        if (!(ok = wait_bounded(bar(CF::BAR_YE + st), ph ^ 1u, abort_flag, timeout, ERR_PRODUCER)))
+                            break;
+                        const uint32_t full = bar(CF::BAR_YF + st);
+                        const uint32_t dst = sY + st * CF::STAGE_BYTES;
+                        mbar_arrive_expect_tx(full, 2 * CF::TILE_BYTES + (DKV ? CF::ROWS_BYTES + CF::INTERVAL_BYTES : 0));
+#pragma unroll
+                        for (int a = 0; a < CF::D_ATOMS; ++a)
+                            tma_load_4d(dst + a * CF::ATOM, &map_y1, full, 64 * a, yb * CF::BN, yh, b);
+                        if constexpr (DKV) {
+                            bulk_load_g2s(dst + 2 * CF::TILE_BYTES,
+                                          p.rows + ((static_cast<int64_t>(b) * p.H + yh) * p.nqb + yb) * 2 * CF::BN,
+                                          CF::ROWS_BYTES, full);
+                            bulk_load_g2s(dst + 2 * CF::TILE_BYTES + CF::ROWS_BYTES,
+                                          p.intervals + (static_cast<int64_t>(b) * p.nqb + yb) * 3 * CF::BN,
+                                          CF::INTERVAL_BYTES, full);
+                        }
+#pragma unroll
+                        for (int a = 0; a < CF::D_ATOMS; ++a)
+                            tma_load_4d(dst + CF::TILE_BYTES + a * CF::ATOM, &map_y2, full, 64 * a, yb * CF::BN, yh, b);
+                        issued |= 256u << st;
+                        parity = (parity & ~(256u << st)) | (ph << (8 + st));
+                        if (++yb == tl.z + tl.w) {
+                            yb = tl.z;
+                            ++yh;
+                        }
+                        if (++st == STAGES) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
                 }
-                x_issued = 1;
-                int st = 0, yb = y_first, yh = DKV ? head * p.group : head / p.group;
-                uint32_t ph = 0;
-                for (int n = 0; n < n_total; ++n) {
-                    if (!wait_bounded(bar(CF::BAR_YE + st), ph ^ 1u, abort_flag, timeout, ERR_PRODUCER))
-                        break;
-                    const uint32_t full = bar(CF::BAR_YF + st);
-                    const uint32_t dst = sY + st * CF::STAGE_BYTES;
-                    mbar_arrive_expect_tx(full, 2 * CF::Y_BYTES + (DKV ? CF::ROWS_BYTES + CF::INTERVAL_BYTES : 0));
-#pragma unroll
-                    for (int a = 0; a < CF::D_ATOMS; ++a)
-                        tma_load_4d(dst + a * CF::YATOM, &map_y1, full, 64 * a, yb * CF::BN, yh, b);
-                    if constexpr (DKV) {
-                        bulk_load_g2s(dst + 2 * CF::Y_BYTES,
-                                      p.rows + ((static_cast<int64_t>(b) * p.H + yh) * p.nqb + yb) * 2 * CF::BN,
-                                      CF::ROWS_BYTES, full);
-                        bulk_load_g2s(dst + 2 * CF::Y_BYTES + CF::ROWS_BYTES,
-                                      p.intervals + (static_cast<int64_t>(b) * p.nqb + yb) * 3 * CF::BN,
-                                      CF::INTERVAL_BYTES, full);
-                    }
-#pragma unroll
-                    for (int a = 0; a < CF::D_ATOMS; ++a)
-                        tma_load_4d(dst + CF::Y_BYTES + a * CF::YATOM, &map_y2, full, 64 * a, yb * CF::BN, yh, b);
-                    y_issued |= 1u << st;
-                    y_par = (y_par & ~(1u << st)) | (ph << st);
-                    if (++yb == y_first + y_count) {
-                        yb = y_first;
-                        ++yh;
-                    }
-                    if (++st == STAGES) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                }
+                xph ^= 1u;
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             }
-            __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
             // the whole warp walks the loop and one elected lane issues: what the
             // instructions are made from stays uniform across the warp
-            if (n_total > 0) {
-                constexpr uint32_t IDESC_1 = mma_idesc_f16(DT, 128, CF::BN, 0, 0);  // both K-major
-                constexpr uint32_t IDESC_2 = mma_idesc_f16(DT, 128, D, 0, 1);       // A from Tensor Memory, Y N-major
-                const uint64_t x_desc = smem_desc_sw128(sX, 16, 1024);
-                const uint64_t y_desc = smem_desc_sw128(sY, 16, 1024);
-                const uint64_t yt_desc = smem_desc_sw128(sY, CF::YATOM, 1024);
-                auto first_products = [&](int w, int st) {
+            constexpr uint32_t IDESC_1 = mma_idesc_f16(DT, 128, CF::BN, 0, 0);  // both K-major
+            constexpr uint32_t IDESC_2 = mma_idesc_f16(DT, 128, D, 0, 1);       // A from Tensor Memory, Y N-major
+            const uint64_t x_desc = smem_desc_sw128(sX, 16, 1024);
+            const uint64_t y_desc = smem_desc_sw128(sY, 16, 1024);
+            const uint64_t yt_desc = smem_desc_sw128(sY, CF::ATOM, 1024);
+            // S (into set `set`) or dP of the block in stage `st` from X1, Y1 or X2, Y2
+            auto first_product = [&](int m, int st, int set, int done) {
+                if (elect_one()) {
                     const uint64_t yd = y_desc + ((st * CF::STAGE_BYTES) >> 4);
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(m ? CF::TMEM_DP : CF::TMEM_S + 128 * set);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint32_t d = tmem_base + static_cast<uint32_t>((m ? CF::TMEM_DP : CF::TMEM_S) + CF::BN * w);
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            tc_mma_f16(d, x_desc + ((m * CF::X_BYTES + (k >> 2) * CF::XATOM + (k & 3) * 32) >> 4),
-                                       yd + ((m * CF::Y_BYTES + (k >> 2) * CF::YATOM + (k & 3) * 32) >> 4), IDESC_1,
-                                       k != 0 ? 1u : 0u);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t at = (m * CF::TILE_BYTES + (k >> 2) * CF::ATOM + (k & 3) * 32) >> 4;
+                        tc_mma_f16(d, x_desc + at, yd + at, IDESC_1, k != 0 ? 1u : 0u);
                     }
-                    tc_commit(bar(CF::BAR_SF + w));
-                };
-                // 16 values of P or dX take 8 columns; each half of the block's lies where its half of the scores was
-                auto p_col = [](int k) { return (k >> 1) * (CF::BN / 2) + (k & 1) * 8; };
-                auto second_products = [&](int w, int st, bool first) {
-                    const uint64_t yd = yt_desc + ((st * CF::STAGE_BYTES) >> 4);
-#pragma unroll
-                    for (int k = 0; k < CF::BN / 16; ++k)  // dV += P^T dO, or B += P c K
-                        tc_mma_f16_ts(tmem_base + CF::TMEM_A0, tmem_base + CF::TMEM_S + CF::BN * w + p_col(k),
-                                      yd + (((DKV ? CF::Y_BYTES : 0) + 2048 * k) >> 4), IDESC_2,
-                                      (!first || k > 0) ? 1u : 0u);
-#pragma unroll
-                    for (int k = 0; k < CF::BN / 16; ++k)  // dK += dX^T Q, or dQ += dX K
-                        tc_mma_f16_ts(tmem_base + CF::TMEM_A1, tmem_base + CF::TMEM_DP + CF::BN * w + p_col(k),
-                                      yd + ((2048 * k) >> 4), IDESC_2, (!first || k > 0) ? 1u : 0u);
-                    tc_commit(bar(CF::BAR_DONE + w));
-                    tc_commit(bar(CF::BAR_YE + st));
-                };
-                int st = 0, st1 = 0;  // stages of block n and of block n + 1
-                uint32_t ph1 = 0;
-                auto wait = [&](int id, uint32_t par, unsigned code) {
-                    return __all_sync(0xffffffffu, wait_bounded(bar(id), par, abort_flag, timeout, code)) != 0;
-                };
-                bool ok = wait(CF::BAR_X, 0, ERR_MMA_DATA);
-                for (int n = -1; ok && n < n_total; ++n) {
-                    if (n + 1 < n_total) {
-                        const int w1 = (n + 1) & 1;
-                        // the buffer's previous P and dX (block n - 1) have been read
-                        if (!wait(CF::BAR_YF + st1, ph1, ERR_MMA_DATA) ||
-                            (n >= 1 && !wait(CF::BAR_DONE + w1, static_cast<uint32_t>((n - 1) >> 1) & 1u, ERR_MMA_ACC)))
-                            break;
-                        tc_fence_after_sync();
-                        if (elect_one())
-                            first_products(w1, st1);
-                        __syncwarp();
-                        if (++st1 == STAGES) {
-                            st1 = 0;
-                            ph1 ^= 1u;
-                        }
-                    }
-                    if (n >= 0) {
-                        if (!wait(CF::BAR_PF + (n & 1), static_cast<uint32_t>(n >> 1) & 1u, ERR_MMA_ACC))
-                            break;
-                        tc_fence_after_sync();
-                        if (elect_one())
-                            second_products(n & 1, st, n == 0);
-                        __syncwarp();
-                        if (++st == STAGES)
-                            st = 0;
-                    }
+                    tc_commit(bar(done));
                 }
-                if (elect_one())
-                    tc_commit(bar(CF::BAR_DRAIN));
                 __syncwarp();
-                wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
+            };
+            // 16 values of P or dX take 8 columns; each 32 of the block's lie where their scores were
+            auto p_col = [](int k) { return (k >> 1) * 32 + (k & 1) * 8; };
+            // dV += P^T dO, or B += P c K (m = 0); dK += dX^T Q, or dQ += dX K (m = 1)
+            auto second_product = [&](int m, int st, int set, bool first, int done, int done2) {
+                if (elect_one()) {
+                    const uint64_t yd = yt_desc + ((st * CF::STAGE_BYTES + (DKV && m == 0 ? CF::TILE_BYTES : 0)) >> 4);
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(m ? CF::TMEM_A1 : CF::TMEM_A0);
+                    const uint32_t a = tmem_base + static_cast<uint32_t>(m ? CF::TMEM_DP : CF::TMEM_S + 128 * set);
+#pragma unroll
+                    for (int k = 0; k < CF::BN / 16; ++k)
+                        tc_mma_f16_ts(d, a + p_col(k), yd + ((2048 * k) >> 4), IDESC_2, (!first || k > 0) ? 1u : 0u);
+                    tc_commit(bar(done));
+                    if (done2 >= 0)
+                        tc_commit(bar(done2));
+                }
+                __syncwarp();
+            };
+            auto wait = [&](int id, uint32_t par) {
+                return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_MMA_DATA)) != 0;
+            };
+            auto commit = [&](int id) {
+                if (elect_one())
+                    tc_commit(bar(id));
+                __syncwarp();
+            };
+            int st = 0;
+            uint32_t ph = 0, g = 0, busy = 0;  // g: blocks so far; busy: tiles with blocks so far
+            int4 tl;
+            bool ok = true;
+            for (int t = 0; ok && take_tile(t, &tl); ++t) {
+                const int n_total = DKV ? tl.w * p.group : tl.w;
+                if (n_total == 0)
+                    continue;
+                // g: block n of the tile; its stage st, S in set g % S_SETS
+                auto issue_s = [&](uint32_t block, int stage, uint32_t phase) {
+                    // every wait follows each phase of its barrier in turn, so no two phases can be mistaken
+                    const int set = static_cast<int>(block % CF::S_SETS);
+                    if (!wait(CF::BAR_YF + stage, phase) ||
+                        (block >= CF::S_SETS && !wait(CF::BAR_PE + set, block / CF::S_SETS - 1)))
+                        return false;
+                    tc_fence_after_sync();
+                    first_product(0, stage, set, CF::BAR_SF + set);
+                    return true;
+                };
+                auto issue_dp = [&](uint32_t block, int stage) {
+                    if (block > 0 && !wait(CF::BAR_DXE, block - 1))
+                        return false;
+                    tc_fence_after_sync();
+                    first_product(1, stage, 0, CF::BAR_DPF);
+                    return true;
+                };
+                ok = wait(CF::BAR_XF, busy) && issue_s(g, st, ph) && issue_dp(g, st);
+                if (ok && n_total == 1)
+                    commit(CF::BAR_XE);
+                for (int n = 0; ok && n < n_total; ++n, ++g) {
+                    const int st1 = st + 1 == STAGES ? 0 : st + 1;
+                    const uint32_t ph1 = st1 == 0 ? ph ^ 1u : ph;
+                    const int set = static_cast<int>(g % CF::S_SETS);
+                    const bool next = n + 1 < n_total;
+                    if (CF::S_SETS > 1 && next && !(ok = issue_s(g + 1, st1, ph1)))
+                        break;
+                    // the last tile's sums have been read before this one's begin
+                    if (!(ok = wait(CF::BAR_PF + set, g / CF::S_SETS)) || (n == 0 && busy > 0 && !(ok = wait(CF::BAR_ACCE, busy - 1))))
+                        break;
+                    tc_fence_after_sync();
+                    second_product(0, st, set, n == 0, CF::BAR_PE + set, -1);
+                    if (CF::S_SETS == 1 && next && !(ok = issue_s(g + 1, st1, ph1)))
+                        break;
+                    if (!(ok = wait(CF::BAR_DXF, g)))
+                        break;
+                    tc_fence_after_sync();
+                    second_product(1, st, 0, n == 0, CF::BAR_DXE, CF::BAR_YE + st);
+                    if (next && !(ok = issue_dp(g + 1, st1)))
+                        break;
+                    if (n + 2 == n_total)
+                        commit(CF::BAR_XE);
+                    st = st1;
+                    ph = ph1;
+                }
+                if (ok)
+                    commit(CF::BAR_ACCF);
+                ++busy;
             }
-            __syncwarp();
+            commit(CF::BAR_DRAIN);
+            wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ tiles
+            bool more = true;
+            for (int t = 0; more; ++t) {
+                if (t >= 2 && !__all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_TE + (t & 1)),
+                                                                    static_cast<uint32_t>((t >> 1) - 1) & 1u, abort_flag,
+                                                                    timeout, ERR_EPILOGUE)))
+                    break;
+                int item = 0;
+                if (lane == 0)
+                    item = atomicAdd(p.next, 1);
+                item = __shfl_sync(0xffffffffu, item, 0);
+                more = item < items;
+                int4 tl = make_int4(-1, 0, 0, 0);
+                if (more) {
+                    // causal: the heaviest tiles first (the first keys, the last queries); else one head's tiles together
+                    const int tile = p.mask.causal ? (DKV ? item / BH : p.tiles - 1 - item / BH) : item % p.tiles;
+                    const int bh = p.mask.causal ? item % BH : item / p.tiles;
+                    const int b = bh / heads, x0 = tile * CF::BM;
+                    const int4 *rg = p.ranges + static_cast<int64_t>(b) * p.nqb;
+                    int first = 0x7FFFFFFF, end = 0;
+                    if constexpr (DKV) {
+                        // the blocks of queries that see some key of the tile
+                        for (int q = lane; q < p.nqb; q += 32) {
+                            const int4 v = __ldg(rg + q);
+                            if (v.x < x0 + CF::BM && v.y > x0) {
+                                first = min(first, q);
+                                end = max(end, q + 1);
+                            }
+                        }
+                        first = __reduce_min_sync(0xffffffffu, first);
+                        end = __reduce_max_sync(0xffffffffu, end);
+                    } else {
+                        const int4 v = __ldg(rg + tile);  // the blocks of keys that some query of the tile sees
+                        first = v.x / CF::BN;
+                        end = (v.y + CF::BN - 1) / CF::BN;
+                    }
+                    tl = make_int4(x0, bh, first, end > first ? end - first : 0);
+                }
+                if (lane == 0) {
+                    tile_slots[t & 1] = tl;
+                    mbar_arrive(bar(CF::BAR_TF + (t & 1)));
+                }
+                __syncwarp();
+            }
         }
+        __syncwarp();
     } else {
         regs_increase<CF::REGS_SOFTMAX>();
-        // ------------------------------------------------------------ P and dX, one row a thread
+        // ------------------------------------------------------------ P and dX: one row and 32 columns a thread
+        constexpr int HN = 32;
+        const int group = (warp - 4) >> 2;         // which 32 columns
+        const int r = (warp & 3) * 32 + lane;      // row of the tile (Tensor Memory lane)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + CF::BN * wg);
-        const uint32_t dp_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_DP + CF::BN * wg);
-        constexpr int HN = CF::BN / 2;  // columns a thread
-        auto wait_warp = [&](int id, uint32_t parity) -> bool {
-            const bool w = wait_bounded(bar(id), parity, abort_flag, timeout, ERR_EPILOGUE);
-            return __all_sync(0xffffffffu, w);
+        const uint32_t s_addr0 = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + HN * group);
+        const uint32_t dp_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_DP + HN * group);
+        auto wait_warp = [&](int id, uint32_t par) -> bool {
+            return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_EPILOGUE));
         };
-        // fp16: P times 2^p_shift, dX times x_mul over P's factor; x_undo takes dX's factor out again
-        constexpr float p_shift = kPShift<DT>;
+        auto arrive = [&](int id) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(id));
+        };
+        // fp16: dX times x_mul over P's factor; x_undo takes dX's factor out again
         float x_mul = 1.0f, x_undo = CAP ? 4.0f : 1.0f;  // capped: 1 - tanh^2 = 4 r (1 - r), bf16 leaves the 4 for the end
         if constexpr (DT == 0) {
             const unsigned bits = __ldg(p.amax);
             // 2^-e with 2^(e-1) <= largest |dO| < 2^e, kept where both 2^e and 2^-e are normal; 1 for 0, inf, NaN
             int e = static_cast<int>(bits >> 23) - 126;
             e = bits == 0 || bits >= 0x7F800000u ? 0 : min(max(e, -100), 100);
-            x_mul = exp2f(static_cast<float>(-e) + 4.0f - p_shift) * x_undo;  // the capped 4 goes in here
+            x_mul = exp2f(static_cast<float>(-e) + 4.0f - kPShift<DT>) * x_undo;  // the capped 4 goes in here
             x_undo = exp2f(static_cast<float>(e) - 4.0f);
         }
-        float row_nlse = -INFINITY, row_ndelta = 0.0f;
-        float2 eps[2] = {splat2(0.0f), splat2(0.0f)};  // dQ: this warpgroup's part of e (times P's factor)
-        if constexpr (!DKV) {
-            const int i = x0 + r;
-            if (i < p.mask.Sq) {
-                const float *rows = p.rows + ((static_cast<int64_t>(b) * p.H + head) * p.nqb + i / CF::BN) * 2 * CF::BN +
-                                    i % CF::BN;
-                row_nlse = rows[0];
-                row_ndelta = rows[CF::BN];
-            }
-        }
+        constexpr float p_undo = DT == 0 ? 1.0f / 1024.0f : 1.0f;
+        uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 1024);
+        uint32_t g = 0, busy = 0;  // blocks and tiles with blocks so far
+        int st = 0;
+        uint32_t ph = 0;
+        int4 tl;
         bool ok = true;
-        int yb = y_first, yh = DKV ? head * p.group : 0;  // block and head of step n
-        auto advance = [&]() {
-            if (++yb == y_first + y_count) {
-                yb = y_first;
-                ++yh;
+        for (int t = 0; ok && take_tile(t, &tl); ++t) {
+            const int b = tl.y / heads, head = tl.y - b * heads, x0 = tl.x;
+            const int row = x0 + r;
+            const int n_total = DKV ? tl.w * p.group : tl.w;
+            int2 seen = make_int2(0, 0);                   // dQ: the row's interval
+            float row_nlse = -INFINITY, row_ndelta = 0.0f;
+            float2 eps = splat2(0.0f);                     // dQ: this thread's part of e (times P's factor)
+            float *row_stats = nullptr;
+            if constexpr (!DKV) {
+                if (row < p.mask.Sq) {
+                    const int64_t block = static_cast<int64_t>(x0 / CF::BN);
+                    const int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + block) * 3 * CF::BN + r;
+                    seen = make_int2(iv[0], iv[CF::BN]);
+                    row_stats = p.rows + ((static_cast<int64_t>(b) * p.H + head) * p.nqb + block) * 2 * CF::BN + r;
+                    row_nlse = row_stats[0];
+                    row_ndelta = row_stats[CF::BN];
+                }
             }
-        };
-        if (wg && n_total > 0)
-            advance();
-        float slope2 = 0.0f;
-        if constexpr (BIAS && !DKV)
-            slope2 = p.score.slopes[head] * 1.4426950408889634f;
-        for (int n = wg; n < n_total; n += 2) {
-            const int st = n % STAGES;
-            int4 rg = make_int4(0, 0, 0, 0);
-            if constexpr (DKV) {
-                rg = __ldg(p.ranges + static_cast<int64_t>(b) * p.nqb + yb);
-                if constexpr (BIAS)
-                    slope2 = __ldg(p.score.slopes + yh) * 1.4426950408889634f;
-                // the info beside the stage's tiles: seen through the copy's own barrier
-                if (!(ok = wait_warp(CF::BAR_YF + st, static_cast<uint32_t>(n / STAGES) & 1u)))
+            float slope2 = 0.0f;
+            if constexpr (BIAS && !DKV)
+                slope2 = __ldg(p.score.slopes + head) * 1.4426950408889634f;
+            int yb = tl.z, yh = head * p.group;  // block, and DKV: head
+            for (int n = 0; n < n_total; ++n, ++g) {
+                int4 rg = make_int4(0, 0, 0, 0);
+                if constexpr (DKV) {
+                    rg = __ldg(p.ranges + static_cast<int64_t>(b) * p.nqb + yb);
+                    if constexpr (BIAS)
+                        slope2 = __ldg(p.score.slopes + yh) * 1.4426950408889634f;
+                    // what lies beside the stage's tiles is seen through the copy's own barrier
+                    if (!(ok = wait_warp(CF::BAR_YF + st, ph)))
+                        break;
+                }
+                const int set = static_cast<int>(g % CF::S_SETS);
+                if (!(ok = wait_warp(CF::BAR_SF + set, g / CF::S_SETS)))
                     break;
+                tc_fence_after_sync();
+                const uint32_t s_addr = s_addr0 + 128 * static_cast<uint32_t>(set);
+                uint32_t sv[HN];
+                tmem_load_32cols(s_addr, sv);
+                // DKV: -lse, -delta, first key, end key and "sees more than one key" of the block's queries
+                const float4 *info = reinterpret_cast<const float4 *>(smem + CF::OFF_Y + st * CF::STAGE_BYTES +
+                                                                      2 * CF::TILE_BYTES) + group * (HN / 4);
+                const int4 *iv = reinterpret_cast<const int4 *>(info + 2 * CF::BN / 4);
+                const float4 *many = info + 4 * CF::BN / 4;
+                const int y0 = yb * CF::BN + HN * group;  // the thread's first column
+                // |p_i - j|: the column's step away from the first column's distance
+                const float dist0 = DKV ? static_cast<float>(p.mask.q_offset + y0 - row)
+                                        : static_cast<float>(p.mask.q_offset + row - y0);
+                const int nlo = seen.x - y0, nhi = seen.y - y0;  // dQ
+                bool whole = DKV ? rg.z <= x0 && rg.w >= x0 + CF::BM : nlo <= 0 && nhi >= HN;
+                whole = __all_sync(0xffffffffu, whole);
+                tmem_load_wait();
+                float2 w[HN / 2];        // P
+                float2 c[CAP ? HN / 2 : 1];  // a quarter of 1 - tanh^2
+                // scores to P; only blocks that cut an interval are masked
+                auto weights = [&](auto masked) {
+                    constexpr bool MASKED = decltype(masked)::value;
+#pragma unroll
+                    for (int e = 0; e < HN; e += 4) {
+                        float4 l4 = make_float4(row_nlse, row_nlse, row_nlse, row_nlse);
+                        int4 lo4 = make_int4(0, 0, 0, 0), hi4 = lo4;
+                        if constexpr (DKV) {
+                            l4 = info[e / 4];
+                            if constexpr (MASKED) {
+                                lo4 = iv[e / 4];
+                                hi4 = iv[CF::BN / 4 + e / 4];
+                            }
+                        }
+#pragma unroll
+                        for (int h = 0; h < 4; h += 2) {
+                            const int i = e + h;
+                            const float2 s = make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+                            const float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+                            float2 x;
+                            if constexpr (CAP) {
+                                const float2 q = cap_reciprocals(s, p.score.cap_arg);
+                                x = ffma2(q, splat2(-2.0f * p.score.cap_log2), fadd2(nl, splat2(p.score.cap_log2)));
+                                c[i / 2] = ffma2(make_float2(-q.x, -q.y), q, q);
+                            } else {
+                                x = ffma2(s, splat2(p.score.scale_log2), nl);
+                            }
+                            if constexpr (BIAS) {
+                                const float f = static_cast<float>(i);
+                                const float2 dist = DKV ? fadd2(splat2(dist0), make_float2(f, f + 1.0f))
+                                                        : fadd2(splat2(dist0), make_float2(-f, -f - 1.0f));
+                                x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
+                            }
+                            float2 v = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
+                            if constexpr (MASKED && DKV) {
+                                v.x = row >= (h ? lo4.z : lo4.x) && row < (h ? hi4.z : hi4.x) ? v.x : 0.0f;
+                                v.y = row >= (h ? lo4.w : lo4.y) && row < (h ? hi4.w : hi4.y) ? v.y : 0.0f;
+                            } else if constexpr (MASKED) {
+                                v.x = i >= nlo && i < nhi ? v.x : 0.0f;
+                                v.y = i + 1 >= nlo && i + 1 < nhi ? v.y : 0.0f;
+                            }
+                            w[i / 2] = v;
+                            if constexpr (CAP && !DKV)
+                                v = fmul2(v, c[i / 2]);
+                            sv[i / 2] = pack2<DT>(v.x, v.y);
+                        }
+                    }
+                };
+                if (whole)
+                    weights(std::false_type{});
+                else
+                    weights(std::true_type{});
+                // over the first half of the columns this thread read itself (others may still read theirs)
+                tmem_store_16cols(s_addr, sv);
+                tmem_store_wait();
+                arrive(CF::BAR_PF + set);
+                if (!(ok = wait_warp(CF::BAR_DPF, g)))
+                    break;
+                tc_fence_after_sync();
+                // dP to dX, 16 columns at a time
+                uint32_t dx[HN / 2];
+                auto gradients = [&](auto masked) {
+                    constexpr bool MASKED = decltype(masked)::value;
+#pragma unroll
+                    for (int e0 = 0; e0 < HN; e0 += 16) {
+                        uint32_t dp[16];
+                        tmem_load_16cols(dp_addr + e0, dp);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            float4 d4 = make_float4(row_ndelta, row_ndelta, row_ndelta, row_ndelta);
+                            float4 m4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                            if constexpr (DKV) {
+                                d4 = info[(CF::BN + e0 + e) / 4];
+                                if constexpr (MASKED)
+                                    m4 = many[(e0 + e) / 4];
+                            }
+#pragma unroll
+                            for (int h = 0; h < 4; h += 2) {
+                                const int i = e0 + e + h;
+                                const float2 nd = h ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
+                                float2 v = fadd2(make_float2(__uint_as_float(dp[e + h]), __uint_as_float(dp[e + h + 1])), nd);
+                                if constexpr (MASKED && DKV)  // a query that sees one key gets dX = 0 exactly
+                                    v = fmul2(v, h ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
+                                v = fmul2(v, w[i / 2]);
+                                if constexpr (!DKV)
+                                    eps = fadd2(eps, v);
+                                if constexpr (CAP)
+                                    v = fmul2(v, c[i / 2]);
+                                if constexpr (DT == 0)
+                                    v = fmul2(v, splat2(x_mul));
+                                dx[i / 2] = pack2<DT>(v.x, v.y);
+                            }
+                        }
+                    }
+                };
+                if (!DKV || whole)
+                    gradients(std::false_type{});
+                else
+                    gradients(std::true_type{});
+                tmem_store_16cols(dp_addr, dx);
+                tmem_store_wait();
+                arrive(CF::BAR_DXF);
+                if (++yb == tl.z + tl.w) {
+                    yb = tl.z;
+                    ++yh;
+                }
+                if (++st == STAGES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
             }
-            if (!(ok = wait_warp(CF::BAR_SF + wg, static_cast<uint32_t>(n >> 1) & 1u)))
+            // all products of the tile complete, then the sums out
+            if (ok && n_total > 0)
+                ok = wait_warp(CF::BAR_ACCF, busy);
+            float e_row = 0.0f;  // dQ: the row's e
+            if constexpr (!DKV) {
+                if (ok) {
+                    float *parts = eps_smem + (t & 1) * 512;
+                    parts[group * 128 + r] = eps.x + eps.y;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(CF::BAR_EPS));
+                    ok = wait_warp(CF::BAR_EPS, static_cast<uint32_t>(t));
+                    e_row = ((parts[r] + parts[128 + r]) + (parts[256 + r] + parts[384 + r])) * p_undo;
+                }
+            }
+            if (!ok)
                 break;
             tc_fence_after_sync();
-            uint32_t sv[HN], dp[HN];
-            tmem_load_32cols(s_addr + HN * half, sv);
-            tmem_load_32cols(dp_addr + HN * half, dp);
-            // DKV: -lse, -delta, first key, end key and "sees more than one key" of the block's queries
-            const float4 *info = reinterpret_cast<const float4 *>(smem + CF::OFF_Y + st * CF::STAGE_BYTES + 2 * CF::Y_BYTES) +
-                                 half * (HN / 4);
-            const int4 *iv = reinterpret_cast<const int4 *>(info + 2 * CF::BN / 4);
-            const float4 *many = info + 4 * CF::BN / 4;
-            // |p_i - j|: the column's step away from the first column's distance
-            const int y0 = yb * CF::BN + HN * half;  // the thread's first column
-            const float dist0 = DKV ? static_cast<float>(p.mask.q_offset + y0 - (x0 + r))
-                                    : static_cast<float>(p.mask.q_offset + x0 + r - y0);
-            const int key = x0 + r;                             // DKV
-            const int nlo = seen.x - y0, nhi = seen.y - y0;     // dQ
-            bool whole = DKV ? rg.z <= x0 && rg.w >= x0 + CF::BM : nlo <= 0 && nhi >= HN;
-            whole = __all_sync(0xffffffffu, whole);
-            tmem_load_wait();
-            // scores and dP to P and dX, in place and packed in pairs; only blocks that cut an interval are masked
-            auto block = [&](auto masked) {
-                constexpr bool MASKED = decltype(masked)::value;
-#pragma unroll
-                for (int e = 0; e < HN; e += 4) {
-                    float4 l4 = make_float4(row_nlse, row_nlse, row_nlse, row_nlse);
-                    float4 d4 = make_float4(row_ndelta, row_ndelta, row_ndelta, row_ndelta);
-                    float4 m4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-                    int4 lo4 = make_int4(0, 0, 0, 0), hi4 = lo4;
-                    if constexpr (DKV) {
-                        l4 = info[e / 4];
-                        d4 = info[CF::BN / 4 + e / 4];
-                        if constexpr (MASKED) {
-                            lo4 = iv[e / 4];
-                            hi4 = iv[CF::BN / 4 + e / 4];
-                            m4 = many[e / 4];
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; c += 2) {
-                        const float2 s = make_float2(__uint_as_float(sv[e + c]), __uint_as_float(sv[e + c + 1]));
-                        const float2 nl = c ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
-                        const float2 nd = c ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
-                        float2 x, cap_r;
-                        if constexpr (CAP) {
-                            cap_r = cap_reciprocals(s, p.score.cap_arg);
-                            x = ffma2(cap_r, splat2(-2.0f * p.score.cap_log2), fadd2(nl, splat2(p.score.cap_log2)));
-                        } else {
-                            x = ffma2(s, splat2(p.score.scale_log2), nl);
-                        }
-                        if constexpr (BIAS) {
-                            const float f = static_cast<float>(e + c);
-                            const float2 dist = DKV ? fadd2(splat2(dist0), make_float2(f, f + 1.0f))
-                                                    : fadd2(splat2(dist0), make_float2(-f, -f - 1.0f));
-                            x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
-                        }
-                        float2 w = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
-                        const float2 dpv = make_float2(__uint_as_float(dp[e + c]), __uint_as_float(dp[e + c + 1]));
-                        float2 g;
-                        if constexpr (MASKED && DKV) {
-                            w.x = key >= (c ? lo4.z : lo4.x) && key < (c ? hi4.z : hi4.x) ? w.x : 0.0f;
-                            w.y = key >= (c ? lo4.w : lo4.y) && key < (c ? hi4.w : hi4.y) ? w.y : 0.0f;
-                            // a query that sees one key gets dX = 0 exactly
-                            const float2 m = c ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y);
-                            g = fmul2(fadd2(dpv, nd), m);
-                        } else {
-                            if constexpr (MASKED) {
-                                w.x = e + c >= nlo && e + c < nhi ? w.x : 0.0f;
-                                w.y = e + c + 1 >= nlo && e + c + 1 < nhi ? w.y : 0.0f;
-                            }
-                            g = fadd2(dpv, nd);
-                        }
-                        float2 ds = fmul2(w, g);
-                        if constexpr (!DKV)
-                            eps[c / 2] = fadd2(eps[c / 2], ds);
-                        if constexpr (CAP) {
-                            const float2 t = ffma2(make_float2(-cap_r.x, -cap_r.y), cap_r, cap_r);
-                            ds = fmul2(ds, t);
-                            if constexpr (!DKV)
-                                w = fmul2(w, t);
-                        }
-                        if constexpr (DT == 0)
-                            ds = fmul2(ds, splat2(x_mul));
-                        sv[(e + c) / 2] = pack2<DT>(w.x, w.y);
-                        dp[(e + c) / 2] = pack2<DT>(ds.x, ds.y);
-                    }
-                }
-            };
-            if (whole)
-                block(std::false_type{});
-            else
-                block(std::true_type{});
-            // over the first half of the columns this thread read itself (the other warpgroup may still read its own)
-            tmem_store_16cols(s_addr + HN * half, sv);
-            tmem_store_16cols(dp_addr + HN * half, dp);
-            tmem_store_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar(CF::BAR_PF + wg));
-            advance();
-            if (n + 1 < n_total)
-                advance();
-        }
-        // all products complete, then the sums out
-        if (ok && n_total > 0)
-            ok = wait_warp(CF::BAR_DRAIN, 0);
-        float e_row = 0.0f;  // dQ: the row's e
-        if constexpr (!DKV) {
-            float *eps_smem = reinterpret_cast<float *>(smem + CF::OFF_EPS);
-            const float2 mine = fadd2(eps[0], eps[1]);
-            eps_smem[group * 128 + r] = mine.x + mine.y;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar(CF::BAR_EPS));
-            ok = ok && wait_warp(CF::BAR_EPS, 0);
-            if (ok)
-                e_row = ((eps_smem[r] + eps_smem[128 + r]) + (eps_smem[256 + r] + eps_smem[384 + r])) *
-                        (DT == 0 ? 1.0f / 1024.0f : 1.0f);
-        }
-        if (ok) {
-            tc_fence_after_sync();
-            const int row = x0 + r;
-            const bool live = row < (DKV ? p.mask.Sk : p.mask.Sq);
-            constexpr float p_undo = DT == 0 ? 1.0f / 1024.0f : 1.0f;
-            // DKV: buffer 0's warpgroups write dK, buffer 1's dV, half the columns each; dQ: a quarter each
-            uint16_t *out = DKV && wg ? p.out1 : p.out0;  // (batch, head, row) strides below
-            const int64_t *sd = DKV && wg ? p.s1 : p.s0;
-            const float mul = DKV && wg ? p_undo : p.scale * x_undo;
-            out += b * sd[0] + head * sd[1] + static_cast<int64_t>(row) * sd[2];
+            // DKV: two warpgroups write dK, two dV, half the columns each; dQ: a quarter each
+            const bool second = DKV && (group & 1);
+            const CUtensorMap *map_out = second ? &map_out1 : &map_out0;
+            const float mul = second ? p_undo : p.scale * x_undo;
             const uint32_t acc0 = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_A0);
-            const uint32_t acc = DKV && wg ? acc0 : tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_A1);
+            const uint32_t acc = second ? acc0 : tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_A1);
             const float e_mul = -e_row * p.scale * p_undo * (CAP ? 4.0f : 1.0f);
             const bool none = n_total == 0 || (!DKV && seen.y - seen.x <= 1);  // nothing comes through
             if constexpr (!DKV) {
-                if (group == 0 && live)
-                    p.rows[((static_cast<int64_t>(b) * p.H + head) * p.nqb + row / CF::BN) * 2 * CF::BN + CF::BN +
-                           row % CF::BN] = row_ndelta - e_row;
+                if (group == 0 && row_stats)
+                    row_stats[CF::BN] = row_ndelta - e_row;
             }
-            const int c0 = DKV ? half * (D / 32) : group * (D / 64), c1 = c0 + (DKV ? D / 32 : D / 64);  // of 16 columns
+            const int c0 = DKV ? (group >> 1) * (D / 32) : group * (D / 64), c1 = c0 + (DKV ? D / 32 : D / 64);  // of 16 columns
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
+            for (int cc = c0; cc < c1; ++cc) {
                 uint32_t o[16];
                 if (n_total > 0) {
-                    tmem_load_16cols(acc + 16 * c, o);
+                    tmem_load_16cols(acc + 16 * cc, o);
                     if constexpr (!DKV) {
                         uint32_t o0[16];
-                        tmem_load_16cols(acc0 + 16 * c, o0);
+                        tmem_load_16cols(acc0 + 16 * cc, o0);
                         tmem_load_wait();
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
@@ -649,34 +777,49 @@ __global__ void __launch_bounds__(640, 1)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * mul);
                     }
                 }
+                if (cc + 1 == c1 && n_total > 0)
+                    arrive(CF::BAR_ACCE);  // in registers: the next tile's sums may begin
                 if (none) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         o[e] = 0;
                 }
-                if (live) {
+                // 32 rows x 16 columns through this warp's buffer; rows behind the tensor's are not written
+                if (lane == 0)
+                    bulk_wait_group_read<0>();
+                __syncwarp();
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        uint4 w;
-                        w.x = pack2<DT>(__uint_as_float(o[8 * v]), __uint_as_float(o[8 * v + 1]));
-                        w.y = pack2<DT>(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3]));
-                        w.z = pack2<DT>(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5]));
-                        w.w = pack2<DT>(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7]));
-                        reinterpret_cast<uint4 *>(out + 16 * c)[v] = w;
-                    }
+                for (int v = 0; v < 2; ++v) {
+                    uint4 x;
+                    x.x = pack2<DT>(__uint_as_float(o[8 * v]), __uint_as_float(o[8 * v + 1]));
+                    x.y = pack2<DT>(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3]));
+                    x.z = pack2<DT>(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5]));
+                    x.w = pack2<DT>(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7]));
+                    out_buf[2 * lane + v] = x;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_4d(map_out, smem_addr(out_buf), 16 * cc, x0 + (warp & 3) * 32, head, b);
+                    bulk_commit_group();
                 }
             }
+            if (n_total > 0)
+                ++busy;
         }
+        if (lane == 0)
+            bulk_wait_group<0>();
+        __syncwarp();
     }
 
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 0 && lane == 0 && *abort_flag) {
-        if (x_issued)
-            wait_drain(bar(CF::BAR_X), 0, timeout);
+        if (issued & 1u)
+            wait_drain(bar(CF::BAR_XF), parity & 1u, timeout);
         for (int s = 0; s < STAGES; ++s)
-            if (y_issued & (1u << s))
-                wait_drain(bar(CF::BAR_YF + s), (y_par >> s) & 1u, timeout);
+            if (issued & (256u << s))
+                wait_drain(bar(CF::BAR_YF + s), (parity >> (8 + s)) & 1u, timeout);
     }
     __syncthreads();
     tc_fence_after_sync();

@@ -39,9 +39,9 @@ inline tl_status take_strides(const int64_t given[3], const int64_t sizes[3], in
 }
 
 // 16-bit tensor of `rank` dimensions (innermost first; strides in elements of
-// dimensions 1..rank-1), 128-byte swizzle; what lies outside reads as zero.
+// dimensions 1..rank-1), 128-byte swizzle or none; what lies outside reads as zero.
 inline bool encode_rows(CUtensorMap *map, const void *base, int dtype, int rank, const int64_t *dims,
-                        const int64_t *strides, const int *box)
+                        const int64_t *strides, const int *box, bool swizzle = true)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn)
@@ -57,7 +57,8 @@ inline bool encode_rows(CUtensorMap *map, const void *base, int dtype, int rank,
     }
     const CUtensorMapDataType dt = dtype == TL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     return fn(map, dt, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, bx, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -69,6 +70,16 @@ inline bool encode_heads(CUtensorMap *map, const void *base, int dtype, int64_t 
     const int64_t strides[3] = {st.s[2], st.s[1], st.s[0]};
     const int box[4] = {64, box_rows, 1, 1};
     return encode_rows(map, base, dtype, 4, dims, strides, box);
+}
+
+// The same tensor for stores of `box_cols` values of `box_rows` rows, rows side by side in shared memory
+inline bool encode_heads_out(CUtensorMap *map, const void *base, int dtype, int64_t batch, int64_t heads, int64_t rows,
+                             int64_t dim, const Strides &st, int box_rows, int box_cols)
+{
+    const int64_t dims[4] = {dim, rows, heads, batch};
+    const int64_t strides[3] = {st.s[2], st.s[1], st.s[0]};
+    const int box[4] = {box_cols, box_rows, 1, 1};
+    return encode_rows(map, base, dtype, 4, dims, strides, box, false);
 }
 
 // A launch whose set-up may overlap the previous kernel on the stream (the
