@@ -79,12 +79,16 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     if ((st = ready_kernel(d, dkv, e.smem, e.launch_regs)) != TL_OK ||
         (st = ready_kernel(d, dq, e.smem, e.launch_regs)) != TL_OK)
         return st;
-    // one box of 128 rows serves both passes
-    CUtensorMap tk, tv, tq, tdo, out_q, out_k, out_v;
+    // tiles of 128 rows and blocks of 64: dK and dV hold the keys, dQ the queries
+    CUtensorMap tk, tv, tq, tdo, bk, bv, bq, bdo, out_q, out_k, out_v;
     if (!encode_heads(&tk, K, dtype, batch, c.kv_heads, seq_k, head_dim, c.k, 128) ||
         !encode_heads(&tv, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, 128) ||
         !encode_heads(&tq, Q, dtype, batch, heads, seq_q, head_dim, c.q, 128) ||
         !encode_heads(&tdo, dO, dtype, batch, heads, seq_q, head_dim, sdo, 128) ||
+        !encode_heads(&bk, K, dtype, batch, c.kv_heads, seq_k, head_dim, c.k, kBwdCols) ||
+        !encode_heads(&bv, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, kBwdCols) ||
+        !encode_heads(&bq, Q, dtype, batch, heads, seq_q, head_dim, c.q, kBwdCols) ||
+        !encode_heads(&bdo, dO, dtype, batch, heads, seq_q, head_dim, sdo, kBwdCols) ||
         !encode_heads_out(&out_q, dQ, dtype, batch, heads, seq_q, head_dim, sdq, 32, 16) ||
         !encode_heads_out(&out_k, dK, dtype, batch, c.kv_heads, seq_k, head_dim, sdk, 32, 16) ||
         !encode_heads_out(&out_v, dV, dtype, batch, c.kv_heads, seq_k, head_dim, sdv, 32, 16))
@@ -150,9 +154,9 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
                                  o0, o1, a);
     };
     if (st == TL_OK)
-        st = launch(dq, tq, tdo, tk, tv, out_q, out_q, pq.tiles * batch * heads, pq);
+        st = launch(dq, tq, tdo, bk, bv, out_q, out_q, pq.tiles * batch * heads, pq);
     if (st == TL_OK)
-        st = launch(dkv, tk, tv, tq, tdo, out_k, out_v, pk.tiles * batch * c.kv_heads, pk);
+        st = launch(dkv, tk, tv, bq, bdo, out_k, out_v, pk.tiles * batch * c.kv_heads, pk);
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == TL_OK)
         st = TL_ERR_CUDA;
     return st;

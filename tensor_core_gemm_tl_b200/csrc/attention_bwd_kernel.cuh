@@ -30,20 +30,25 @@
 // as 16-bit values over the scores they came from and feed the second products
 // from there; nothing of size queries x keys leaves the SM.
 //
-// Pipeline (a block is 128 x 128 scores): sixteen warps, 32 columns a thread, turn
-// S(n) into P(n) and dP(n) into dX(n) in two steps, written over the scores they
-// came from.  The products go out as dV(n), S(n + 1), dK(n), dP(n + 1): S(n + 1) is
-// there when dX(n) is done, and dP(n + 1) when P(n + 1) is.  With D = 128 Tensor
-// Memory is full (S, dP and the two sums are 512 columns), so S(n + 1) waits until
-// dV(n) has read P(n); with D = 64 S has two sets of columns and does not.  The
-// CTAs are persistent and take tiles from a counter; the next tile's operands load
-// while this one's sums leave through shared memory and TMA stores (stores of a
-// row a thread held up every other memory operation of the SM, the products'
+// Pipeline: a block is 128 x 64 scores; blocks alternate between two sets of
+// Tensor Memory columns (S and dP) and two teams of eight warps, 32 columns a
+// thread, so that one team's exponentials run beside the other's second step and
+// the products of both.  The products of a block go out as dV(n), dK(n), S(n + 2),
+// dP(n + 2): S(n + 2) takes the columns dV(n) has read P(n) from and dP(n + 2) those
+// of dX(n), each wait covered by the product in between.  (Blocks of 128 x 128 in
+// one set, which D = 128 leaves room for, need 2080 instead of 2800 clocks of
+// products a 128 x 128 but left warps and products waiting for one another:
+// 3300, and 5700 with capped scores.)
+//
+// The CTAs are persistent and take tiles from a counter; the next tile's operands
+// load while this one's sums leave through shared memory and TMA stores (stores
+// of a row a thread held up every other memory operation of the SM, the products'
 // issue included: 5000 clocks a tile).
 //
-// What bounds it: 4 products of 128 x 128 x D a block, 2048 clocks with D = 128
-// at 4096 multiply-adds a clock and SM, against one 2^x a score (1024 clocks;
-// 2.5 times that with capped scores).
+// What bounds it: 4 products of 128 x 64 x D a block, with D = 128 1024 clocks at
+// 4096 multiply-adds a clock and SM, 1400 as S and dP read 48 bytes of shared
+// memory operands for every 32 clocks' worth of products, against one 2^x a score
+// (512 clocks; 2.5 times that with capped scores).
 //
 // 16-bit range: bf16 takes P and dX as they are.  fp16 holds P times 2^10 and
 // dX times 2^4 over the power of two above the largest |dO| (P of long rows
@@ -57,7 +62,7 @@
 
 namespace tl {
 
-constexpr int kBwdCols = 128;  // rows and columns of a block of scores
+constexpr int kBwdCols = 64;  // columns of a block of scores
 template <int DT>
 constexpr float kPShift = DT == 0 ? 10.0f : 0.0f;  // fp16 holds P times 2^10
 
@@ -65,12 +70,12 @@ struct AttnBwdParams {
     MaskParams mask;
     ScoreParams score;
     int32_t B, H, Hk, group;
-    int32_t nqb;               // blocks of 128 queries
+    int32_t nqb;               // blocks of 64 queries
     int32_t tiles;             // 128-row tiles of the keys (DKV) or of the queries
     float scale;               // softmax scale
-    float *rows;               // [B][H][nqb][2][128]: -lse in log2 units (-inf where the row sees nothing) plus the
+    float *rows;               // [B][H][nqb][2][64]: -lse in log2 units (-inf where the row sees nothing) plus the
                                // exponent of P's factor, -delta
-    const int32_t *intervals;  // [B][nqb][3][128]: first and end key of each query; 0.0f where it sees one key, else 1.0f
+    const int32_t *intervals;  // [B][nqb][3][64]: first and end key of each query; 0.0f where it sees one key, else 1.0f
     const int4 *ranges;        // [B][nqb]: least first, largest end, largest first, least end of the block's queries
     const unsigned *amax;      // fp16: bits of the largest |dO|, else null
     int32_t *next;             // counter that tiles are taken from, 0 at the start
@@ -90,7 +95,7 @@ struct AttnBwdRowsParams {
     int32_t *next;             // the two passes' tile counters
 };
 
-// One CTA (256 threads) per 128 queries of a head: 8 lanes a row.  Bound by
+// One CTA (256 threads) per 64 queries of a head: 8 lanes a row.  Bound by
 // reading O and dO once.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRowsParams p)
@@ -183,26 +188,26 @@ struct AttnBwdConfig {
     static constexpr int D = D_;
     static constexpr int BM = 128, BN = kBwdCols;
     static constexpr int D_ATOMS = D / 64;
-    static constexpr int ATOM = 128 * 128;  // bytes of 64 columns of a tile
-    static constexpr int TILE_BYTES = D_ATOMS * ATOM;
+    static constexpr int XATOM = BM * 128, YATOM = BN * 128;  // bytes of 64 columns
+    static constexpr int X_BYTES = D_ATOMS * XATOM, Y_BYTES = D_ATOMS * YATOM;
     static constexpr int ROWS_BYTES = 2 * BN * 4, INTERVAL_BYTES = 3 * BN * 4;  // of a block of queries
-    static constexpr int STAGES = D == 128 ? 2 : 4;
-    static constexpr int STAGE_BYTES = 2 * TILE_BYTES + 3072;  // Y1, Y2, rows, intervals
+    static constexpr int STAGES = 4;
+    static constexpr int STAGE_BYTES = 2 * Y_BYTES + 2048;  // Y1, Y2, rows, intervals
     static constexpr int OFF_X = 0;
-    static constexpr int OFF_Y = 2 * TILE_BYTES;
+    static constexpr int OFF_Y = 2 * X_BYTES;
     static constexpr int OFF_BAR = OFF_Y + STAGES * STAGE_BYTES;
     static constexpr int BAR_XF = 0, BAR_XE = 1, BAR_YF = 2, BAR_YE = 2 + STAGES;
     static constexpr int BAR_SF = 2 + 2 * STAGES;  // [set]: S in Tensor Memory
-    static constexpr int BAR_DPF = BAR_SF + 2;     // dP in Tensor Memory
-    static constexpr int BAR_PF = BAR_DPF + 1;     // [set]: P in Tensor Memory (16 warps arrive)
-    static constexpr int BAR_DXF = BAR_PF + 2;     // dX in Tensor Memory (16 warps)
-    static constexpr int BAR_PE = BAR_DXF + 1;     // [set]: P has been read
-    static constexpr int BAR_DXE = BAR_PE + 2;     // dX has been read
-    static constexpr int BAR_ACCF = BAR_DXE + 1;   // a tile's sums are complete
+    static constexpr int BAR_DPF = BAR_SF + 2;     // [set]: dP in Tensor Memory
+    static constexpr int BAR_PF = BAR_DPF + 2;     // [set]: P in Tensor Memory (8 warps arrive)
+    static constexpr int BAR_DXF = BAR_PF + 2;     // [set]: dX in Tensor Memory (8 warps)
+    static constexpr int BAR_PE = BAR_DXF + 2;     // [set]: P has been read
+    static constexpr int BAR_DXE = BAR_PE + 2;     // [set]: dX has been read
+    static constexpr int BAR_ACCF = BAR_DXE + 2;   // a tile's sums are complete
     static constexpr int BAR_ACCE = BAR_ACCF + 1;  // and have been read (16 warps)
     static constexpr int BAR_EPS = BAR_ACCE + 1;   // dQ: the warpgroups' parts of e are in shared memory (16 warps)
     static constexpr int BAR_TF = BAR_EPS + 1;     // [slot]: a tile's description is in shared memory
-    static constexpr int BAR_TE = BAR_TF + 2;      // [slot]: and has been read (18: producer, MMA issuer, 16 warps)
+    static constexpr int BAR_TE = BAR_TF + 2;      // [slot]: and has been read (19: producer, two MMA issuers, 16 warps)
     static constexpr int BAR_DRAIN = BAR_TE + 2;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
@@ -213,10 +218,10 @@ struct AttnBwdConfig {
     static constexpr int THREADS = 640;  // 4 control warps, 4 warpgroups for P and dX
     static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 104;
     static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 512 * REGS_SOFTMAX + THREADS - 1) / THREADS;
-    static constexpr int S_SETS = D == 128 ? 1 : 2;  // sets of columns S alternates between
-    static constexpr int TMEM_S = 0, TMEM_DP = 128 * S_SETS, TMEM_A0 = TMEM_DP + 128, TMEM_A1 = TMEM_A0 + D;
+    // Tensor Memory columns: S and dP of set w at 64 w beyond these, the sums
+    static constexpr int TMEM_S = 0, TMEM_DP = 128, TMEM_A0 = 256, TMEM_A1 = 256 + D;
     static_assert(TMEM_A1 + D <= 512, "Tensor Memory columns");
-    static_assert(ROWS_BYTES + INTERVAL_BYTES <= 3072 && SMEM_BYTES <= 232448, "shared memory");
+    static_assert(ROWS_BYTES + INTERVAL_BYTES <= 2048 && SMEM_BYTES <= 232448, "shared memory");
 };
 
 // X1, X2: the CTA's 128 rows (K and V, or Q and dO); Y1, Y2: the blocks it runs
@@ -256,20 +261,20 @@ __global__ void __launch_bounds__(640, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(CF::BAR_SF + i), 1);
-            mbar_init(bar(CF::BAR_PF + i), 16);
+            mbar_init(bar(CF::BAR_DPF + i), 1);
+            mbar_init(bar(CF::BAR_PF + i), 8);
+            mbar_init(bar(CF::BAR_DXF + i), 8);
             mbar_init(bar(CF::BAR_PE + i), 1);
+            mbar_init(bar(CF::BAR_DXE + i), 1);
         }
-        mbar_init(bar(CF::BAR_DPF), 1);
-        mbar_init(bar(CF::BAR_DXF), 16);
-        mbar_init(bar(CF::BAR_DXE), 1);
         mbar_init(bar(CF::BAR_ACCF), 1);
         mbar_init(bar(CF::BAR_ACCE), 16);
         mbar_init(bar(CF::BAR_EPS), 16);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(CF::BAR_TF + i), 1);
-            mbar_init(bar(CF::BAR_TE + i), 18);
+            mbar_init(bar(CF::BAR_TE + i), 19);
         }
-        mbar_init(bar(CF::BAR_DRAIN), 1);
+        mbar_init(bar(CF::BAR_DRAIN), 2);
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -324,11 +329,11 @@ __global__ void __launch_bounds__(640, 1)
                 if (lane == 0) {
                     ok = wait_bounded(bar(CF::BAR_XE), xph ^ 1u, abort_flag, timeout, ERR_PRODUCER);
                     if (ok) {
-                        mbar_arrive_expect_tx(bar(CF::BAR_XF), 2 * CF::TILE_BYTES);
+                        mbar_arrive_expect_tx(bar(CF::BAR_XF), 2 * CF::X_BYTES);
 #pragma unroll
                         for (int a = 0; a < CF::D_ATOMS; ++a) {
-                            tma_load_4d(sX + a * CF::ATOM, &map_x1, bar(CF::BAR_XF), 64 * a, tl.x, head, b);
-                            tma_load_4d(sX + CF::TILE_BYTES + a * CF::ATOM, &map_x2, bar(CF::BAR_XF), 64 * a, tl.x, head, b);
+                            tma_load_4d(sX + a * CF::XATOM, &map_x1, bar(CF::BAR_XF), 64 * a, tl.x, head, b);
+                            tma_load_4d(sX + CF::X_BYTES + a * CF::XATOM, &map_x2, bar(CF::BAR_XF), 64 * a, tl.x, head, b);
                         }
                         issued |= 1u;
                         parity = (parity & ~1u) | xph;
@@ -341,21 +346,21 @@ __global__ void __launch_bounds__(640, 1)
                             break;
                         const uint32_t full = bar(CF::BAR_YF + st);
                         const uint32_t dst = sY + st * CF::STAGE_BYTES;
-                        mbar_arrive_expect_tx(full, 2 * CF::TILE_BYTES + (DKV ? CF::ROWS_BYTES + CF::INTERVAL_BYTES : 0));
+                        mbar_arrive_expect_tx(full, 2 * CF::Y_BYTES + (DKV ? CF::ROWS_BYTES + CF::INTERVAL_BYTES : 0));
 #pragma unroll
                         for (int a = 0; a < CF::D_ATOMS; ++a)
-                            tma_load_4d(dst + a * CF::ATOM, &map_y1, full, 64 * a, yb * CF::BN, yh, b);
+                            tma_load_4d(dst + a * CF::YATOM, &map_y1, full, 64 * a, yb * CF::BN, yh, b);
                         if constexpr (DKV) {
-                            bulk_load_g2s(dst + 2 * CF::TILE_BYTES,
+                            bulk_load_g2s(dst + 2 * CF::Y_BYTES,
                                           p.rows + ((static_cast<int64_t>(b) * p.H + yh) * p.nqb + yb) * 2 * CF::BN,
                                           CF::ROWS_BYTES, full);
-                            bulk_load_g2s(dst + 2 * CF::TILE_BYTES + CF::ROWS_BYTES,
+                            bulk_load_g2s(dst + 2 * CF::Y_BYTES + CF::ROWS_BYTES,
                                           p.intervals + (static_cast<int64_t>(b) * p.nqb + yb) * 3 * CF::BN,
                                           CF::INTERVAL_BYTES, full);
                         }
 #pragma unroll
                         for (int a = 0; a < CF::D_ATOMS; ++a)
-                            tma_load_4d(dst + CF::TILE_BYTES + a * CF::ATOM, &map_y2, full, 64 * a, yb * CF::BN, yh, b);
+                            tma_load_4d(dst + CF::Y_BYTES + a * CF::YATOM, &map_y2, full, 64 * a, yb * CF::BN, yh, b);
                         issued |= 256u << st;
                         parity = (parity & ~(256u << st)) | (ph << (8 + st));
                         if (++yb == tl.z + tl.w) {
@@ -371,43 +376,46 @@ __global__ void __launch_bounds__(640, 1)
                 xph ^= 1u;
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             }
-        } else if (warp == 1) {
-            // ------------------------------------------------------------ MMA issuer
-            // the whole warp walks the loop and one elected lane issues: what the
-            // instructions are made from stays uniform across the warp
+        } else if (warp == 1 || warp == 3) {
+            // ------------------------------------------------------------ MMA issuers
+            // Warp 1 issues S and dP, warp 3 dV and dK: one's waits (some 150 clocks
+            // each even on a completed barrier) pass while the other's products
+            // run.  What one needs of the other comes through the barriers.  A
+            // whole warp walks the loop and one elected lane issues: what the
+            // instructions are made from stays uniform across the warp.
             constexpr uint32_t IDESC_1 = mma_idesc_f16(DT, 128, CF::BN, 0, 0);  // both K-major
             constexpr uint32_t IDESC_2 = mma_idesc_f16(DT, 128, D, 0, 1);       // A from Tensor Memory, Y N-major
             const uint64_t x_desc = smem_desc_sw128(sX, 16, 1024);
             const uint64_t y_desc = smem_desc_sw128(sY, 16, 1024);
-            const uint64_t yt_desc = smem_desc_sw128(sY, CF::ATOM, 1024);
-            // S (into set `set`) or dP of the block in stage `st` from X1, Y1 or X2, Y2
-            auto first_product = [&](int m, int st, int set, int done) {
+            const uint64_t yt_desc = smem_desc_sw128(sY, CF::YATOM, 1024);
+            // S (m = 0) or dP (m = 1) of the block in stage `st` into set `set`, from X1, Y1 or X2, Y2
+            auto first_product = [&](int m, int st, int set) {
                 if (elect_one()) {
-                    const uint64_t yd = y_desc + ((st * CF::STAGE_BYTES) >> 4);
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(m ? CF::TMEM_DP : CF::TMEM_S + 128 * set);
+                    const uint64_t yd = y_desc + ((st * CF::STAGE_BYTES + m * CF::Y_BYTES) >> 4);
+                    const uint64_t xd = x_desc + ((m * CF::X_BYTES) >> 4);
+                    const uint32_t d = tmem_base + static_cast<uint32_t>((m ? CF::TMEM_DP : CF::TMEM_S) + CF::BN * set);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t at = (m * CF::TILE_BYTES + (k >> 2) * CF::ATOM + (k & 3) * 32) >> 4;
-                        tc_mma_f16(d, x_desc + at, yd + at, IDESC_1, k != 0 ? 1u : 0u);
-                    }
-                    tc_commit(bar(done));
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_f16(d, xd + (((k >> 2) * CF::XATOM + (k & 3) * 32) >> 4),
+                                   yd + (((k >> 2) * CF::YATOM + (k & 3) * 32) >> 4), IDESC_1, k != 0 ? 1u : 0u);
+                    tc_commit(bar((m ? CF::BAR_DPF : CF::BAR_SF) + set));
                 }
                 __syncwarp();
             };
             // 16 values of P or dX take 8 columns; each 32 of the block's lie where their scores were
             auto p_col = [](int k) { return (k >> 1) * 32 + (k & 1) * 8; };
             // dV += P^T dO, or B += P c K (m = 0); dK += dX^T Q, or dQ += dX K (m = 1)
-            auto second_product = [&](int m, int st, int set, bool first, int done, int done2) {
+            auto second_product = [&](int m, int st, int set, bool first) {
                 if (elect_one()) {
-                    const uint64_t yd = yt_desc + ((st * CF::STAGE_BYTES + (DKV && m == 0 ? CF::TILE_BYTES : 0)) >> 4);
+                    const uint64_t yd = yt_desc + ((st * CF::STAGE_BYTES + (DKV && m == 0 ? CF::Y_BYTES : 0)) >> 4);
                     const uint32_t d = tmem_base + static_cast<uint32_t>(m ? CF::TMEM_A1 : CF::TMEM_A0);
-                    const uint32_t a = tmem_base + static_cast<uint32_t>(m ? CF::TMEM_DP : CF::TMEM_S + 128 * set);
+                    const uint32_t a = tmem_base + static_cast<uint32_t>((m ? CF::TMEM_DP : CF::TMEM_S) + CF::BN * set);
 #pragma unroll
                     for (int k = 0; k < CF::BN / 16; ++k)
                         tc_mma_f16_ts(d, a + p_col(k), yd + ((2048 * k) >> 4), IDESC_2, (!first || k > 0) ? 1u : 0u);
-                    tc_commit(bar(done));
-                    if (done2 >= 0)
-                        tc_commit(bar(done2));
+                    tc_commit(bar((m ? CF::BAR_DXE : CF::BAR_PE) + set));
+                    if (m)
+                        tc_commit(bar(CF::BAR_YE + st));
                 }
                 __syncwarp();
             };
@@ -419,62 +427,50 @@ __global__ void __launch_bounds__(640, 1)
                     tc_commit(bar(id));
                 __syncwarp();
             };
-            int st = 0;
-            uint32_t ph = 0, g = 0, busy = 0;  // g: blocks so far; busy: tiles with blocks so far
+            uint32_t g = 0, busy = 0;  // blocks and tiles with blocks so far
             int4 tl;
             bool ok = true;
+            // S and dP of block `blk`.  Every wait follows each phase of its barrier
+            // in turn, so no two phases can be mistaken.
+            auto issue_first = [&](uint32_t blk) {
+                const int st = static_cast<int>(blk % STAGES), set = static_cast<int>(blk & 1u);
+                if (!wait(CF::BAR_YF + st, blk / STAGES) || (blk >= 2 && !wait(CF::BAR_PE + set, (blk >> 1) - 1)))
+                    return false;
+                tc_fence_after_sync();
+                first_product(0, st, set);
+                if (blk >= 2 && !wait(CF::BAR_DXE + set, (blk >> 1) - 1))
+                    return false;
+                tc_fence_after_sync();
+                first_product(1, st, set);
+                return true;
+            };
             for (int t = 0; ok && take_tile(t, &tl); ++t) {
                 const int n_total = DKV ? tl.w * p.group : tl.w;
                 if (n_total == 0)
                     continue;
-                // g: block n of the tile; its stage st, S in set g % S_SETS
-                auto issue_s = [&](uint32_t block, int stage, uint32_t phase) {
-                    // every wait follows each phase of its barrier in turn, so no two phases can be mistaken
-                    const int set = static_cast<int>(block % CF::S_SETS);
-                    if (!wait(CF::BAR_YF + stage, phase) ||
-                        (block >= CF::S_SETS && !wait(CF::BAR_PE + set, block / CF::S_SETS - 1)))
-                        return false;
-                    tc_fence_after_sync();
-                    first_product(0, stage, set, CF::BAR_SF + set);
-                    return true;
-                };
-                auto issue_dp = [&](uint32_t block, int stage) {
-                    if (block > 0 && !wait(CF::BAR_DXE, block - 1))
-                        return false;
-                    tc_fence_after_sync();
-                    first_product(1, stage, 0, CF::BAR_DPF);
-                    return true;
-                };
-                ok = wait(CF::BAR_XF, busy) && issue_s(g, st, ph) && issue_dp(g, st);
-                if (ok && n_total == 1)
-                    commit(CF::BAR_XE);
-                for (int n = 0; ok && n < n_total; ++n, ++g) {
-                    const int st1 = st + 1 == STAGES ? 0 : st + 1;
-                    const uint32_t ph1 = st1 == 0 ? ph ^ 1u : ph;
-                    const int set = static_cast<int>(g % CF::S_SETS);
-                    const bool next = n + 1 < n_total;
-                    if (CF::S_SETS > 1 && next && !(ok = issue_s(g + 1, st1, ph1)))
-                        break;
-                    // the last tile's sums have been read before this one's begin
-                    if (!(ok = wait(CF::BAR_PF + set, g / CF::S_SETS)) || (n == 0 && busy > 0 && !(ok = wait(CF::BAR_ACCE, busy - 1))))
-                        break;
-                    tc_fence_after_sync();
-                    second_product(0, st, set, n == 0, CF::BAR_PE + set, -1);
-                    if (CF::S_SETS == 1 && next && !(ok = issue_s(g + 1, st1, ph1)))
-                        break;
-                    if (!(ok = wait(CF::BAR_DXF, g)))
-                        break;
-                    tc_fence_after_sync();
-                    second_product(1, st, 0, n == 0, CF::BAR_DXE, CF::BAR_YE + st);
-                    if (next && !(ok = issue_dp(g + 1, st1)))
-                        break;
-                    if (n + 2 == n_total)
+                if (warp == 1) {
+                    ok = wait(CF::BAR_XF, busy);
+                    for (int n = 0; ok && n < n_total; ++n, ++g)
+                        ok = issue_first(g);
+                    if (ok)
                         commit(CF::BAR_XE);
-                    st = st1;
-                    ph = ph1;
+                } else {
+                    for (int n = 0; ok && n < n_total; ++n, ++g) {
+                        const int st = static_cast<int>(g % STAGES), set = static_cast<int>(g & 1u);
+                        // the last tile's sums have been read before this one's begin
+                        if (!(ok = wait(CF::BAR_PF + set, g >> 1)) ||
+                            (n == 0 && busy > 0 && !(ok = wait(CF::BAR_ACCE, busy - 1))))
+                            break;
+                        tc_fence_after_sync();
+                        second_product(0, st, set, n == 0);
+                        if (!(ok = wait(CF::BAR_DXF + set, g >> 1)))
+                            break;
+                        tc_fence_after_sync();
+                        second_product(1, st, set, n == 0);
+                    }
+                    if (ok)
+                        commit(CF::BAR_ACCF);
                 }
-                if (ok)
-                    commit(CF::BAR_ACCF);
                 ++busy;
             }
             commit(CF::BAR_DRAIN);
@@ -512,9 +508,12 @@ __global__ void __launch_bounds__(640, 1)
                         first = __reduce_min_sync(0xffffffffu, first);
                         end = __reduce_max_sync(0xffffffffu, end);
                     } else {
-                        const int4 v = __ldg(rg + tile);  // the blocks of keys that some query of the tile sees
-                        first = v.x / CF::BN;
-                        end = (v.y + CF::BN - 1) / CF::BN;
+                        // the blocks of keys that some query of the tile sees
+                        for (int q = tile * (CF::BM / CF::BN); q < min(p.nqb, (tile + 1) * (CF::BM / CF::BN)); ++q) {
+                            const int4 v = __ldg(rg + q);
+                            first = min(first, v.x / CF::BN);
+                            end = max(end, (v.y + CF::BN - 1) / CF::BN);
+                        }
                     }
                     tl = make_int4(x0, bh, first, end > first ? end - first : 0);
                 }
@@ -530,11 +529,12 @@ __global__ void __launch_bounds__(640, 1)
         regs_increase<CF::REGS_SOFTMAX>();
         // ------------------------------------------------------------ P and dX: one row and 32 columns a thread
         constexpr int HN = 32;
-        const int group = (warp - 4) >> 2;         // which 32 columns
+        const int group = (warp - 4) >> 2;         // warpgroup: its team (and set) and which 32 of the 64 columns
+        const int team = group & 1, half = group >> 1;
         const int r = (warp & 3) * 32 + lane;      // row of the tile (Tensor Memory lane)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_addr0 = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + HN * group);
-        const uint32_t dp_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_DP + HN * group);
+        const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + CF::BN * team + HN * half);
+        const uint32_t dp_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_DP + CF::BN * team + HN * half);
         auto wait_warp = [&](int id, uint32_t par) -> bool {
             return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_EPILOGUE));
         };
@@ -556,9 +556,7 @@ __global__ void __launch_bounds__(640, 1)
         }
         constexpr float p_undo = DT == 0 ? 1.0f / 1024.0f : 1.0f;
         uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 1024);
-        uint32_t g = 0, busy = 0;  // blocks and tiles with blocks so far
-        int st = 0;
-        uint32_t ph = 0;
+        uint32_t g0 = 0, busy = 0;  // blocks and tiles with blocks so far
         int4 tl;
         bool ok = true;
         for (int t = 0; ok && take_tile(t, &tl); ++t) {
@@ -571,10 +569,10 @@ __global__ void __launch_bounds__(640, 1)
             float *row_stats = nullptr;
             if constexpr (!DKV) {
                 if (row < p.mask.Sq) {
-                    const int64_t block = static_cast<int64_t>(x0 / CF::BN);
-                    const int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + block) * 3 * CF::BN + r;
+                    const int64_t block = row / CF::BN;
+                    const int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + block) * 3 * CF::BN + row % CF::BN;
                     seen = make_int2(iv[0], iv[CF::BN]);
-                    row_stats = p.rows + ((static_cast<int64_t>(b) * p.H + head) * p.nqb + block) * 2 * CF::BN + r;
+                    row_stats = p.rows + ((static_cast<int64_t>(b) * p.H + head) * p.nqb + block) * 2 * CF::BN + row % CF::BN;
                     row_nlse = row_stats[0];
                     row_ndelta = row_stats[CF::BN];
                 }
@@ -582,30 +580,40 @@ __global__ void __launch_bounds__(640, 1)
             float slope2 = 0.0f;
             if constexpr (BIAS && !DKV)
                 slope2 = __ldg(p.score.slopes + head) * 1.4426950408889634f;
-            int yb = tl.z, yh = head * p.group;  // block, and DKV: head
-            for (int n = 0; n < n_total; ++n, ++g) {
+            // this team's blocks; where they lie, and DKV: in which head
+            const int n_first = static_cast<int>((static_cast<uint32_t>(team) - g0) & 1u);
+            int yb = tl.z + n_first, yh = head * p.group;
+            auto carry = [&]() {
+                while (yb >= tl.z + tl.w) {
+                    yb -= tl.w;
+                    ++yh;
+                }
+            };
+            for (int n = n_first; n < n_total; n += 2, yb += 2) {
+                if constexpr (DKV)
+                    carry();
+                const uint32_t g = g0 + static_cast<uint32_t>(n);
+                const int st = static_cast<int>(g % STAGES);
                 int4 rg = make_int4(0, 0, 0, 0);
                 if constexpr (DKV) {
                     rg = __ldg(p.ranges + static_cast<int64_t>(b) * p.nqb + yb);
                     if constexpr (BIAS)
                         slope2 = __ldg(p.score.slopes + yh) * 1.4426950408889634f;
                     // what lies beside the stage's tiles is seen through the copy's own barrier
-                    if (!(ok = wait_warp(CF::BAR_YF + st, ph)))
+                    if (!(ok = wait_warp(CF::BAR_YF + st, g / STAGES)))
                         break;
                 }
-                const int set = static_cast<int>(g % CF::S_SETS);
-                if (!(ok = wait_warp(CF::BAR_SF + set, g / CF::S_SETS)))
+                if (!(ok = wait_warp(CF::BAR_SF + team, g >> 1)))
                     break;
                 tc_fence_after_sync();
-                const uint32_t s_addr = s_addr0 + 128 * static_cast<uint32_t>(set);
                 uint32_t sv[HN];
                 tmem_load_32cols(s_addr, sv);
                 // DKV: -lse, -delta, first key, end key and "sees more than one key" of the block's queries
                 const float4 *info = reinterpret_cast<const float4 *>(smem + CF::OFF_Y + st * CF::STAGE_BYTES +
-                                                                      2 * CF::TILE_BYTES) + group * (HN / 4);
+                                                                      2 * CF::Y_BYTES) + half * (HN / 4);
                 const int4 *iv = reinterpret_cast<const int4 *>(info + 2 * CF::BN / 4);
                 const float4 *many = info + 4 * CF::BN / 4;
-                const int y0 = yb * CF::BN + HN * group;  // the thread's first column
+                const int y0 = yb * CF::BN + HN * half;  // the thread's first column
                 // |p_i - j|: the column's step away from the first column's distance
                 const float dist0 = DKV ? static_cast<float>(p.mask.q_offset + y0 - row)
                                         : static_cast<float>(p.mask.q_offset + row - y0);
@@ -670,8 +678,8 @@ __global__ void __launch_bounds__(640, 1)
                 // over the first half of the columns this thread read itself (others may still read theirs)
                 tmem_store_16cols(s_addr, sv);
                 tmem_store_wait();
-                arrive(CF::BAR_PF + set);
-                if (!(ok = wait_warp(CF::BAR_DPF, g)))
+                arrive(CF::BAR_PF + team);
+                if (!(ok = wait_warp(CF::BAR_DPF + team, g >> 1)))
                     break;
                 tc_fence_after_sync();
                 // dP to dX, 16 columns at a time
@@ -717,16 +725,9 @@ __global__ void __launch_bounds__(640, 1)
                     gradients(std::true_type{});
                 tmem_store_16cols(dp_addr, dx);
                 tmem_store_wait();
-                arrive(CF::BAR_DXF);
-                if (++yb == tl.z + tl.w) {
-                    yb = tl.z;
-                    ++yh;
-                }
-                if (++st == STAGES) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+                arrive(CF::BAR_DXF + team);
             }
+            g0 += static_cast<uint32_t>(n_total);
             // all products of the tile complete, then the sums out
             if (ok && n_total > 0)
                 ok = wait_warp(CF::BAR_ACCF, busy);
