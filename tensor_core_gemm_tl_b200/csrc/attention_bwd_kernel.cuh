@@ -207,7 +207,7 @@ struct AttnBwdConfig {
     static constexpr int BAR_ACCE = BAR_ACCF + 1;  // and have been read (16 warps)
     static constexpr int BAR_EPS = BAR_ACCE + 1;   // dQ: the warpgroups' parts of e are in shared memory (16 warps)
     static constexpr int BAR_TF = BAR_EPS + 1;     // [slot]: a tile's description is in shared memory
-    static constexpr int BAR_TE = BAR_TF + 2;      // [slot]: and has been read (19: producer, two MMA issuers, 16 warps)
+    static constexpr int BAR_TE = BAR_TF + 2;      // [slot]: and has been read (19: three MMA issuers, 16 warps)
     static constexpr int BAR_DRAIN = BAR_TE + 2;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(640, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(bar(CF::BAR_XF), 1);
-        mbar_init(bar(CF::BAR_XE), 1);
+        mbar_init(bar(CF::BAR_XE), 2);  // S and dP of a tile complete
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(bar(CF::BAR_YF + s), 1);
             mbar_init(bar(CF::BAR_YE + s), 1);
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(640, 1)
             mbar_init(bar(CF::BAR_TF + i), 1);
             mbar_init(bar(CF::BAR_TE + i), 19);
         }
-        mbar_init(bar(CF::BAR_DRAIN), 2);
+        mbar_init(bar(CF::BAR_DRAIN), 3);
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -317,12 +317,64 @@ __global__ void __launch_bounds__(640, 1)
     if (warp < 4) {
         regs_decrease<CF::REGS_CONTROL>();
         if (warp == 0) {
-            // ------------------------------------------------------------ producer
+            // ------------------------------------------------------------ tiles and loads
+            // Takes tile t from the counter, works out which blocks it visits and
+            // leaves its description for the others.
+            auto next_tile = [&](int t, int4 *out) {
+                if (t >= 2 && !__all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_TE + (t & 1)),
+                                                                    static_cast<uint32_t>((t >> 1) - 1) & 1u, abort_flag,
+                                                                    timeout, ERR_PRODUCER)))
+                    return false;
+                int item = 0;
+                if (lane == 0)
+                    item = atomicAdd(p.next, 1);
+                item = __shfl_sync(0xffffffffu, item, 0);
+                int4 tl = make_int4(-1, 0, 0, 0);
+                if (item < items) {
+                    // causal: the heaviest tiles first (the first keys, the last queries); else one head's tiles together
+                    const int tile = p.mask.causal ? (DKV ? item / BH : p.tiles - 1 - item / BH) : item % p.tiles;
+                    const int bh = p.mask.causal ? item % BH : item / p.tiles;
+                    const int b = bh / heads, x0 = tile * CF::BM;
+                    const int4 *rg = p.ranges + static_cast<int64_t>(b) * p.nqb;
+                    int first = 0x7FFFFFFF, end = 0;
+                    if constexpr (DKV) {
+                        // the blocks of queries that see some key of the tile
+                        for (int q = lane; q < p.nqb; q += 32) {
+                            const int4 v = __ldg(rg + q);
+                            if (v.x < x0 + CF::BM && v.y > x0) {
+                                first = min(first, q);
+                                end = max(end, q + 1);
+                            }
+                        }
+                        first = __reduce_min_sync(0xffffffffu, first);
+                        end = __reduce_max_sync(0xffffffffu, end);
+                    } else {
+                        // the blocks of keys that some query of the tile sees
+                        for (int q = tile * (CF::BM / CF::BN); q < min(p.nqb, (tile + 1) * (CF::BM / CF::BN)); ++q) {
+                            const int4 v = __ldg(rg + q);
+                            first = min(first, v.x / CF::BN);
+                            end = max(end, (v.y + CF::BN - 1) / CF::BN);
+                        }
+                    }
+                    tl = make_int4(x0, bh, first, end > first ? end - first : 0);
+                }
+                if (lane == 0) {
+                    tile_slots[t & 1] = tl;
+                    mbar_arrive(bar(CF::BAR_TF + (t & 1)));
+                }
+                __syncwarp();
+                *out = tl;
+                return true;
+            };
             int st = 0;
             uint32_t ph = 0, xph = 0;
-            int4 tl;
-            bool ok = true;
-            for (int t = 0; ok && take_tile(t, &tl); ++t) {
+            int4 tl, after;
+            bool ok = next_tile(0, &after);
+            for (int t = 0; ok; ++t) {
+                tl = after;
+                // the next tile is taken before this one's loads wait for room
+                if (tl.x < 0 || !(ok = next_tile(t + 1, &after)))
+                    break;
                 if (tl.w == 0)
                     continue;
                 const int b = tl.y / heads, head = tl.y - b * heads;
@@ -376,13 +428,14 @@ __global__ void __launch_bounds__(640, 1)
                 xph ^= 1u;
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             }
-        } else if (warp == 1 || warp == 3) {
+        } else {
             // ------------------------------------------------------------ MMA issuers
-            // Warp 1 issues S and dP, warp 3 dV and dK: one's waits (some 150 clocks
-            // each even on a completed barrier) pass while the other's products
-            // run.  What one needs of the other comes through the barriers.  A
-            // whole warp walks the loop and one elected lane issues: what the
-            // instructions are made from stays uniform across the warp.
+            // Warp 1 issues S, warp 2 dP, warp 3 dV and dK: one's waits (some 150
+            // clocks each even on a completed barrier) pass while the others'
+            // products run (one issuer for all: 2350 clocks a block; two: 1750).
+            // What one needs of another comes through the barriers.  A whole warp
+            // walks the loop and one elected lane issues: what the instructions
+            // are made from stays uniform across the warp.
             constexpr uint32_t IDESC_1 = mma_idesc_f16(DT, 128, CF::BN, 0, 0);  // both K-major
             constexpr uint32_t IDESC_2 = mma_idesc_f16(DT, 128, D, 0, 1);       // A from Tensor Memory, Y N-major
             const uint64_t x_desc = smem_desc_sw128(sX, 16, 1024);
@@ -430,28 +483,24 @@ __global__ void __launch_bounds__(640, 1)
             uint32_t g = 0, busy = 0;  // blocks and tiles with blocks so far
             int4 tl;
             bool ok = true;
-            // S and dP of block `blk`.  Every wait follows each phase of its barrier
-            // in turn, so no two phases can be mistaken.
-            auto issue_first = [&](uint32_t blk) {
-                const int st = static_cast<int>(blk % STAGES), set = static_cast<int>(blk & 1u);
-                if (!wait(CF::BAR_YF + st, blk / STAGES) || (blk >= 2 && !wait(CF::BAR_PE + set, (blk >> 1) - 1)))
-                    return false;
-                tc_fence_after_sync();
-                first_product(0, st, set);
-                if (blk >= 2 && !wait(CF::BAR_DXE + set, (blk >> 1) - 1))
-                    return false;
-                tc_fence_after_sync();
-                first_product(1, st, set);
-                return true;
-            };
+            // Every wait follows each phase of its barrier in turn, so no two phases
+            // can be mistaken.
             for (int t = 0; ok && take_tile(t, &tl); ++t) {
                 const int n_total = DKV ? tl.w * p.group : tl.w;
                 if (n_total == 0)
                     continue;
-                if (warp == 1) {
+                if (warp < 3) {
+                    // S takes the columns that dV has read P of two blocks before from, dP those of dX
+                    const int m = warp - 1, free_bar = m ? CF::BAR_DXE : CF::BAR_PE;
                     ok = wait(CF::BAR_XF, busy);
-                    for (int n = 0; ok && n < n_total; ++n, ++g)
-                        ok = issue_first(g);
+                    for (int n = 0; ok && n < n_total; ++n, ++g) {
+                        const int st = static_cast<int>(g % STAGES), set = static_cast<int>(g & 1u);
+                        if (!(ok = wait(CF::BAR_YF + st, g / STAGES)) ||
+                            (g >= 2 && !(ok = wait(free_bar + set, (g >> 1) - 1))))
+                            break;
+                        tc_fence_after_sync();
+                        first_product(m, st, set);
+                    }
                     if (ok)
                         commit(CF::BAR_XE);
                 } else {
@@ -475,54 +524,6 @@ __global__ void __launch_bounds__(640, 1)
             }
             commit(CF::BAR_DRAIN);
             wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
-        } else if (warp == 2) {
-            // ------------------------------------------------------------ tiles
-            bool more = true;
-            for (int t = 0; more; ++t) {
-                if (t >= 2 && !__all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_TE + (t & 1)),
-                                                                    static_cast<uint32_t>((t >> 1) - 1) & 1u, abort_flag,
-                                                                    timeout, ERR_EPILOGUE)))
-                    break;
-                int item = 0;
-                if (lane == 0)
-                    item = atomicAdd(p.next, 1);
-                item = __shfl_sync(0xffffffffu, item, 0);
-                more = item < items;
-                int4 tl = make_int4(-1, 0, 0, 0);
-                if (more) {
-                    // causal: the heaviest tiles first (the first keys, the last queries); else one head's tiles together
-                    const int tile = p.mask.causal ? (DKV ? item / BH : p.tiles - 1 - item / BH) : item % p.tiles;
-                    const int bh = p.mask.causal ? item % BH : item / p.tiles;
-                    const int b = bh / heads, x0 = tile * CF::BM;
-                    const int4 *rg = p.ranges + static_cast<int64_t>(b) * p.nqb;
-                    int first = 0x7FFFFFFF, end = 0;
-                    if constexpr (DKV) {
-                        // the blocks of queries that see some key of the tile
-                        for (int q = lane; q < p.nqb; q += 32) {
-                            const int4 v = __ldg(rg + q);
-                            if (v.x < x0 + CF::BM && v.y > x0) {
-                                first = min(first, q);
-                                end = max(end, q + 1);
-                            }
-                        }
-                        first = __reduce_min_sync(0xffffffffu, first);
-                        end = __reduce_max_sync(0xffffffffu, end);
-                    } else {
-                        // the blocks of keys that some query of the tile sees
-                        for (int q = tile * (CF::BM / CF::BN); q < min(p.nqb, (tile + 1) * (CF::BM / CF::BN)); ++q) {
-                            const int4 v = __ldg(rg + q);
-                            first = min(first, v.x / CF::BN);
-                            end = max(end, (v.y + CF::BN - 1) / CF::BN);
-                        }
-                    }
-                    tl = make_int4(x0, bh, first, end > first ? end - first : 0);
-                }
-                if (lane == 0) {
-                    tile_slots[t & 1] = tl;
-                    mbar_arrive(bar(CF::BAR_TF + (t & 1)));
-                }
-                __syncwarp();
-            }
         }
         __syncwarp();
     } else {
@@ -545,13 +546,13 @@ __global__ void __launch_bounds__(640, 1)
                 mbar_arrive(bar(id));
         };
         // fp16: dX times x_mul over P's factor; x_undo takes dX's factor out again
-        float x_mul = 1.0f, x_undo = CAP ? 4.0f : 1.0f;  // capped: 1 - tanh^2 = 4 r (1 - r), bf16 leaves the 4 for the end
+        float x_mul = 1.0f, x_undo = 1.0f;
         if constexpr (DT == 0) {
             const unsigned bits = __ldg(p.amax);
             // 2^-e with 2^(e-1) <= largest |dO| < 2^e, kept where both 2^e and 2^-e are normal; 1 for 0, inf, NaN
             int e = static_cast<int>(bits >> 23) - 126;
             e = bits == 0 || bits >= 0x7F800000u ? 0 : min(max(e, -100), 100);
-            x_mul = exp2f(static_cast<float>(-e) + 4.0f - kPShift<DT>) * x_undo;  // the capped 4 goes in here
+            x_mul = exp2f(static_cast<float>(-e) + 4.0f - kPShift<DT>);
             x_undo = exp2f(static_cast<float>(e) - 4.0f);
         }
         constexpr float p_undo = DT == 0 ? 1.0f / 1024.0f : 1.0f;
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(640, 1)
                 whole = __all_sync(0xffffffffu, whole);
                 tmem_load_wait();
                 float2 w[HN / 2];        // P
-                float2 c[CAP ? HN / 2 : 1];  // a quarter of 1 - tanh^2
+                float2 c[CAP ? HN / 2 : 1];  // 1 - tanh^2
                 // scores to P; only blocks that cut an interval are masked
                 auto weights = [&](auto masked) {
                     constexpr bool MASKED = decltype(masked)::value;
@@ -644,9 +645,8 @@ __global__ void __launch_bounds__(640, 1)
                             const float2 nl = h ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
                             float2 x;
                             if constexpr (CAP) {
-                                const float2 q = cap_reciprocals(s, p.score.cap_arg);
-                                x = ffma2(q, splat2(-2.0f * p.score.cap_log2), fadd2(nl, splat2(p.score.cap_log2)));
-                                c[i / 2] = ffma2(make_float2(-q.x, -q.y), q, q);
+                                x = ffma2(s, splat2(p.score.cap_log2), nl);
+                                c[i / 2] = ffma2(make_float2(-s.x, -s.y), s, splat2(1.0f));
                             } else {
                                 x = ffma2(s, splat2(p.score.scale_log2), nl);
                             }
@@ -671,6 +671,8 @@ __global__ void __launch_bounds__(640, 1)
                         }
                     }
                 };
+                if constexpr (CAP)
+                    tanh_scores<HN>(sv, p.score.cap_arg);
                 if (whole)
                     weights(std::false_type{});
                 else
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(640, 1)
             const float mul = second ? p_undo : p.scale * x_undo;
             const uint32_t acc0 = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_A0);
             const uint32_t acc = second ? acc0 : tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_A1);
-            const float e_mul = -e_row * p.scale * p_undo * (CAP ? 4.0f : 1.0f);
+            const float e_mul = -e_row * p.scale * p_undo;
             const bool none = n_total == 0 || (!DKV && seen.y - seen.x <= 1);  // nothing comes through
             if constexpr (!DKV) {
                 if (group == 0 && row_stats)

@@ -134,24 +134,60 @@ __device__ __forceinline__ int2 visible_keys(const MaskParams &m, const int32_t 
 
 struct ScoreParams {
     float scale_log2;  // scale * log2(e)
-    float cap_arg;     // 2 scale log2(e) / cap: e^(2 x) = 2^(cap_arg a) for x = scale a / cap
+    float cap_arg;     // scale / cap
     float cap_log2;    // cap * log2(e)
     const float *slopes;  // [heads], or null
 };
 
-// tanh x = 1 - 2 / (1 + e^(2x)) of two scores at once: one reciprocal of the
-// product of the two denominators serves both, so a pair costs two 2^x and
-// one reciprocal.  The exponent is held below 2^60 (tanh is 1 to 2^-59 there)
-// so that the product stays finite.  The result is absolutely exact to about
-// 2^-22, which is what a score needs: cap 50 leaves 1e-5 in y.  r receives
-// 1 / (1 + e^(2x)): tanh x = 1 - 2 r and 1 - tanh^2 x = 4 r (1 - r).
-__device__ __forceinline__ float2 cap_reciprocals(float2 a, float cap_arg)
+// The N raw scores v to tanh(arg v), in place, N a multiple of 4.
+//
+// Where the warp's |arg v| are all at most 1 -- scores inside the cap, the usual
+// case -- tanh x = x p(x^2) with p of degree 6, the minimax fit of csrc/fit_tanh.py
+// (relative error 5e-8): 4.5 multiply-adds a score, two to an instruction, and no
+// special-function operation.  Otherwise tanh x = 1 - 2 / (1 + 2^(2 log2(e) x)),
+// one 2^x a score and one reciprocal for two, of the product of their
+// denominators; the exponent is held below 2^60 (tanh is 1 to 2^-59 there) so that
+// the product stays finite.  Both are absolutely exact to about 2^-22, which is
+// what a score needs: a cap of 50 leaves 1e-5.  The second form alone made a
+// capped forward of 16 heads x 4096^2 x 128 take 150 us.
+template <int N>
+__device__ __forceinline__ void tanh_scores(uint32_t *v, float arg)
 {
-    const float2 z = fmul2(a, splat2(cap_arg));
-    const float2 d = fadd2(make_float2(exp2_approx_ftz(fmin_nan(z.x, 60.0f)), exp2_approx_ftz(fmin_nan(z.y, 60.0f))),
-                           splat2(1.0f));
-    const float r = rcp_approx(d.x * d.y);
-    return make_float2(r * d.y, r * d.x);
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 x = fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), splat2(arg));
+        v[e] = __float_as_uint(x.x);
+        v[e + 1] = __float_as_uint(x.y);
+        top = fmax3(top, fabsf(x.x), fabsf(x.y));
+    }
+    if (__all_sync(0xffffffffu, top <= 1.0f)) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 x = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            const float2 u = fmul2(x, x);
+            float2 t = ffma2(u, splat2(0.001041022636f), splat2(-0.006203379112f));
+            t = ffma2(u, t, splat2(0.02028998043f));
+            t = ffma2(u, t, splat2(-0.05345702957f));
+            t = ffma2(u, t, splat2(0.1332520408f));
+            t = ffma2(u, t, splat2(-0.3333283915f));
+            t = ffma2(u, t, splat2(0.9999999502f));
+            t = fmul2(t, x);
+            v[e] = __float_as_uint(t.x);
+            v[e + 1] = __float_as_uint(t.y);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 z = fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), splat2(2.8853900817779268f));
+            const float2 d = fadd2(make_float2(exp2_approx_ftz(fmin_nan(z.x, 60.0f)), exp2_approx_ftz(fmin_nan(z.y, 60.0f))),
+                                   splat2(1.0f));
+            const float r = -2.0f * rcp_approx(d.x * d.y);
+            const float2 t = ffma2(splat2(r), make_float2(d.y, d.x), splat2(1.0f));
+            v[e] = __float_as_uint(t.x);
+            v[e + 1] = __float_as_uint(t.y);
+        }
+    }
 }
 
 } // namespace tl

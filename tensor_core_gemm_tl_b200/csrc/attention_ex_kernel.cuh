@@ -13,8 +13,8 @@
 // interval pay for masking.
 //
 // What bounds it: 4 D multiply-adds a pair at the tensor core's 8192 a clock
-// and SM against one 2^x a pair (2.5 with capped scores: two 2^x and half a
-// reciprocal) at 16 a clock: with D = 128 the exponentials, not the products.
+// and SM against one 2^x a pair at 16 a clock: 1024 clocks a tile and block each
+// with D = 128; capped scores add the multiply-adds of tanh_scores.
 //
 // Warp roles (384 threads): warp 0 TMA producer, warp 1 TMEM allocator and MMA
 // issuer, warps 2..3 idle, warps 4..7 softmax of tile 0, 8..11 of tile 1.
@@ -329,18 +329,17 @@ __global__ void __launch_bounds__(384, 1)
             tmem_load_wait();
             tmem_load_32cols(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
             tmem_load_32cols(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
-            // capped or biased scores, in log2 units, in place of the raw ones
+            // tanh of the capped scores, or biased scores in log2 units, in place of the raw ones
             const float dist0 = static_cast<float>(pos - key0);
             auto transform = [&](int half) {
+                if constexpr (CAP)
+                    tanh_scores<64>(sv + 64 * half, p.score.cap_arg);
+                if constexpr (!BIAS)
+                    return;
 #pragma unroll
                 for (int e = 64 * half; e < 64 * half + 64; e += 2) {
-                    float2 x = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                    if constexpr (CAP) {
-                        const float2 r = cap_reciprocals(x, p.score.cap_arg);
-                        x = ffma2(r, splat2(-2.0f * p.score.cap_log2), splat2(p.score.cap_log2));
-                    } else {
-                        x = fmul2(x, splat2(p.score.scale_log2));
-                    }
+                    float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                                     splat2(CAP ? p.score.cap_log2 : p.score.scale_log2));
                     if constexpr (BIAS) {
                         const float2 dist = fadd2(splat2(dist0), make_float2(-static_cast<float>(e), -static_cast<float>(e + 1)));
                         x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
@@ -377,14 +376,14 @@ __global__ void __launch_bounds__(384, 1)
             for (int g = 0; g < 8; ++g)
                 t[g] = fmaxf(t[g], t[g + 8]);
             float mx = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
-            if constexpr (!CAP && !BIAS)
-                mx *= p.score.scale_log2;
+            const float to_log2 = CAP ? p.score.cap_log2 : p.score.scale_log2;  // of a score without a bias
+            if constexpr (!BIAS)
+                mx *= to_log2;
             // move the reference maximum only when the weights would exceed 2^8
             const bool resc = mx > m + CF::RESCALE_LOG2;
             const float m_new = resc ? mx : m;
             const float m_ref = m_new == -INFINITY ? 0.0f : m_new;  // no visible key yet: all weights 0
             const float alpha = resc ? exp2_approx_ftz(m - m_ref) : 1.0f;  // 0 when m is -inf
-            const float2 scale2 = splat2(CAP || BIAS ? 1.0f : p.score.scale_log2);
             const float2 negm2 = splat2(-m_ref);
             float2 part[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
 #pragma unroll
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(384, 1)
                 for (int e2 = 0; e2 < 32; ++e2) {
                     const int e = 64 * g + 2 * e2;
                     const float2 s = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                    const float2 x = CAP || BIAS ? fadd2(s, negm2) : ffma2(s, scale2, negm2);
+                    const float2 x = BIAS ? fadd2(s, negm2) : ffma2(s, splat2(to_log2), negm2);
                     const float2 w = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
                     part[e2 & 3] = fadd2(part[e2 & 3], w);
                     pk[e2] = pack2<DT>(w.x, w.y);  // keys 2 e2, 2 e2 + 1 of this half: one 32-bit column

@@ -127,7 +127,7 @@ inline ScoreParams score_params(float scale, float cap, const float *slopes)
 {
     ScoreParams s{};
     s.scale_log2 = scale * 1.4426950408889634f;
-    s.cap_arg = cap > 0.0f ? 2.0f * 1.4426950408889634f * scale / cap : 0.0f;
+    s.cap_arg = cap > 0.0f ? scale / cap : 0.0f;
     s.cap_log2 = cap * 1.4426950408889634f;
     s.slopes = slopes;
     return s;

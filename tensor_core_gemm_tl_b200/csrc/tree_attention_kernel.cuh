@@ -527,20 +527,17 @@ __global__ void __launch_bounds__(384, 1)
                                     sv[32 * q + e] = __float_as_uint(value);
                         }
                     };
-                    // a page's unused rows may hold anything, and the cap's shared reciprocal takes two keys at once
+                    // a page's unused rows may hold anything, and a reciprocal shared by two keys would spread it
                     if (CAP && !context_only)
                         hide(0.0f);
                     if constexpr (CAP || BIAS) {
                         const float dist0 = static_cast<float>(pos - key0);
+                        if constexpr (CAP)
+                            tanh_scores<128>(sv, p.score.cap_arg);
 #pragma unroll
-                        for (int e = 0; e < 128; e += 2) {
-                            float2 x = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                            if constexpr (CAP) {
-                                const float2 c = cap_reciprocals(x, p.score.cap_arg);
-                                x = ffma2(c, splat2(-2.0f * p.score.cap_log2), splat2(p.score.cap_log2));
-                            } else {
-                                x = fmul2(x, splat2(p.score.scale_log2));
-                            }
+                        for (int e = 0; e < 128 && BIAS; e += 2) {
+                            float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                                             splat2(CAP ? p.score.cap_log2 : p.score.scale_log2));
                             if constexpr (BIAS) {
                                 float2 dist = make_float2(dist0 - static_cast<float>(e), dist0 - static_cast<float>(e + 1));
                                 if (!context_only) {
@@ -570,8 +567,9 @@ __global__ void __launch_bounds__(384, 1)
                     for (int q = 0; q < 8; ++q)
                         t[q] = fmaxf(t[q], t[q + 8]);
                     float mx = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
-                    if constexpr (!CAP && !BIAS)
-                        mx *= p.score.scale_log2;
+                    const float to_log2 = CAP ? p.score.cap_log2 : p.score.scale_log2;  // of a score without a bias
+                    if constexpr (!BIAS)
+                        mx *= to_log2;
                     const bool resc = mx > m + CF::RESCALE_LOG2;
                     const float m_new = resc ? mx : m;
                     const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
@@ -585,7 +583,7 @@ __global__ void __launch_bounds__(384, 1)
                         for (int e2 = 0; e2 < 32; ++e2) {
                             const int e = 64 * q + 2 * e2;
                             const float2 v = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                            const float2 x = CAP || BIAS ? fadd2(v, negm2) : ffma2(v, splat2(p.score.scale_log2), negm2);
+                            const float2 x = BIAS ? fadd2(v, negm2) : ffma2(v, splat2(to_log2), negm2);
                             const float2 e2v = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
                             part[e2 & 3] = fadd2(part[e2 & 3], e2v);
                             pk[e2] = pack2<DT>(e2v.x, e2v.y);
