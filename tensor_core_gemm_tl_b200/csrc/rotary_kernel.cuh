@@ -7,9 +7,13 @@
 // through.  The negative angle is the inverse up to scale^2 and, the map being
 // linear, its own backward.
 //
-// Bound by reading and writing q and k once.  The angles are taken once a token
-// and frequency, not once a head: a CTA turns the positions of a few tokens
-// into sines and cosines in shared memory and applies them to all their heads.
+// Bound by reading and writing q and k once.  A warp takes a token (or, where
+// tokens are few, part of its heads): it works the angles out, two frequencies a
+// lane, hands them round through its own shared memory and keeps those of its
+// lanes' words in registers for all heads, the first heads' words already on
+// their way meanwhile.  With the angles in shared memory for a whole CTA and read
+// for every head the kernel issued 340 instructions for every 32 items and was
+// bound by that (39 us for 16384 tokens of 20 heads of 128, 26 us of traffic).
 // position * inv_freq is multiplied and reduced to [-pi, pi] in double (a
 // float product is off by 0.06 rad at position 10^6), the sine and cosine are
 // fp32.
@@ -30,7 +34,7 @@ struct RotaryParams {
     RotaryTensor t[2];
     int32_t B, S, D, rot;
     int32_t interleaved, inverse;
-    int32_t tokens_per_cta;
+    int32_t warps_per_token;
     const void *positions;  // int32 or int64, [S] or [B][S]
     int64_t pos_batch;      // its batch stride (0: shared by the batch)
     int32_t pos64;
@@ -38,91 +42,145 @@ struct RotaryParams {
     float scale;
 };
 
+// (a cos - b sin, a sin + b cos), rounded the same way on every path
+__device__ __forceinline__ float2 turn_pair(float a, float b, float cos, float sin)
+{
+    return make_float2(fmaf(a, cos, -__fmul_rn(b, sin)), fmaf(a, sin, __fmul_rn(b, cos)));
+}
+
 // Words of 16 bytes (VEC) or single values: VEC needs D, rot and the strides
 // in whole words and, in the half layout, rot / 2 too.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p)
 {
-    extern __shared__ float2 turn[];  // [token][frequency]: cos, sin
+    extern __shared__ __align__(16) float2 turn_smem[];  // [warp][frequency]: cos, sin
     grid_dependency_wait();
     grid_launch_dependents();
     const int n = p.rot / 2;
-    const int64_t total = static_cast<int64_t>(p.B) * p.S;
-    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tokens_per_cta;
-    const int toks = static_cast<int>(total - tok0 < p.tokens_per_cta ? total - tok0 : p.tokens_per_cta);
-    for (int i = threadIdx.x; i < toks * n; i += 256) {
-        const int64_t tok = tok0 + i / n;
-        const int64_t at = tok / p.S * p.pos_batch + tok % p.S;
-        const double pos = p.pos64 ? static_cast<double>(static_cast<const int64_t *>(p.positions)[at])
-                                   : static_cast<double>(static_cast<const int32_t *>(p.positions)[at]);
-        const double f = pos * static_cast<double>(p.inv_freq[i % n]);
-        const double turns = rint(f * 0.15915494309189533577);
-        // 2 pi in two parts: the product with the first is exact enough for |turns| < 2^27
-        const float r = static_cast<float>(fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586232, f)));
-        float s, c;
-        sincosf(r, &s, &c);
-        turn[i] = make_float2(c * p.scale, (p.inverse ? -s : s) * p.scale);
-    }
-    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+    const int tok = static_cast<int>(w / p.warps_per_token);
+    if (tok >= p.B * p.S)
+        return;
+    const int part = static_cast<int>(w - static_cast<int64_t>(tok) * p.warps_per_token);
+    const int b = tok / p.S;
+    const int64_t s = tok - b * p.S;
+    float2 *turn = turn_smem + warp * ((n + 1) & ~1);
+
+    // A lane keeps its item of a head (a pair of words in the half layout, a word
+    // of pairs interleaved, or a word that passes through) and goes over heads; a
+    // warp takes as many heads at a time as its lanes hold.  Heads of more than
+    // 32 items are gone over once for every 32.
+    constexpr int W = VEC ? 8 : 1, AHEAD = 4;
     const int heads = p.t[0].heads + p.t[1].heads;
-    constexpr int W = VEC ? 8 : 1;
-    // work items of a head: pairs of words (half layout) or words of pairs, then words that pass through
     const int turned = VEC ? (p.interleaved ? p.rot / 8 : n / 8) : n;
     const int items = turned + (p.D - p.rot) / W;
-    for (int i = threadIdx.x; i < toks * heads * items; i += 256) {
-        const int item = i % items;
-        const int th = i / items;
-        const int head = th % heads, t = th / heads;
-        const bool second = head >= p.t[0].heads;
-        const RotaryTensor &q = p.t[second ? 1 : 0];
-        const int h = second ? head - p.t[0].heads : head;
-        const int64_t tok = tok0 + t;
-        const int64_t b = tok / p.S, s = tok - b * p.S;
-        const uint16_t *x = q.x + b * q.xs[0] + h * q.xs[1] + s * q.xs[2];
-        uint16_t *y = q.y + b * q.ys[0] + h * q.ys[1] + s * q.ys[2];
-        if (item >= turned) {
-            const int c = p.rot + (item - turned) * W;
-            if constexpr (VEC)
-                *reinterpret_cast<uint4 *>(y + c) = *reinterpret_cast<const uint4 *>(x + c);
-            else
-                y[c] = x[c];
-            continue;
-        }
-        const float2 *cs = turn + t * n;
-        if constexpr (VEC) {
-            auto lo = [](uint32_t v) { return to_float<DT>(static_cast<uint16_t>(v & 0xFFFFu)); };
-            auto hi = [](uint32_t v) { return to_float<DT>(static_cast<uint16_t>(v >> 16)); };
-            if (p.interleaved) {
-                uint4 w = *reinterpret_cast<const uint4 *>(x + 8 * item);
-                uint32_t *u = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = cs[4 * item + e];
-                    const float a = lo(u[e]), c = hi(u[e]);
-                    u[e] = pack2<DT>(a * f.x - c * f.y, a * f.y + c * f.x);
-                }
-                *reinterpret_cast<uint4 *>(y + 8 * item) = w;
+    const int lanes = min(items, 32);
+    const int warp_rows = 32 / lanes, sub = lane / lanes;
+    const int step = warp_rows * p.warps_per_token, h0 = part * warp_rows + sub;
+    const uint16_t *xq = p.t[0].x + b * p.t[0].xs[0] + s * p.t[0].xs[2];
+    uint16_t *yq = p.t[0].y + b * p.t[0].ys[0] + s * p.t[0].ys[2];
+    const uint16_t *xk = p.t[1].x + b * p.t[1].xs[0] + s * p.t[1].xs[2];
+    uint16_t *yk = p.t[1].y + b * p.t[1].ys[0] + s * p.t[1].ys[2];
+    auto lo = [](uint32_t v) { return to_float<DT>(static_cast<uint16_t>(v & 0xFFFFu)); };
+    auto hi = [](uint32_t v) { return to_float<DT>(static_cast<uint16_t>(v >> 16)); };
+
+    for (int item0 = 0; item0 < items; item0 += 32) {
+        const int item = item0 + lane - sub * lanes;
+        const bool mine = sub < warp_rows && item < items;
+        const bool turns = item < turned;
+        // value offsets of the one or two words
+        const int at = turns ? (!VEC && p.interleaved ? 2 * item : W * item) : p.rot + (item - turned) * W;
+        const int second = !turns || (VEC && p.interleaved) ? 0 : p.interleaved ? at + 1 : at + n;
+        uint4 va[AHEAD], vb[AHEAD];
+        auto fetch = [&](int h, uint4 &a, uint4 &c) {
+            if (!mine || h >= heads)
+                return;
+            const uint16_t *x = h < p.t[0].heads ? xq + h * p.t[0].xs[1] : xk + (h - p.t[0].heads) * p.t[1].xs[1];
+            if constexpr (VEC) {
+                a = *reinterpret_cast<const uint4 *>(x + at);
+                if (second)
+                    c = *reinterpret_cast<const uint4 *>(x + second);
             } else {
-                uint4 wa = *reinterpret_cast<const uint4 *>(x + 8 * item);
-                uint4 wb = *reinterpret_cast<const uint4 *>(x + n + 8 * item);
-                uint32_t *ua = reinterpret_cast<uint32_t *>(&wa), *ub = reinterpret_cast<uint32_t *>(&wb);
+                a.x = x[at];
+                if (second)
+                    c.x = x[second];
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            fetch(h0 + i * step, va[i], vb[i]);
+        if (item0 == 0) {
+            const double pos = p.pos64 ? static_cast<double>(static_cast<const int64_t *>(p.positions)[b * p.pos_batch + s])
+                                       : static_cast<double>(static_cast<const int32_t *>(p.positions)[b * p.pos_batch + s]);
+            for (int i = lane; i < n; i += 32) {
+                const double f = pos * static_cast<double>(p.inv_freq[i]);
+                const double rounds = rint(f * 0.15915494309189533577);
+                // 2 pi in two parts: the product with the first is exact enough for |rounds| < 2^27
+                const float r =
+                    static_cast<float>(fma(-rounds, 2.4492935982947064e-16, fma(-rounds, 6.283185307179586232, f)));
+                float sn, cs;
+                sincosf(r, &sn, &cs);
+                turn[i] = make_float2(cs * p.scale, (p.inverse ? -sn : sn) * p.scale);
+            }
+            __syncwarp();
+        }
+        float2 f[W];  // the lane's cos and sin
+        if (mine && turns) {
+            if constexpr (VEC) {
+                const float4 *t4 = reinterpret_cast<const float4 *>(turn + (p.interleaved ? 4 * item : 8 * item));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 f = cs[8 * item + 2 * e], g = cs[8 * item + 2 * e + 1];
-                    const float a0 = lo(ua[e]), a1 = hi(ua[e]), b0 = lo(ub[e]), b1 = hi(ub[e]);
-                    ua[e] = pack2<DT>(a0 * f.x - b0 * f.y, a1 * g.x - b1 * g.y);
-                    ub[e] = pack2<DT>(a0 * f.y + b0 * f.x, a1 * g.y + b1 * g.x);
+                    if (e < 2 || !p.interleaved) {
+                        const float4 v = t4[e];
+                        f[2 * e] = make_float2(v.x, v.y);
+                        f[2 * e + 1] = make_float2(v.z, v.w);
+                    }
                 }
-                *reinterpret_cast<uint4 *>(y + 8 * item) = wa;
-                *reinterpret_cast<uint4 *>(y + n + 8 * item) = wb;
+            } else {
+                f[0] = turn[item];
             }
-        } else {
-            const int ia = p.interleaved ? 2 * item : item, ib = p.interleaved ? 2 * item + 1 : n + item;
-            const float2 f = cs[item];
-            const float a = to_float<DT>(x[ia]), c = to_float<DT>(x[ib]);
-            const uint32_t w = pack2<DT>(a * f.x - c * f.y, a * f.y + c * f.x);
-            y[ia] = static_cast<uint16_t>(w & 0xFFFFu);
-            y[ib] = static_cast<uint16_t>(w >> 16);
+        }
+        for (int h = h0; h < heads; h += AHEAD * step) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int hh = h + i * step;
+                if (!mine || hh >= heads)
+                    continue;
+                uint16_t *y = hh < p.t[0].heads ? yq + hh * p.t[0].ys[1] : yk + (hh - p.t[0].heads) * p.t[1].ys[1];
+                uint4 a = va[i], c = vb[i];
+                if constexpr (VEC) {
+                    uint32_t *ua = reinterpret_cast<uint32_t *>(&a), *uc = reinterpret_cast<uint32_t *>(&c);
+                    if (second) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v0 = turn_pair(lo(ua[e]), lo(uc[e]), f[2 * e].x, f[2 * e].y);
+                            const float2 v1 = turn_pair(hi(ua[e]), hi(uc[e]), f[2 * e + 1].x, f[2 * e + 1].y);
+                            ua[e] = pack2<DT>(v0.x, v1.x);
+                            uc[e] = pack2<DT>(v0.y, v1.y);
+                        }
+                        *reinterpret_cast<uint4 *>(y + second) = c;
+                    } else if (turns) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v = turn_pair(lo(ua[e]), hi(ua[e]), f[e].x, f[e].y);
+                            ua[e] = pack2<DT>(v.x, v.y);
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(y + at) = a;
+                } else {
+                    uint32_t v = a.x;
+                    if (second) {
+                        const float2 t = turn_pair(lo(a.x), lo(c.x), f[0].x, f[0].y);
+                        v = pack2<DT>(t.x, t.y);
+                        y[second] = static_cast<uint16_t>(v >> 16);
+                    }
+                    y[at] = static_cast<uint16_t>(v & 0xFFFFu);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                fetch(h + (AHEAD + i) * step, va[i], vb[i]);
         }
     }
 }

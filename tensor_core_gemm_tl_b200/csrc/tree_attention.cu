@@ -228,9 +228,16 @@ tl_status rotary_impl(const void *Q, const void *K, void *Qout, void *Kout, cons
     p.pos64 = o.positions_int64;
     p.inv_freq = inv_freq;
     p.scale = o.scale > 0.0f ? o.scale : 1.0f;
-    p.tokens_per_cta = 1;
-    const int64_t grid = ceil_div(batch * seq, p.tokens_per_cta);
-    const int smem = p.tokens_per_cta * static_cast<int>(rot_dim / 2) * 8;
+    // a warp a token; where tokens are few, up to eight, each with part of the heads
+    const int items = vec ? static_cast<int>((o.interleaved ? rot_dim / 8 : rot_dim / 16) + (head_dim - rot_dim) / 8)
+                          : static_cast<int>(rot_dim / 2 + head_dim - rot_dim);
+    const int64_t goes = ceil_div(heads + kv_heads, items < 32 ? 32 / items : 1);  // of a warp alone over a token's heads
+    int wpt = 1;
+    while (wpt < 8 && 2 * wpt <= goes && batch * seq * wpt < 8 * static_cast<int64_t>(d->num_sms))
+        wpt *= 2;
+    p.warps_per_token = wpt;
+    const int64_t grid = ceil_div(batch * seq * wpt, 8);
+    const int smem = 8 * static_cast<int>((rot_dim / 2 + 1) / 2 * 2) * 8;
     if (vec)
         return launch_overlapped(dtype == TL_BF16 ? rotary_kernel<1, true> : rotary_kernel<0, true>, grid, 256, smem,
                                  stream, p);
