@@ -14,7 +14,7 @@
 // their way meanwhile.  With the angles in shared memory for a whole CTA and read
 // for every head the kernel issued 340 instructions for every 32 items and was
 // bound by that (39 us for 16384 tokens of 20 heads of 128, 26 us of traffic).
-// position * inv_freq is multiplied and reduced to [-pi, pi] in double (a
+// position * inv_freq is multiplied and reduced to half a turn in double (a
 // float product is off by 0.06 rad at position 10^6), the sine and cosine are
 // fp32.
 #pragma once
@@ -51,7 +51,7 @@ __device__ __forceinline__ float2 turn_pair(float a, float b, float cos, float s
 // Words of 16 bytes (VEC) or single values: VEC needs D, rot and the strides
 // in whole words and, in the half layout, rot / 2 too.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p)
+__global__ void __launch_bounds__(256, 4) rotary_kernel(const RotaryParams p)
 {
     extern __shared__ __align__(16) float2 turn_smem[];  // [warp][frequency]: cos, sin
     grid_dependency_wait();
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p)
     // of pairs interleaved, or a word that passes through) and goes over heads; a
     // warp takes as many heads at a time as its lanes hold.  Heads of more than
     // 32 items are gone over once for every 32.
-    constexpr int W = VEC ? 8 : 1, AHEAD = 4;
+    constexpr int W = VEC ? 8 : 1, AHEAD = 2;
     const int heads = p.t[0].heads + p.t[1].heads;
     const int turned = VEC ? (p.interleaved ? p.rot / 8 : n / 8) : n;
     const int items = turned + (p.D - p.rot) / W;
@@ -114,13 +114,11 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryParams p)
             const double pos = p.pos64 ? static_cast<double>(static_cast<const int64_t *>(p.positions)[b * p.pos_batch + s])
                                        : static_cast<double>(static_cast<const int32_t *>(p.positions)[b * p.pos_batch + s]);
             for (int i = lane; i < n; i += 32) {
-                const double f = pos * static_cast<double>(p.inv_freq[i]);
-                const double rounds = rint(f * 0.15915494309189533577);
-                // 2 pi in two parts: the product with the first is exact enough for |rounds| < 2^27
-                const float r =
-                    static_cast<float>(fma(-rounds, 2.4492935982947064e-16, fma(-rounds, 6.283185307179586232, f)));
+                // whole turns go in double: what is left is exact to 2^-53 of the angle
+                double t = pos * static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;
+                t -= rint(t);
                 float sn, cs;
-                sincosf(r, &sn, &cs);
+                sincospif(static_cast<float>(2.0 * t), &sn, &cs);
                 turn[i] = make_float2(cs * p.scale, (p.inverse ? -sn : sn) * p.scale);
             }
             __syncwarp();
