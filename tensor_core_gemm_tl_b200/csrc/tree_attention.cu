@@ -13,7 +13,7 @@ using CombineFn = void (*)(TreeParams, int);
 struct TreeEntry {
     TreeFn fn[2][2][2];  // [dtype][capped][biased]
     CombineFn combine[2];
-    int smem_fixed, smem_max, launch_regs;
+    int smem_fixed, smem_max, tile_bytes, most_slots, launch_regs;
 };
 
 template <int D>
@@ -26,7 +26,9 @@ TreeEntry make_tree()
               {tree_attention_kernel<CF, 1, true, false>, tree_attention_kernel<CF, 1, true, true>}}},
             {tree_combine_kernel<0, D>, tree_combine_kernel<1, D>},
             CF::SMEM_FIXED,
-            CF::SMEM_FIXED + 4 * (kTreeMaxBatch + 1),
+            CF::SMEM_MAX,
+            CF::TILE_BYTES,
+            CF::KS,
             CF::LAUNCH_REGS};
 }
 
@@ -119,6 +121,12 @@ tl_status tree_attention_impl(const void *Q, const void *K, const void *V, const
     p.o_row = out.s[2];
     p.lse = lse;
     p.timeout_ns = kDefaultTimeoutNs;
+    // the Q tiles take what their rows need, the K and V slots as much of the rest as they can use
+    p.q_bytes = static_cast<int32_t>(ceil_div(group * tile_tokens, 8) * 1024 * (head_dim / 64));
+    const int fixed = e.smem_fixed + static_cast<int>(ceil_div(4 * (batch + 1), 16) * 16) + 2 * p.q_bytes;
+    p.slots = (e.smem_max - fixed) / (2 * e.tile_bytes);
+    p.slots = p.slots < e.most_slots ? p.slots : e.most_slots;
+    const int smem = fixed + p.slots * 2 * e.tile_bytes;
 
     CUtensorMap tq, tk, tv;
     {
@@ -145,7 +153,7 @@ tl_status tree_attention_impl(const void *Q, const void *K, const void *V, const
         return TL_ERR_CUDA;
     p.part_o = static_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + o_bytes);
-    st = launch_overlapped(fn, grid, 384, e.smem_fixed + 4 * (p.B + 1), stream, tq, tk, tv, p);
+    st = launch_overlapped(fn, grid, 384, smem, stream, tq, tk, tv, p);
     if (st == TL_OK)
         st = launch_overlapped(e.combine[dtype], batch * units * ceil_div(tile_tokens * group, 4), 128, 0, stream, p,
                                grid);

@@ -23,6 +23,12 @@
 // the result; the others leave fp32 sums with their maximum, which
 // tree_combine_kernel joins.  A CTA prefetches across the ends of its pieces.
 //
+// Shared memory goes to the K and V slots: a Q tile keeps only the rows it has
+// (rounded up to 8).  The products still read 128 rows and find other tiles'
+// bytes behind them, which only reaches Tensor Memory lanes that are never
+// looked at.  With 16 rows that leaves three slots of each instead of two, and V,
+// which waits for its block's weights, needs the third.
+//
 // Inside a CTA consecutive blocks alternate between two sets of Tensor Memory
 // columns (scores and sums) and two softmax warpgroups, joined at the end of
 // the piece, so that one block's exponentials overlap the next one's products.
@@ -53,6 +59,8 @@ struct TreeParams {
     float *lse;                       // [B][H][T], or null
     float *part_o;                    // [2 CTAs][128][D]
     float2 *part_ml;                  // [2 CTAs][128]: maximum (log2 units), sum
+    int32_t slots;                    // K and V slots
+    int32_t q_bytes;                  // of one Q tile: D / 64 atoms of its rows
     uint64_t timeout_ns;
 };
 
@@ -79,14 +87,10 @@ template <int D_>
 struct TreeConfig {
     static constexpr int D = D_;
     static constexpr int BN = 128;
-    static constexpr int KS = D == 128 ? 2 : 4;
+    static constexpr int KS = D == 128 ? 3 : 6;              // most K and V slots
     static constexpr int ATOM_BYTES = 128 * 128;
     static constexpr int D_ATOMS = D / 64;
-    static constexpr int TILE_BYTES = D_ATOMS * ATOM_BYTES;  // a Q tile, a K block, a V block
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
-    static constexpr int OFF_V = OFF_K + KS * TILE_BYTES;
-    static constexpr int OFF_BAR = OFF_V + KS * TILE_BYTES;
+    static constexpr int TILE_BYTES = D_ATOMS * ATOM_BYTES;  // a K block, a V block
     static constexpr int BAR_QF = 0, BAR_QE = 2, BAR_KF = 4, BAR_KE = 4 + KS, BAR_VF = 4 + 2 * KS, BAR_VE = 4 + 3 * KS;
     static constexpr int BAR_SF = 4 + 4 * KS;     // [stream]: scores in Tensor Memory
     static constexpr int BAR_PF = BAR_SF + 2;     // [stream]: weights in Tensor Memory (4 warps arrive)
@@ -98,18 +102,21 @@ struct TreeConfig {
     static constexpr int BAR_ML = BAR_ZR + 1;     // both streams of a piece are complete, their statistics in shared memory (8 warps)
     static constexpr int BAR_DRAIN = BAR_ML + 1;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-    static constexpr int OFF_ML = (OFF_MISC + 16 + 15) / 16 * 16;         // [piece & 1][stream][128] float2
+    static_assert(2 * TILE_BYTES >= ATOM_BYTES, "what is read behind a Q tile's rows lies in the K slots");
+    // behind the Q tiles, the K slots and the V slots:
+    static constexpr int OFF_MISC = (NUM_BARS * 8 + 15) / 16 * 16;        // TMEM address, abort flag
+    static constexpr int OFF_ML = OFF_MISC + 16;                          // [piece & 1][stream][128] float2
     static constexpr int OFF_TREE = OFF_ML + 2 * 2 * 128 * 8;             // [piece & 1][64] masks, then depths
     static constexpr int OFF_PARENT = OFF_TREE + 2 * kTreeMaxTokens * 12;  // [warp][64]
     static constexpr int OFF_CUM = OFF_PARENT + 2 * kTreeMaxTokens * 4;   // [batch]: blocks of the requests before
-    static constexpr int SMEM_FIXED = OFF_CUM + 1024;                     // + 4 (batch + 1)
+    static constexpr int SMEM_FIXED = OFF_CUM + 1024;                     // + 4 (batch + 1), Q tiles, slots
     static constexpr int THREADS = 384;
     static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 216;
     static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
     static constexpr int TMEM_S = 0, TMEM_O = 256;
     static constexpr float RESCALE_LOG2 = 8.0f;
-    static_assert(SMEM_FIXED + 4 * (kTreeMaxBatch + 1) <= 232448, "shared memory");
+    static constexpr int SMEM_MAX = 232448;
+    static_assert(SMEM_FIXED + 4 * (kTreeMaxBatch + 1) + 6 * TILE_BYTES <= SMEM_MAX, "two whole Q tiles and two slots each");
 };
 
 // A piece: consecutive blocks of one tile (request, key/value head, row tile)
@@ -143,24 +150,28 @@ __global__ void __launch_bounds__(384, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v, const TreeParams p)
 {
-    constexpr int D = CF::D, KS = CF::KS;
+    constexpr int D = CF::D;
+    const int KS = p.slots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t sQ = smem_addr(smem + CF::OFF_Q);
-    const uint32_t sK = smem_addr(smem + CF::OFF_K);
-    const uint32_t sV = smem_addr(smem + CF::OFF_V);
-    const uint32_t bar0 = smem_addr(smem + CF::OFF_BAR);
+    // Q tiles first: what the products read behind their rows are the K slots, never past the allocation
+    const int off_k = 2 * p.q_bytes, off_v = off_k + KS * CF::TILE_BYTES;
+    uint8_t *fixed = smem + off_v + KS * CF::TILE_BYTES;
+    const uint32_t sQ = smem_addr(smem);
+    const uint32_t sK = sQ + static_cast<uint32_t>(off_k);
+    const uint32_t sV = sQ + static_cast<uint32_t>(off_v);
+    const uint32_t bar0 = smem_addr(fixed);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CF::OFF_MISC);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fixed + CF::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float2 *ml = reinterpret_cast<float2 *>(smem + CF::OFF_ML);
-    uint64_t *tree_mask = reinterpret_cast<uint64_t *>(smem + CF::OFF_TREE);
-    int32_t *tree_depth = reinterpret_cast<int32_t *>(smem + CF::OFF_TREE + 2 * kTreeMaxTokens * 8);
-    int32_t *parent_smem = reinterpret_cast<int32_t *>(smem + CF::OFF_PARENT);
-    int32_t *cum = reinterpret_cast<int32_t *>(smem + CF::OFF_CUM);
+    float2 *ml = reinterpret_cast<float2 *>(fixed + CF::OFF_ML);
+    uint64_t *tree_mask = reinterpret_cast<uint64_t *>(fixed + CF::OFF_TREE);
+    int32_t *tree_depth = reinterpret_cast<int32_t *>(fixed + CF::OFF_TREE + 2 * kTreeMaxTokens * 8);
+    int32_t *parent_smem = reinterpret_cast<int32_t *>(fixed + CF::OFF_PARENT);
+    int32_t *cum = reinterpret_cast<int32_t *>(fixed + CF::OFF_CUM);
 
     if (threadIdx.x == 32) {
         for (int i = 0; i < 2; ++i) {
@@ -229,13 +240,13 @@ __global__ void __launch_bounds__(384, 1)
     const int g0 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta) * work / ctas) : 0;
     const int g1 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta + 1) * work / ctas) : 0;
 
-    uint32_t issued = 0, parity = 0;  // bits: Q buffers 0..1, K slots 8.., V slots 16..
+    uint32_t issued = 0, parity = 0;  // bits: Q tiles 0..1, K slots 8.., V slots 16..
     if (warp < 4) {
         regs_decrease<CF::REGS_CONTROL>();
         if (warp == 0) {
             // ------------------------------------------------------------ producer (the whole warp, a box a lane)
             const int boxes = CF::BN / p.box_rows;
-            const uint32_t q_bytes = static_cast<uint32_t>(CF::D_ATOMS * 128 * p.group * p.tile_tokens);
+            const uint32_t q_load = static_cast<uint32_t>(CF::D_ATOMS * 128 * p.group * p.tile_tokens);
             bool ok = true;
             int st = 0, seg = 0;
             uint32_t ph = 0;
@@ -262,10 +273,10 @@ __global__ void __launch_bounds__(384, 1)
                 if (!(ok = wait_w(CF::BAR_QE + qi, qp ^ 1u)))
                     break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(CF::BAR_QF + qi), q_bytes);
+                    mbar_arrive_expect_tx(bar(CF::BAR_QF + qi), q_load);
 #pragma unroll
                     for (int a = 0; a < CF::D_ATOMS; ++a)
-                        tma_load_5d(sQ + qi * CF::TILE_BYTES + a * CF::ATOM_BYTES, &tmap_q, bar(CF::BAR_QF + qi), 64 * a,
+                        tma_load_5d(sQ + (qi * CF::D_ATOMS + a) * (p.q_bytes / CF::D_ATOMS), &tmap_q, bar(CF::BAR_QF + qi), 64 * a,
                                     0, hk, rt * p.tile_tokens, s.b);
                 }
                 mark(qi, qp);
@@ -313,6 +324,7 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t k_desc = smem_desc_sw128(sK, 16, 1024);
                 const uint64_t v_desc = smem_desc_sw128(sV, CF::ATOM_BYTES, 1024);
                 auto kmaj = [](int k) { return static_cast<uint64_t>(((k >> 2) * CF::ATOM_BYTES + (k & 3) * 32) >> 4); };
+                const int q_atom = p.q_bytes / CF::D_ATOMS;
                 auto wait = [&](int id, uint32_t par) {
                     return wait_bounded(bar(id), par, abort_flag, timeout, ERR_MMA_DATA);
                 };
@@ -332,11 +344,12 @@ __global__ void __launch_bounds__(384, 1)
                         if (n >= 1 && !wait(CF::BAR_DONE + w1, static_cast<uint32_t>((n - 1) >> 1) & 1u))
                             break;
                         tc_fence_after_sync();
-                        const uint64_t qd = q_desc + (((seg1 & 1) * CF::TILE_BYTES) >> 4);
+                        const uint64_t qd = q_desc + (((seg1 & 1) * p.q_bytes) >> 4);
                         const uint64_t kd = k_desc + ((st1 * CF::TILE_BYTES) >> 4);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            tc_mma_f16(tmem_base + CF::TMEM_S + 128 * w1, qd + kmaj(k), kd + kmaj(k), IDESC_QK,
+                            tc_mma_f16(tmem_base + CF::TMEM_S + 128 * w1, qd + (((k >> 2) * q_atom + (k & 3) * 32) >> 4),
+                                       kd + kmaj(k), IDESC_QK,
                                        k != 0 ? 1u : 0u);
                         tc_commit(bar(CF::BAR_SF + w1));
                         tc_commit(bar(CF::BAR_KE + st1));
@@ -445,7 +458,7 @@ __global__ void __launch_bounds__(384, 1)
                     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int a = 0; a < CF::D_ATOMS; ++a) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(smem + CF::OFF_V + st * CF::TILE_BYTES + a * CF::ATOM_BYTES);
+                        uint4 *dst = reinterpret_cast<uint4 *>(smem + off_v + st * CF::TILE_BYTES + a * CF::ATOM_BYTES);
                         for (int i = from * 8 + t; i < CF::BN * 8; i += 64)
                             dst[i] = zero;
                     }
