@@ -155,7 +155,7 @@ tl_status tree_attention_impl(const void *Q, const void *K, const void *V, const
     p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + o_bytes);
     st = launch_overlapped(fn, grid, 384, smem, stream, tq, tk, tv, p);
     if (st == TL_OK)
-        st = launch_overlapped(e.combine[dtype], batch * units * ceil_div(tile_tokens * group, 4), 128, 0, stream, p,
+        st = launch_overlapped(e.combine[dtype], batch * units * ceil_div(tile_tokens * group, 32), 256, 0, stream, p,
                                grid);
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == TL_OK)
         st = TL_ERR_CUDA;

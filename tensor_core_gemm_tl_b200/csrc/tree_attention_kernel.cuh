@@ -57,7 +57,7 @@ struct TreeParams {
     uint16_t *O;
     int64_t o_batch, o_head, o_row;
     float *lse;                       // [B][H][T], or null
-    float *part_o;                    // [2 CTAs][128][D]
+    float *part_o;                    // [2 CTAs][D / 4][128][4]: a row a lane, so a warp's rows lie side by side
     float2 *part_ml;                  // [2 CTAs][128]: maximum (log2 units), sum
     int32_t slots;                    // K and V slots
     int32_t q_bytes;                  // of one Q tile: D / 64 atoms of its rows
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(384, 1)
                 const float inv = whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
                 const int slot = 2 * cta + (s.first == 0 ? 1 : 0);
                 uint16_t *orow = p.O + s.b * p.o_batch + head * p.o_head + static_cast<int64_t>(tok) * p.o_row;
-                float *prow = p.part_o + (static_cast<int64_t>(slot) * 128 + r) * D;
+                float4 *prow = reinterpret_cast<float4 *>(p.part_o) + static_cast<int64_t>(slot) * (D / 4) * 128 + r;
 #pragma unroll 1
                 for (int c0 = w * (D / 2); c0 < (w + 1) * (D / 2); c0 += 32) {
                     uint32_t o0[32], o1[32];
@@ -688,8 +688,9 @@ __global__ void __launch_bounds__(384, 1)
                         } else {
 #pragma unroll
                             for (int v = 0; v < 8; ++v)
-                                reinterpret_cast<uint4 *>(prow + c0)[v] =
-                                    make_uint4(o0[4 * v], o0[4 * v + 1], o0[4 * v + 2], o0[4 * v + 3]);
+                                prow[(c0 / 4 + v) * 128] =
+                                    make_float4(__uint_as_float(o0[4 * v]), __uint_as_float(o0[4 * v + 1]),
+                                                __uint_as_float(o0[4 * v + 2]), __uint_as_float(o0[4 * v + 3]));
                         }
                     }
                 }
@@ -729,92 +730,85 @@ __global__ void __launch_bounds__(384, 1)
         tmem_dealloc(tmem_base, 512);
 }
 
-// Joins the pieces of each tile whose blocks fell to several CTAs: a warp a
-// row.  The pieces are added in the order of the keys.
+// Joins the pieces of each tile whose blocks fell to several CTAs: a row a lane,
+// D / 8 columns a warp.  The pieces are added in the order of the keys.
 template <int DT, int D>
-__global__ void __launch_bounds__(128) tree_combine_kernel(const TreeParams p, int grid)
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams p, int grid)
 {
-    constexpr int V = D / 32;  // values a lane
-    __shared__ int sums[2];
+    constexpr int C4 = D / 32;  // groups of four columns a warp
     grid_dependency_wait();
     grid_launch_dependents();
-    const int row_blocks = (p.tile_tokens * p.group + 3) / 4;
-    const int rb = static_cast<int>(blockIdx.x % row_blocks), bu = static_cast<int>(blockIdx.x / row_blocks);
-    const int unit = bu % p.units, b = bu / p.units;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < 2)
-        sums[threadIdx.x] = 0;
-    __syncthreads();
+    const int row_groups = (p.tile_tokens * p.group + 31) / 32;
+    const int rb = static_cast<int>(blockIdx.x % row_groups), bu = static_cast<int>(blockIdx.x / row_groups);
+    const int unit = bu % p.units, b = bu / p.units;
     int before = 0, all = 0;
-    for (int i = threadIdx.x; i < p.B; i += 128) {
-        const int x = tree_request(p, i).blocks();
-        all += x;
-        before += i < b ? x : 0;
+    TreeRequest rq{0, 0, 0};
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int i = b0 + lane;
+        TreeRequest x{0, 0, 0};
+        if (i < p.B)
+            x = tree_request(p, i);
+        all += x.blocks();
+        before += i < b ? x.blocks() : 0;
+        if (b >= b0 && b < b0 + 32) {
+            rq.tokens = __shfl_sync(0xffffffffu, x.tokens, b - b0);
+            rq.keys = __shfl_sync(0xffffffffu, x.keys, b - b0);
+        }
     }
     before = __reduce_add_sync(0xffffffffu, before);
     all = __reduce_add_sync(0xffffffffu, all);
-    if (lane == 0) {
-        atomicAdd(&sums[0], before);
-        atomicAdd(&sums[1], all);
-    }
-    __syncthreads();
-    const TreeRequest rq = tree_request(p, b);
     const int blocks = rq.blocks();
     if (blocks == 0)
         return;
-    const int64_t work = static_cast<int64_t>(sums[1]) * p.units;
-    const int64_t first = static_cast<int64_t>(sums[0]) * p.units + static_cast<int64_t>(unit) * blocks;
-    const int ctas = tree_ctas(grid, static_cast<int>(work));
+    const int work = all * p.units;
+    const int first = before * p.units + unit * blocks;
+    const int ctas = tree_ctas(grid, work);
     // the CTA whose run [c work / ctas, (c + 1) work / ctas) holds block g
-    auto owner = [&](int64_t g) { return static_cast<int>(((g + 1) * ctas - 1) / work); };
+    auto owner = [&](int g) { return static_cast<int>(((static_cast<int64_t>(g) + 1) * ctas - 1) / work); };
     const int c0 = owner(first), c1 = owner(first + blocks - 1);
     if (c0 == c1)
         return;
     const int hk = unit / p.row_tiles, rt = unit - hk * p.row_tiles;
     const int rows = min(p.tile_tokens, rq.tokens - rt * p.tile_tokens) * p.group;
-    const int r = 4 * rb + warp;
-    if (r < rows) {
-        auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * 128 + r; };
-        float M = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32)
-            M = fmaxf(M, p.part_ml[slot(c)].x);
+    const int r = 32 * rb + lane;
+    if (r >= rows)
+        return;
+    auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)); };
+    const float4 *parts = reinterpret_cast<const float4 *>(p.part_o) + warp * C4 * 128 + r;
+    float M = -INFINITY, L = 0.0f, acc[4 * C4];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        float L = 0.0f, acc[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            acc[v] = 0.0f;
+    for (int v = 0; v < 4 * C4; ++v)
+        acc[v] = 0.0f;
 #pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float2 x = p.part_ml[slot(c)];
-            const float f = x.x == -INFINITY ? 0.0f : exp2_approx_ftz(x.x - M);
-            L = fmaf(x.y, f, L);
-            const float *o = p.part_o + slot(c) * D + lane * V;
-            if constexpr (V == 4) {
-                const float4 w = *reinterpret_cast<const float4 *>(o);
-                acc[0] = fmaf(w.x, f, acc[0]);
-                acc[1] = fmaf(w.y, f, acc[1]);
-                acc[2] = fmaf(w.z, f, acc[2]);
-                acc[3] = fmaf(w.w, f, acc[3]);
-            } else {
-                const float2 w = *reinterpret_cast<const float2 *>(o);
-                acc[0] = fmaf(w.x, f, acc[0]);
-                acc[1] = fmaf(w.y, f, acc[1]);
-            }
+    for (int c = c0; c <= c1; ++c)
+        M = fmaxf(M, p.part_ml[slot(c) * 128 + r].x);
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+        const float2 x = p.part_ml[slot(c) * 128 + r];
+        const float f = x.x == -INFINITY ? 0.0f : exp2_approx_ftz(x.x - M);
+        L = fmaf(x.y, f, L);
+#pragma unroll
+        for (int v = 0; v < C4; ++v) {
+            const float4 w = parts[(slot(c) * (D / 4) + v) * 128];
+            acc[4 * v] = fmaf(w.x, f, acc[4 * v]);
+            acc[4 * v + 1] = fmaf(w.y, f, acc[4 * v + 1]);
+            acc[4 * v + 2] = fmaf(w.z, f, acc[4 * v + 2]);
+            acc[4 * v + 3] = fmaf(w.w, f, acc[4 * v + 3]);
         }
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const int tok = rt * p.tile_tokens + r / p.group, head = hk * p.group + r % p.group;
-        uint16_t *orow = p.O + b * p.o_batch + head * p.o_head + static_cast<int64_t>(tok) * p.o_row + lane * V;
-        if constexpr (V == 4)
-            *reinterpret_cast<uint2 *>(orow) =
-                make_uint2(pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t *>(orow) = pack2<DT>(acc[0] * inv, acc[1] * inv);
-        if (p.lse && lane == 0)
-            p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + tok] =
-                L == 0.0f ? -INFINITY : M * 0.69314718055994531f + logf(L);
     }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int tok = rt * p.tile_tokens + r / p.group, head = hk * p.group + r % p.group;
+    uint16_t *orow = p.O + b * p.o_batch + head * p.o_head + static_cast<int64_t>(tok) * p.o_row + warp * 4 * C4;
+#pragma unroll
+    for (int v = 0; v < C4; v += 2)
+        *reinterpret_cast<uint4 *>(orow + 4 * v) =
+            make_uint4(pack2<DT>(acc[4 * v] * inv, acc[4 * v + 1] * inv), pack2<DT>(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv),
+                       pack2<DT>(acc[4 * v + 4] * inv, acc[4 * v + 5] * inv),
+                       pack2<DT>(acc[4 * v + 6] * inv, acc[4 * v + 7] * inv));
+    if (p.lse && warp == 0)
+        p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + tok] =
+            L == 0.0f ? -INFINITY : M * 0.69314718055994531f + logf(L);
 }
 
 } // namespace tl
