@@ -13,7 +13,7 @@ using CombineFn = void (*)(TreeParams, int);
 struct TreeEntry {
     TreeFn fn[2][2][2];  // [dtype][capped][biased]
     CombineFn combine[2];
-    int smem_fixed, smem_max, tile_bytes, most_slots, launch_regs;
+    int smem_fixed, smem_max, tile_bytes, most_slots;
 };
 
 template <int D>
@@ -28,8 +28,7 @@ TreeEntry make_tree()
             CF::SMEM_FIXED,
             CF::SMEM_MAX,
             CF::TILE_BYTES,
-            CF::KS,
-            CF::LAUNCH_REGS};
+            CF::KS};
 }
 
 const TreeEntry kTree64 = make_tree<64>();
@@ -94,7 +93,7 @@ tl_status tree_attention_impl(const void *Q, const void *K, const void *V, const
     const TreeEntry &e = head_dim == 64 ? kTree64 : kTree128;
     const float scale = o.softmax_scale > 0.0f ? o.softmax_scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     TreeFn fn = e.fn[dtype][o.score_cap > 0.0f][o.slopes != nullptr];
-    if ((st = ready_kernel(d, fn, e.smem_max, e.launch_regs)) != TL_OK)
+    if ((st = raise_smem_limit(d, reinterpret_cast<const void *>(fn), e.smem_max)) != TL_OK)
         return st;
 
     TreeParams p{};

@@ -111,8 +111,6 @@ struct TreeConfig {
     static constexpr int OFF_CUM = OFF_PARENT + 2 * kTreeMaxTokens * 4;   // [batch]: blocks of the requests before
     static constexpr int SMEM_FIXED = OFF_CUM + 1024;                     // + 4 (batch + 1), Q tiles, slots
     static constexpr int THREADS = 384;
-    static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 216;
-    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
     static constexpr int TMEM_S = 0, TMEM_O = 256;
     static constexpr float RESCALE_LOG2 = 8.0f;
     static constexpr int SMEM_MAX = 232448;
@@ -242,7 +240,6 @@ __global__ void __launch_bounds__(384, 1)
 
     uint32_t issued = 0, parity = 0;  // bits: Q tiles 0..1, K slots 8.., V slots 16..
     if (warp < 4) {
-        regs_decrease<CF::REGS_CONTROL>();
         if (warp == 0) {
             // ------------------------------------------------------------ producer (the whole warp, a box a lane)
             const int boxes = CF::BN / p.box_rows;
@@ -473,7 +470,6 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
         }
     } else {
-        regs_increase<CF::REGS_SOFTMAX>();
         // ------------------------------------------------------------ softmax of every other block, output of a piece
         const int w = (warp - 4) >> 2;
         const int r = (warp & 3) * 32 + lane;
@@ -515,72 +511,80 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_after_sync();
                 if (active) {
                     const int key0 = (s.first + i) * CF::BN;
-                    uint32_t sv[128];
-                    tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                    tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-                    tmem_load_32cols(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
-                    tmem_load_32cols(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
-                    tmem_load_wait();
                     const bool context_only = key0 + CF::BN <= rq.context;
-                    // put `value` in the place of the keys the row does not see
-                    auto hide = [&](float value) {
+                    const float to_log2 = CAP ? p.score.cap_log2 : p.score.scale_log2;  // of a score without a bias
+                    // 32 columns at a time, in loops: a call visits few blocks, and straight-line code for 128
+                    // columns spent its time on instruction fetches
+                    uint32_t sv[32];
+                    // put `value` in the place of the keys the row does not see, of columns 32 q ..
+                    auto hide = [&](int q, float value) {
+                        const int a = key0 + 32 * q - rq.context;  // the first key among the drafted
+                        uint32_t see;
+                        if (a <= -32)
+                            see = 0xFFFFFFFFu;
+                        else if (a < 0)
+                            see = (static_cast<uint32_t>(mask) << -a) | ((1u << -a) - 1u);
+                        else
+                            see = a < 64 ? static_cast<uint32_t>(mask >> a) : 0u;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int a = key0 + 32 * q - rq.context;  // the word's first key among the drafted
-                            uint32_t see;
-                            if (a <= -32)
-                                see = 0xFFFFFFFFu;
-                            else if (a < 0)
-                                see = (static_cast<uint32_t>(mask) << -a) | ((1u << -a) - 1u);
-                            else
-                                see = a < 64 ? static_cast<uint32_t>(mask >> a) : 0u;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see & (1u << e)))
-                                    sv[32 * q + e] = __float_as_uint(value);
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see & (1u << e)))
+                                sv[e] = __float_as_uint(value);
                     };
-                    // a page's unused rows may hold anything, and a reciprocal shared by two keys would spread it
-                    if (CAP && !context_only)
-                        hide(0.0f);
-                    if constexpr (CAP || BIAS) {
-                        const float dist0 = static_cast<float>(pos - key0);
-                        if constexpr (CAP)
-                            tanh_scores<128>(sv, p.score.cap_arg);
+                    // with a bias: the scores in log2 units
+                    auto biased = [&](int q) {
+                        const float dist0 = static_cast<float>(pos - key0 - 32 * q);
 #pragma unroll
-                        for (int e = 0; e < 128 && BIAS; e += 2) {
-                            float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
-                                             splat2(CAP ? p.score.cap_log2 : p.score.scale_log2));
-                            if constexpr (BIAS) {
-                                float2 dist = make_float2(dist0 - static_cast<float>(e), dist0 - static_cast<float>(e + 1));
-                                if (!context_only) {
-                                    // a drafted key lies at the context's end plus its depth
-                                    const int a = key0 + e - rq.context;
-                                    const int32_t *dep = tree_depth + buf * kTreeMaxTokens;
-                                    if (a >= 0)
-                                        dist.x = static_cast<float>(pos - rq.context - dep[min(a, kTreeMaxTokens - 1)]);
-                                    if (a + 1 >= 0)
-                                        dist.y = static_cast<float>(pos - rq.context - dep[min(a + 1, kTreeMaxTokens - 1)]);
-                                }
-                                x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), splat2(to_log2));
+                            float2 dist = make_float2(dist0 - static_cast<float>(e), dist0 - static_cast<float>(e + 1));
+                            if (!context_only) {
+                                // a drafted key lies at the context's end plus its depth
+                                const int a = key0 + 32 * q + e - rq.context;
+                                const int32_t *dep = tree_depth + buf * kTreeMaxTokens;
+                                if (a >= 0)
+                                    dist.x = static_cast<float>(pos - rq.context - dep[min(a, kTreeMaxTokens - 1)]);
+                                if (a + 1 >= 0)
+                                    dist.y = static_cast<float>(pos - rq.context - dep[min(a + 1, kTreeMaxTokens - 1)]);
                             }
+                            x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
                             sv[e] = __float_as_uint(x.x);
                             sv[e + 1] = __float_as_uint(x.y);
                         }
-                    }
-                    if (!context_only)
-                        hide(-INFINITY);
-                    float t[16];
+                    };
+                    // Columns 32 q .., hidden keys at -inf.  A page's unused rows may hold anything, and a
+                    // reciprocal shared by two keys would spread it: they are 0 before the cap.
+                    auto scores = [&](int q, bool cap) {
+                        tmem_load_32cols(s_addr + 32 * q, sv);
+                        tmem_load_wait();
+                        if (cap) {
+                            if (!context_only)
+                                hide(q, 0.0f);
+                            tanh_scores<32>(sv, p.score.cap_arg);
+                        }
+                        if constexpr (BIAS)
+                            biased(q);
+                        if (!context_only)
+                            hide(q, -INFINITY);
+                    };
+                    // the maximum; the cap is monotonic, so without a bias that of the raw scores serves
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        scores(q, CAP && BIAS);
+                        const float *f = reinterpret_cast<const float *>(sv);
+                        float t[4];
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float *f = reinterpret_cast<const float *>(&sv[8 * q]);
-                        t[q] = fmax3(fmax3(f[0], f[1], f[2]), fmax3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+                        for (int i = 0; i < 4; ++i)
+                            t[i] = fmax3(fmax3(f[8 * i], f[8 * i + 1], f[8 * i + 2]),
+                                         fmax3(f[8 * i + 3], f[8 * i + 4], f[8 * i + 5]), fmaxf(f[8 * i + 6], f[8 * i + 7]));
+                        mx = fmax3(mx, fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                     }
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        t[q] = fmaxf(t[q], t[q + 8]);
-                    float mx = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
-                    const float to_log2 = CAP ? p.score.cap_log2 : p.score.scale_log2;  // of a score without a bias
+                    if constexpr (CAP && !BIAS) {
+                        if (mx != -INFINITY)
+                            mx = 1.0f - 2.0f * rcp_approx(1.0f + exp2_approx_ftz(fminf(2.8853900817779268f * p.score.cap_arg * mx,
+                                                                                      60.0f)));
+                    }
                     if constexpr (!BIAS)
                         mx *= to_log2;
                     const bool resc = mx > m + CF::RESCALE_LOG2;
@@ -588,22 +592,21 @@ __global__ void __launch_bounds__(384, 1)
                     const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
                     const float alpha = resc ? exp2_approx_ftz(m - m_ref) : 1.0f;
                     const float2 negm2 = splat2(-m_ref);
-                    float2 part[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
+                    float2 part[2] = {splat2(0.0f), splat2(0.0f)};
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        scores(q, CAP);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int e2 = 0; e2 < 32; ++e2) {
-                            const int e = 64 * q + 2 * e2;
+                        for (int e = 0; e < 32; e += 2) {
                             const float2 v = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                             const float2 x = BIAS ? fadd2(v, negm2) : ffma2(v, splat2(to_log2), negm2);
-                            const float2 e2v = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
-                            part[e2 & 3] = fadd2(part[e2 & 3], e2v);
-                            pk[e2] = pack2<DT>(e2v.x, e2v.y);
+                            const float2 w2 = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
+                            part[(e >> 1) & 1] = fadd2(part[(e >> 1) & 1], w2);
+                            sv[e / 2] = pack2<DT>(w2.x, w2.y);
                         }
-                        tmem_store_32cols(s_addr + 32 * q, pk);
+                        tmem_store_16cols(s_addr + 16 * q, sv);  // over columns that have been read
                     }
-                    const float2 ps = fadd2(fadd2(part[0], part[1]), fadd2(part[2], part[3]));
+                    const float2 ps = fadd2(part[0], part[1]);
                     l = l * alpha + (ps.x + ps.y);
                     m = m_new;
                     // S(n) was issued after this stream's last P V had completed, so O is whole here
