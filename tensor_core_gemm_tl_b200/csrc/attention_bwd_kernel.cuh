@@ -788,6 +788,9 @@ __global__ void __launch_bounds__(640, 1)
                         o[e] = 0;
                 }
                 // 32 rows x 16 columns through this warp's buffer; rows behind the tensor's are not written
+                const int row0 = x0 + (warp & 3) * 32;
+                if (row0 >= (DKV ? p.mask.Sk : p.mask.Sq))
+                    continue;
                 if (lane == 0)
                     bulk_wait_group_read<0>();
                 __syncwarp();
@@ -803,7 +806,7 @@ __global__ void __launch_bounds__(640, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_4d(map_out, smem_addr(out_buf), 16 * cc, x0 + (warp & 3) * 32, head, b);
+                    tma_store_4d(map_out, smem_addr(out_buf), 16 * cc, row0, head, b);
                     bulk_commit_group();
                 }
             }

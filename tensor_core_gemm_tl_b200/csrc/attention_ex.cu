@@ -72,7 +72,7 @@ tl_status attention_call(const void *Q, const void *K, const void *V, const void
 
 namespace {
 
-using ExFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnExParams);
+using ExFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnExParams);
 
 struct ExEntry {
     ExFn fn[2][2][2];  // [dtype][capped][biased]
@@ -110,10 +110,11 @@ tl_status attention_ex_impl(const void *Q, const void *K, const void *V, void *O
     ExFn fn = e.fn[dtype][c.cap > 0.0f][c.slopes != nullptr];
     if ((st = ready_kernel(d, fn, e.smem, e.launch_regs)) != TL_OK)
         return st;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     if (!encode_heads(&tq, Q, dtype, batch, heads, seq_q, head_dim, c.q, 128) ||
         !encode_heads(&tk, K, dtype, batch, c.kv_heads, seq_k, head_dim, c.k, 128) ||
-        !encode_heads(&tv, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, 128))
+        !encode_heads(&tv, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, 128) ||
+        !encode_heads_out(&to, O, dtype, batch, heads, seq_q, head_dim, c.o, 32, 16))
         return TL_ERR_CUDA;
     AttnExParams p{};
     p.mask = c.mask;
@@ -122,13 +123,9 @@ tl_status attention_ex_impl(const void *Q, const void *K, const void *V, void *O
     p.H = static_cast<int32_t>(heads);
     p.group = static_cast<int32_t>(heads / c.kv_heads);
     p.num_pairs = static_cast<int32_t>(ceil_div(seq_q, 256));
-    p.O = static_cast<uint16_t *>(O);
-    p.o_batch = c.o.s[0];
-    p.o_head = c.o.s[1];
-    p.o_row = c.o.s[2];
     p.lse = lse;
     p.timeout_ns = kDefaultTimeoutNs;
-    return launch_overlapped(fn, p.num_pairs * batch * heads, 384, e.smem, stream, tq, tk, tv, p);
+    return launch_overlapped(fn, p.num_pairs * batch * heads, 640, e.smem, stream, tq, tk, tv, to, p);
 }
 
 } // namespace

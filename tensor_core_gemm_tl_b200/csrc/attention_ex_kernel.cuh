@@ -4,21 +4,29 @@
 //
 //     O_i = sum_j w_ij V_j,   w_ij = exp(y_ij - lse_i),   lse_i = log sum_j exp(y_ij)
 //
-// One CTA computes two 128-row query tiles of one head against one stream of
-// 128-key blocks, the tiles in ping-pong: while one warpgroup turns a tile's
-// scores into weights, the tensor core works on the other tile.  Tensor
-// Memory holds, per tile, S_i (128 fp32 columns; the 16-bit weights P_i are
-// written over its first 64) and O_i (D columns).  Each tile visits only the
-// blocks that some of its rows see; inside, only blocks that cut a row's
-// interval pay for masking.
+// An item is a pair of 128-row query tiles of one head against one stream of
+// 128-key blocks, the tiles in ping-pong: while one tile's scores become weights,
+// the tensor core works on the other.  Tensor Memory holds, per tile, S_i (128
+// fp32 columns) and O_i (D columns); the 16-bit weights P_i are written over S_i
+// (D = 128) or into columns of their own (D = 64, so that the next S_i need not
+// wait for P V).  Each tile visits only the blocks that some of its rows see;
+// inside, only blocks that cut a row's interval pay for masking.
 //
-// What bounds it: 4 D multiply-adds a pair at the tensor core's 8192 a clock
-// and SM against one 2^x a pair at 16 a clock: 1024 clocks a tile and block each
-// with D = 128; capped scores add the multiply-adds of tanh_scores.
+// Two warpgroups share a tile, 64 columns of a row a thread, and agree on the
+// row's maximum through shared memory: four warps on each scheduler hide one
+// another's latencies, which two warps of 128 columns a thread did not (1970
+// clocks a tile and block against 1024 of products).  CTAs are persistent: a CTA
+// that has issued its item's loads takes over one that has not started yet
+// (cluster launch control), so set-up, the masks' ranges and the next item's loads
+// pass beside the work; a CTA an item spent 6 us on them, more than a short
+// document's attention takes.
 //
-// Warp roles (384 threads): warp 0 TMA producer, warp 1 TMEM allocator and MMA
-// issuer, warps 2..3 idle, warps 4..7 softmax of tile 0, 8..11 of tile 1.
-// Every wait is bounded.
+// What bounds it: 2 products of 128 x 128 x D a tile and block (1024 clocks with
+// D = 128 at 4096 multiply-adds a clock and SM) against one 2^x a pair at 16 a
+// clock (1024 clocks); capped scores add the multiply-adds of tanh_scores.
+//
+// Warps: 0 items and TMA loads, 1 issues S (and allocates Tensor Memory), 2 issues
+// P V, 3 idle, 4..19 softmax.  Every wait is bounded.
 #pragma once
 
 #include "attention_common.cuh"
@@ -30,8 +38,6 @@ struct AttnExParams {
     ScoreParams score;
     int32_t B, H, group;     // batch, query heads, query heads per key/value head
     int32_t num_pairs;       // pairs of 128-row query tiles
-    uint16_t *O;
-    int64_t o_batch, o_head, o_row;  // O's strides in elements
     float *lse;              // [B][H][Sq] natural log, or null
     uint64_t timeout_ns;
 };
@@ -48,48 +54,80 @@ struct AttnExConfig {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
     static constexpr int OFF_V = OFF_K + KS * KV_BYTES;
-    static constexpr int OFF_BAR = OFF_V + KS * KV_BYTES;
-    static constexpr int BAR_Q = 0, BAR_KF = 1, BAR_KE = 1 + KS, BAR_VF = 1 + 2 * KS, BAR_VE = 1 + 3 * KS;
-    static constexpr int BAR_SF = 1 + 4 * KS;   // [tile]: S_i in Tensor Memory
-    static constexpr int BAR_PF = BAR_SF + 2;   // [tile]: P_i in Tensor Memory (4 warps arrive)
+    static constexpr int OFF_OUT = OFF_V + KS * KV_BYTES;  // [warp] 32 rows x 16 columns on their way out
+    static constexpr int OFF_BAR = OFF_OUT + 16 * 1024;
+    static constexpr int BAR_QF = 0, BAR_QE = 1;
+    static constexpr int BAR_KF = 2, BAR_KE = 2 + KS, BAR_VF = 2 + 2 * KS, BAR_VE = 2 + 3 * KS;
+    static constexpr int BAR_SF = 2 + 4 * KS;   // [tile]: S_i in Tensor Memory
+    static constexpr int BAR_SE = BAR_SF + 2;   // [tile]: S_i read into registers (8 warps; separate P only)
+    static constexpr int BAR_PF = BAR_SE + 2;   // [tile]: P_i in Tensor Memory (8 warps)
     static constexpr int BAR_PV = BAR_PF + 2;   // [tile]: O_i += P_i V completed
-    static constexpr int BAR_DRAIN = BAR_PV + 2;
+    static constexpr int BAR_MX = BAR_PV + 2;   // [tile]: both halves' maxima (or sums) are in shared memory (8 warps)
+    static constexpr int BAR_OE = BAR_MX + 2;   // [tile]: O_i has been read (8 warps)
+    static constexpr int BAR_TF = BAR_OE + 2;   // [slot]: an item's description is in shared memory
+    static constexpr int BAR_TE = BAR_TF + 2;   // [slot]: and has been read (18: two MMA issuers, 16 warps)
+    static constexpr int BAR_CLC = BAR_TE + 2;  // the answer to a request for another item
+    static constexpr int BAR_DRAIN = BAR_CLC + 1;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;  // TMEM address, abort flag, the tiles' key ranges
-    static constexpr int OFF_DOCS = OFF_MISC + 32;
-    static constexpr int SMEM_BYTES = OFF_DOCS + kDocsInSmem * 4 + 1024;
-    static constexpr int THREADS = 384;
-    static constexpr int FIRST_SOFTMAX_WARP = 4;
-    static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 216;
-    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
-    static constexpr int TMEM_S = 0, TMEM_O = 256;  // S_i at 128 i, O_i at 256 + D i
+    static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
+    static constexpr int OFF_CLC = OFF_MISC + 16;
+    static constexpr int OFF_ITEMS = OFF_CLC + 16;      // [slot] pair, head, first and end block of each tile
+    static constexpr int OFF_MX = OFF_ITEMS + 2 * 32;   // [block & 1][tile][half][128] floats
+    static constexpr int SMEM_BYTES = OFF_MX + 2 * 2 * 2 * 512 + 1024;
+    static constexpr int THREADS = 640;
+    static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 104;
+    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 512 * REGS_SOFTMAX + THREADS - 1) / THREADS;
+    static constexpr bool SEPARATE_P = D == 64;
+    // Tensor Memory columns: S_i at 128 i, O_i at 256 + D i, separate P_i at 384 + 64 i
+    static constexpr int TMEM_S = 0, TMEM_O = 256, TMEM_P = 256 + 2 * D;
+    static_assert(!SEPARATE_P || TMEM_P + 128 <= 512, "Tensor Memory columns");
+    // 16 values of P take 8 columns; over S each half's 64 lie where its scores were
+    __host__ __device__ static constexpr int p_col(int k) { return SEPARATE_P ? 8 * k : (k >> 2) * 64 + (k & 3) * 8; }
+    __host__ __device__ static constexpr int p_tile(int i) { return SEPARATE_P ? TMEM_P + 64 * i : TMEM_S + 128 * i; }
     static constexpr float RESCALE_LOG2 = 8.0f;     // m moves when a row maximum exceeds it by 2^8
     static_assert(D == 64 || D == 128, "head dim");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
+// Asks for a CTA of this grid that has not started: its index arrives at `dst`
+// (16 bytes), counted as 16 bytes on `bar`.
+__device__ __forceinline__ void clc_request(uint32_t dst, uint32_t bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+
+// The answer at `src`: the blockIdx.x taken over, or -1 when none is left
+__device__ __forceinline__ int clc_answer(uint32_t src)
+{
+    uint32_t taken, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(taken), "=r"(x)
+        : "r"(src)
+        : "memory");
+    return taken ? static_cast<int>(x) : -1;
+}
+
 template <class CF, int DT, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     attention_ex_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                        const __grid_constant__ CUtensorMap tmap_v, const AttnExParams p)
+                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
+                        const AttnExParams p)
 {
     constexpr int D = CF::D;
     constexpr int KS = CF::KS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);  // uniform for the compiler too
     const int lane = threadIdx.x & 31;
-    // blocks start in the order of blockIdx.x.  Causal: every head's last
-    // (heaviest) pair of tiles first; else the pairs of one head together, so
-    // that the CTAs running side by side share its K and V in L2.
-    const int BH = p.B * p.H;
-    const int bx = static_cast<int>(blockIdx.x);
-    const int qp = p.mask.causal ? p.num_pairs - 1 - bx / BH : bx % p.num_pairs;
-    const int bh = p.mask.causal ? bx % BH : bx / p.num_pairs;
-    const int b = bh / p.H, h = bh % p.H, hk = h / p.group;
-    const int q0 = qp * 2 * CF::BM;
-
     const uint32_t sQ = smem_addr(smem + CF::OFF_Q);
     const uint32_t sK = smem_addr(smem + CF::OFF_K);
     const uint32_t sV = smem_addr(smem + CF::OFF_V);
@@ -97,11 +135,12 @@ __global__ void __launch_bounds__(384, 1)
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CF::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *range = reinterpret_cast<int *>(tmem_slot + 2);  // [tile][first key, end key]
-    int32_t *docs_smem = reinterpret_cast<int32_t *>(smem + CF::OFF_DOCS);
+    int4 *item_slots = reinterpret_cast<int4 *>(smem + CF::OFF_ITEMS);
+    float *mx_smem = reinterpret_cast<float *>(smem + CF::OFF_MX);
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(CF::BAR_Q), 1);
+        mbar_init(bar(CF::BAR_QF), 1);
+        mbar_init(bar(CF::BAR_QE), 1);
         for (int s = 0; s < KS; ++s) {
             mbar_init(bar(CF::BAR_KF + s), 1);
             mbar_init(bar(CF::BAR_KE + s), 1);
@@ -110,368 +149,492 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(CF::BAR_SF + i), 1);
-            mbar_init(bar(CF::BAR_PF + i), 4);
+            mbar_init(bar(CF::BAR_SE + i), 8);
+            mbar_init(bar(CF::BAR_PF + i), 8);
             mbar_init(bar(CF::BAR_PV + i), 1);
-            range[2 * i] = 0x7FFFFFFF;
-            range[2 * i + 1] = 0;
+            mbar_init(bar(CF::BAR_MX + i), 8);
+            mbar_init(bar(CF::BAR_OE + i), 8);
+            mbar_init(bar(CF::BAR_TF + i), 1);
+            mbar_init(bar(CF::BAR_TE + i), 18);
         }
-        mbar_init(bar(CF::BAR_DRAIN), 1);
+        mbar_init(bar(CF::BAR_CLC), 1);
+        mbar_init(bar(CF::BAR_DRAIN), 2);
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
     }
-    if (warp == 0 && lane == 0) {
+    if (threadIdx.x == 96) {
         tma_prefetch_map(&tmap_q);
         tma_prefetch_map(&tmap_k);
         tma_prefetch_map(&tmap_v);
+        tma_prefetch_map(&tmap_o);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), 512);
         tmem_relinquish();
     }
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int32_t *docs = p.mask.doc_offsets
-                              ? p.mask.doc_offsets + static_cast<int64_t>(b) * (p.mask.num_docs + 1) : nullptr;
-    if (docs && p.mask.num_docs < kDocsInSmem) {
-        for (int i = threadIdx.x; i <= p.mask.num_docs; i += CF::THREADS)
-            docs_smem[i] = docs[i];
-        docs = docs_smem;
-    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    // each softmax thread's row and the keys it sees; the tiles' key ranges
-    const int tile = warp >= CF::FIRST_SOFTMAX_WARP ? (warp - CF::FIRST_SOFTMAX_WARP) >> 2 : 0;
-    const int row = q0 + tile * CF::BM + (warp & 3) * 32 + lane;  // query index (softmax warps)
-    int2 seen = make_int2(0, 0);
-    if (warp >= CF::FIRST_SOFTMAX_WARP) {
-        seen = visible_keys(p.mask, docs, b, row);
-        const int lo = __reduce_min_sync(0xffffffffu, seen.y > seen.x ? seen.x : 0x7FFFFFFF);
-        const int hi = __reduce_max_sync(0xffffffffu, seen.y);
-        if (lane == 0) {
-            atomicMin(&range[2 * tile], lo);
-            atomicMax(&range[2 * tile + 1], hi);
-        }
-    }
-    __syncthreads();
     const uint32_t tmem_base = *tmem_slot;
     const uint64_t timeout = p.timeout_ns;
-    // key blocks tile i visits: [first(i), end(i)); empty when no row sees a key
-    int first_b[2], end_b[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool any = range[2 * i + 1] > 0;
-        first_b[i] = any ? range[2 * i] / CF::BN : 0;
-        end_b[i] = any ? (range[2 * i + 1] + CF::BN - 1) / CF::BN : 0;
-    }
-    // the stream of blocks both tiles are fed from
-    const bool e0 = end_b[0] > first_b[0], e1 = end_b[1] > first_b[1];
-    const int j0 = e0 && e1 ? min(first_b[0], first_b[1]) : e0 ? first_b[0] : first_b[1];
-    const int j1 = max(end_b[0], end_b[1]);
-    auto visits = [&](int i, int j) { return i ? j >= first_b[1] && j < end_b[1] : j >= first_b[0] && j < end_b[0]; };
+    grid_dependency_wait();
+    grid_launch_dependents();
 
-    uint32_t q_issued = 0, k_issued = 0, k_par = 0, v_issued = 0, v_par = 0;
-    if (warp < CF::FIRST_SOFTMAX_WARP) {
+    // An item as every role sees it: the pair and head, and the key blocks
+    // [first, end) of each tile (empty: first = end = 0)
+    struct Item {
+        int b, h, q0, fb[2], eb[2], j0, j1;
+        __device__ bool visits(int i, int j) const { return i ? j >= fb[1] && j < eb[1] : j >= fb[0] && j < eb[0]; }
+    };
+    auto unpack = [&](const int4 &x, const int4 &y) {
+        Item it;
+        it.b = x.y / p.H;
+        it.h = x.y - it.b * p.H;
+        it.q0 = x.x * 2 * CF::BM;
+        it.fb[0] = x.z;
+        it.eb[0] = x.w;
+        it.fb[1] = y.x;
+        it.eb[1] = y.y;
+        const bool e0 = x.w > x.z, e1 = y.y > y.x;
+        it.j0 = e0 && e1 ? min(x.z, y.x) : e0 ? x.z : y.x;
+        it.j1 = max(x.w, y.y);
+        return it;
+    };
+    auto take_item = [&](int t, Item *out) {
+        const bool w = __all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_TF + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u,
+                                                            abort_flag, timeout, ERR_EPILOGUE));
+        if (!w)
+            return false;
+        const int4 x = item_slots[2 * (t & 1)], y = item_slots[2 * (t & 1) + 1];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar(CF::BAR_TE + (t & 1)));
+        if (x.x < 0)
+            return false;
+        *out = unpack(x, y);
+        return true;
+    };
+
+    uint32_t issued = 0, parity = 0;  // bit 0: Q, bits 8..: K slots, bits 16..: V slots
+    if (warp < 4) {
         regs_decrease<CF::REGS_CONTROL>();
         if (warp == 0) {
-            // ------------------------------------------------------------ producer
-            if (lane == 0 && j0 < j1) {
-                mbar_arrive_expect_tx(bar(CF::BAR_Q), 2 * CF::Q_BYTES);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int a = 0; a < CF::D_ATOMS; ++a)
-                        tma_load_4d(sQ + i * CF::Q_BYTES + a * CF::ATOM_BYTES, &tmap_q, bar(CF::BAR_Q), 64 * a,
-                                    q0 + i * CF::BM, h, b);
-                q_issued = 1;
-                int st = 0;
-                uint32_t ph = 0;
-                for (int j = j0; j < j1; ++j) {
-                    if (!wait_bounded(bar(CF::BAR_KE + st), ph ^ 1u, abort_flag, timeout, ERR_PRODUCER))
-                        break;
-                    mbar_arrive_expect_tx(bar(CF::BAR_KF + st), CF::KV_BYTES);
-#pragma unroll
-                    for (int a = 0; a < CF::D_ATOMS; ++a)
-                        tma_load_4d(sK + st * CF::KV_BYTES + a * CF::ATOM_BYTES, &tmap_k, bar(CF::BAR_KF + st),
-                                    64 * a, j * CF::BN, hk, b);
-                    k_issued |= 1u << st;
-                    k_par = (k_par & ~(1u << st)) | (ph << st);
-                    if (!wait_bounded(bar(CF::BAR_VE + st), ph ^ 1u, abort_flag, timeout, ERR_PRODUCER))
-                        break;
-                    mbar_arrive_expect_tx(bar(CF::BAR_VF + st), CF::KV_BYTES);
-#pragma unroll
-                    for (int a = 0; a < CF::D_ATOMS; ++a)
-                        tma_load_4d(sV + st * CF::KV_BYTES + a * CF::ATOM_BYTES, &tmap_v, bar(CF::BAR_VF + st),
-                                    64 * a, j * CF::BN, hk, b);
-                    v_issued |= 1u << st;
-                    v_par = (v_par & ~(1u << st)) | (ph << st);
-                    if (++st == KS) {
-                        st = 0;
-                        ph ^= 1u;
+            // ------------------------------------------------------------ items and loads
+            const int BH = p.B * p.H;
+            const uint32_t clc_dst = smem_addr(smem + CF::OFF_CLC);
+            auto wait = [&](int id, uint32_t par) {
+                return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_PRODUCER)) != 0;
+            };
+            // Item `index` (-1: none) as the t-th: which blocks its tiles visit, for the others
+            auto publish = [&](int t, int index, Item *out) {
+                if (t >= 2 && !wait(CF::BAR_TE + (t & 1), static_cast<uint32_t>(t >> 1) - 1))
+                    return false;
+                int4 x = make_int4(-1, 0, 0, 0), y = make_int4(0, 0, 0, 0);
+                if (index >= 0) {
+                    // CTAs start in the order of their index.  Causal: every head's last (heaviest) pair of tiles
+                    // first; else the pairs of one head together, so that those running side by side share its K and V.
+                    x.x = p.mask.causal ? p.num_pairs - 1 - index / BH : index % p.num_pairs;
+                    x.y = p.mask.causal ? index % BH : index / p.num_pairs;
+                    const int b = x.y / p.H;
+                    const int32_t *docs = p.mask.doc_offsets
+                                              ? p.mask.doc_offsets + static_cast<int64_t>(b) * (p.mask.num_docs + 1) : nullptr;
+                    // Intervals move on from row to row, so a tile's keys reach from its first row's first key to its last
+                    // row's end: lanes 2 i and 2 i + 1 look up tile i's first and last row that lie in a document.
+                    int i0 = x.x * 2 * CF::BM + ((lane >> 1) & 1) * CF::BM, i1 = min(i0 + CF::BM, p.mask.Sq) - 1;
+                    if (docs) {
+                        i0 = max(i0, docs[0] - p.mask.q_offset);
+                        i1 = min(i1, docs[p.mask.num_docs] - 1 - p.mask.q_offset);
                     }
+                    int2 seen = make_int2(0, 0);
+                    if (lane < 4 && i0 <= i1)
+                        seen = visible_keys(p.mask, docs, b, lane & 1 ? i1 : i0);
+                    const int lo0 = __shfl_sync(0xffffffffu, seen.x, 0), hi0 = __shfl_sync(0xffffffffu, seen.y, 1);
+                    const int lo1 = __shfl_sync(0xffffffffu, seen.x, 2), hi1 = __shfl_sync(0xffffffffu, seen.y, 3);
+                    if (hi0 > lo0) {
+                        x.z = lo0 / CF::BN;
+                        x.w = (hi0 + CF::BN - 1) / CF::BN;
+                    }
+                    if (hi1 > lo1) {
+                        y.x = lo1 / CF::BN;
+                        y.y = (hi1 + CF::BN - 1) / CF::BN;
+                    }
+                    *out = unpack(x, y);
                 }
-            }
-            __syncwarp();
-        } else if (warp == 1) {
-            // ------------------------------------------------------------ MMA issuer
-            if (lane == 0 && j0 < j1) {
-                constexpr uint32_t IDESC_QK = mma_idesc_f16(DT, 128, 128, 0, 0);  // Q, K both K-major
-                constexpr uint32_t IDESC_PV = mma_idesc_f16(DT, 128, D, 0, 1);    // P K-major (TMEM), V N-major
-                const uint64_t k_desc0 = smem_desc_sw128(sK, 16, 1024);
-                const uint64_t v_desc0 = smem_desc_sw128(sV, CF::ATOM_BYTES, 1024);
-                auto kmaj = [](int k) { return static_cast<uint64_t>(((k >> 2) * CF::ATOM_BYTES + (k & 3) * 32) >> 4); };
-                int kst = 0, vst = 0;
-                uint32_t kph = 0, vph = 0;
-                bool ok = wait_bounded(bar(CF::BAR_Q), 0, abort_flag, timeout, ERR_MMA_DATA);
-                auto issue_s = [&](int i) {  // S_i = Q_i K^T from the current K slot
-                    const uint64_t q_desc = smem_desc_sw128(sQ + i * CF::Q_BYTES, 16, 1024);
-                    const uint64_t kd = k_desc0 + ((kst * CF::KV_BYTES) >> 4);
-                    const uint32_t d_s = tmem_base + static_cast<uint32_t>(CF::TMEM_S + i * 128);
+                if (lane == 0) {
+                    item_slots[2 * (t & 1)] = x;
+                    item_slots[2 * (t & 1) + 1] = y;
+                    mbar_arrive(bar(CF::BAR_TF + (t & 1)));
+                }
+                __syncwarp();
+                return index >= 0;
+            };
+            Item it;
+            int st = 0;
+            uint32_t ph = 0, qph = 0;
+            bool ok = publish(0, static_cast<int>(blockIdx.x), &it);
+            for (int t = 0; ok; ++t) {
+                // the request for the next item is under way while this one's loads go out
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(bar(CF::BAR_CLC), 16);
+                    clc_request(clc_dst, bar(CF::BAR_CLC));
+                }
+                __syncwarp();
+                if (it.j0 < it.j1) {
+                    const int hk = it.h / p.group;
+                    if (lane == 0) {
+                        ok = wait_bounded(bar(CF::BAR_QE), qph ^ 1u, abort_flag, timeout, ERR_PRODUCER);
+                        if (ok) {
+                            mbar_arrive_expect_tx(bar(CF::BAR_QF), 2 * CF::Q_BYTES);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma_f16(d_s, q_desc + kmaj(k), kd + kmaj(k), IDESC_QK, k != 0 ? 1u : 0u);
-                    tc_commit(bar(CF::BAR_SF + i));
-                };
-                auto issue_pv = [&](int i, bool first) {  // O_i (+)= P_i V from the current V slot
-                    const uint32_t d_o = tmem_base + static_cast<uint32_t>(CF::TMEM_O + i * D);
-                    const uint32_t a_p = tmem_base + static_cast<uint32_t>(CF::TMEM_S + i * 128);
-                    const uint64_t vd = v_desc0 + ((vst * CF::KV_BYTES) >> 4);
+                            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int k = 0; k < CF::BN / 16; ++k)
-                        tc_mma_f16_ts(d_o, a_p + 8 * k, vd + ((2048 * k) >> 4), IDESC_PV,
-                                      (!first || k > 0) ? 1u : 0u);
-                    tc_commit(bar(CF::BAR_PV + i));
-                };
-                // j counts one ahead for S: S_i(j) for the stream's first block, then in the loop S_i(j + 1)
-                for (int j = j0 - 1; ok && j < j1; ++j) {
-                    bool k_ready = false;  // K(j + 1) waited for
-                    if (j >= j0 && !wait_bounded(bar(CF::BAR_VF + vst), vph, abort_flag, timeout, ERR_MMA_DATA)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int i = 0; ok && i < 2; ++i) {
-                        const bool here = j >= j0 && visits(i, j);
-                        const uint32_t jp = static_cast<uint32_t>(j - first_b[i]) & 1u;
-                        if (here) {
-                            if (!wait_bounded(bar(CF::BAR_PF + i), jp, abort_flag, timeout, ERR_MMA_DATA)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after_sync();
-                            issue_pv(i, j == first_b[i]);
+                                for (int a = 0; a < CF::D_ATOMS; ++a)
+                                    tma_load_4d(sQ + i * CF::Q_BYTES + a * CF::ATOM_BYTES, &tmap_q, bar(CF::BAR_QF), 64 * a,
+                                                it.q0 + i * CF::BM, it.h, it.b);
+                            issued |= 1u;
+                            parity = (parity & ~1u) | qph;
                         }
-                        if (j >= j0 && i == 1)
-                            tc_commit(bar(CF::BAR_VE + vst));  // V(j) free once the last P V of block j is done
-                        if (j + 1 < j1) {
-                            if (!k_ready && !wait_bounded(bar(CF::BAR_KF + kst), kph, abort_flag, timeout,
-                                                          ERR_MMA_DATA)) {
-                                ok = false;
-                                break;
-                            }
-                            k_ready = true;
-                            if (visits(i, j + 1)) {
-                                // S_i(j + 1) overwrites the P_i(j) that PV_i(j) reads: wait for it
-                                if (here && !wait_bounded(bar(CF::BAR_PV + i), jp, abort_flag, timeout, ERR_MMA_ACC)) {
-                                    ok = false;
+                        for (int j = it.j0; ok && j < it.j1; ++j) {
+#pragma unroll
+                            for (int kv = 0; kv < 2; ++kv) {
+                                const int full = (kv ? CF::BAR_VF : CF::BAR_KF) + st;
+                                if (!(ok = ok && wait_bounded(bar((kv ? CF::BAR_VE : CF::BAR_KE) + st), ph ^ 1u, abort_flag,
+                                                              timeout, ERR_PRODUCER)))
                                     break;
-                                }
-                                tc_fence_after_sync();
-                                issue_s(i);
+                                mbar_arrive_expect_tx(bar(full), CF::KV_BYTES);
+#pragma unroll
+                                for (int a = 0; a < CF::D_ATOMS; ++a)
+                                    tma_load_4d((kv ? sV : sK) + st * CF::KV_BYTES + a * CF::ATOM_BYTES,
+                                                kv ? &tmap_v : &tmap_k, bar(full), 64 * a, j * CF::BN, hk, it.b);
+                                const int bit = (kv ? 16 : 8) + st;
+                                issued |= 1u << bit;
+                                parity = (parity & ~(1u << bit)) | (ph << bit);
+                            }
+                            if (++st == KS) {
+                                st = 0;
+                                ph ^= 1u;
                             }
                         }
                     }
-                    if (!ok)
-                        break;
-                    if (j >= j0 && ++vst == KS) {
-                        vst = 0;
-                        vph ^= 1u;
-                    }
-                    if (k_ready) {
-                        tc_commit(bar(CF::BAR_KE + kst));
-                        if (++kst == KS) {
-                            kst = 0;
-                            kph ^= 1u;
-                        }
-                    }
+                    qph ^= 1u;
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 }
-                tc_commit(bar(CF::BAR_DRAIN));
-                wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
+                // the answer is taken in even after a failed wait: it lands in this CTA's shared memory
+                const bool answered = __all_sync(0xffffffffu, wait_drain(bar(CF::BAR_CLC), static_cast<uint32_t>(t) & 1u, timeout));
+                if (!ok || !answered)
+                    break;
+                const int next = clc_answer(clc_dst);
+                ok = publish(t + 1, next, &it);
             }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ S = Q K^T
+            // The two issuers' waits pass while the other's products run.  The whole
+            // warp walks the loop and one elected lane issues: what the instructions
+            // are made from stays uniform across the warp.
+            constexpr uint32_t IDESC_QK = mma_idesc_f16(DT, 128, 128, 0, 0);  // Q, K both K-major
+            const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024), k_desc = smem_desc_sw128(sK, 16, 1024);
+            auto kmaj = [](int k) { return static_cast<uint64_t>(((k >> 2) * CF::ATOM_BYTES + (k & 3) * 32) >> 4); };
+            auto wait = [&](int id, uint32_t par) {
+                return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_MMA_DATA)) != 0;
+            };
+            Item it;
+            uint32_t count[2] = {0, 0}, busy = 0, kg = 0;  // blocks of each tile, items with blocks, blocks of K so far
+            bool ok = true;
+            for (int t = 0; ok && take_item(t, &it); ++t) {
+                if (it.j0 >= it.j1)
+                    continue;
+                ok = wait(CF::BAR_QF, busy);
+                for (int j = it.j0; ok && j < it.j1; ++j, ++kg) {
+                    const int st = static_cast<int>(kg % KS);
+                    ok = wait(CF::BAR_KF + st, kg / KS);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ok || !it.visits(i, j))
+                            continue;
+                        // its columns are free: P_i has been read by P V, or S_i by the softmax
+                        const uint32_t c = count[i];
+                        if (c > 0 && !(ok = wait((CF::SEPARATE_P ? CF::BAR_SE : CF::BAR_PV) + i, c - 1)))
+                            break;
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint64_t qd = q_desc + ((i * CF::Q_BYTES) >> 4);
+                            const uint64_t kd = k_desc + ((st * CF::KV_BYTES) >> 4);
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k)
+                                tc_mma_f16(tmem_base + static_cast<uint32_t>(CF::TMEM_S + i * 128), qd + kmaj(k), kd + kmaj(k),
+                                           IDESC_QK, k != 0 ? 1u : 0u);
+                            tc_commit(bar(CF::BAR_SF + i));
+                        }
+                        __syncwarp();
+                        count[i] = c + 1;
+                    }
+                    if (ok && elect_one()) {
+                        tc_commit(bar(CF::BAR_KE + st));
+                        if (j + 1 == it.j1)
+                            tc_commit(bar(CF::BAR_QE));
+                    }
+                    __syncwarp();
+                }
+                ++busy;
+            }
+            if (elect_one())
+                tc_commit(bar(CF::BAR_DRAIN));
             __syncwarp();
+            wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ O += P V
+            constexpr uint32_t IDESC_PV = mma_idesc_f16(DT, 128, D, 0, 1);  // P K-major (TMEM), V N-major
+            const uint64_t v_desc = smem_desc_sw128(sV, CF::ATOM_BYTES, 1024);
+            auto wait = [&](int id, uint32_t par) {
+                return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_MMA_ACC)) != 0;
+            };
+            Item it;
+            uint32_t count[2] = {0, 0}, busy[2] = {0, 0}, vg = 0;  // blocks and items of each tile, blocks of V so far
+            bool ok = true;
+            for (int t = 0; ok && take_item(t, &it); ++t) {
+                for (int j = it.j0; ok && j < it.j1; ++j, ++vg) {
+                    const int st = static_cast<int>(vg % KS);
+                    ok = wait(CF::BAR_VF + st, vg / KS);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ok || !it.visits(i, j))
+                            continue;
+                        const uint32_t c = count[i];
+                        const bool first = j == it.fb[i];
+                        // the last item's O_i has been read before this one's begins
+                        if ((first && busy[i] > 0 && !(ok = wait(CF::BAR_OE + i, busy[i] - 1))) ||
+                            !(ok = wait(CF::BAR_PF + i, c)))
+                            break;
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint64_t vd = v_desc + ((st * CF::KV_BYTES) >> 4);
+#pragma unroll
+                            for (int k = 0; k < CF::BN / 16; ++k)
+                                tc_mma_f16_ts(tmem_base + static_cast<uint32_t>(CF::TMEM_O + i * D),
+                                              tmem_base + static_cast<uint32_t>(CF::p_tile(i) + CF::p_col(k)),
+                                              vd + ((2048 * k) >> 4), IDESC_PV, (!first || k > 0) ? 1u : 0u);
+                            tc_commit(bar(CF::BAR_PV + i));
+                        }
+                        __syncwarp();
+                        count[i] = c + 1;
+                        busy[i] += first ? 1u : 0u;
+                    }
+                    if (ok && elect_one())
+                        tc_commit(bar(CF::BAR_VE + st));
+                    __syncwarp();
+                }
+            }
+            if (elect_one())
+                tc_commit(bar(CF::BAR_DRAIN));
+            __syncwarp();
+            wait_drain(bar(CF::BAR_DRAIN), 0, timeout);
         }
+        __syncwarp();
     } else {
         regs_increase<CF::REGS_SOFTMAX>();
         // ------------------------------------------------------------ softmax and output of one tile
-        const int fb = tile ? first_b[1] : first_b[0], eb = tile ? end_b[1] : end_b[0];
-        check_ok(CF::TMEM_O + tile * D + D <= 512 && eb <= (p.mask.Sk + CF::BN - 1) / CF::BN && bh < BH);
+        constexpr int HN = 64;
+        const int wgi = (warp - 4) >> 2;
+        const int tile = wgi & 1, half = wgi >> 1;
+        const int r = (warp & 3) * 32 + lane;  // row of the tile (Tensor Memory lane)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + tile * 128);
-        const uint32_t o_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + tile * D);
-        auto wait_warp = [&](int id, uint32_t parity) -> bool {
-            const bool w = wait_bounded(bar(id), parity, abort_flag, timeout, ERR_EPILOGUE);
-            return __all_sync(0xffffffffu, w);
+        const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + tile * 128 + HN * half);
+        const uint32_t p_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::p_tile(tile) + CF::p_col(4 * half));
+        const uint32_t o_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + tile * D + half * (D / 2));
+        uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 1024);
+        auto wait_warp = [&](int id, uint32_t par) -> bool {
+            return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_EPILOGUE));
         };
-        const float slope2 = BIAS ? p.score.slopes[h] * 1.4426950408889634f : 0.0f;
-        const int pos = p.mask.q_offset + row;
-        // m: the reference maximum of the row's weights (log2 units); l: sum of the weights against m
-        float m = -INFINITY, l = 0.0f;
+        // this thread's value and its row's in the other half
+        uint32_t swaps = 0;
+        auto other_half = [&](float v, bool *good) {
+            float *mine = mx_smem + (swaps & 1u) * 512 + tile * 256;
+            mine[half * 128 + r] = v;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(CF::BAR_MX + tile));
+            *good = wait_warp(CF::BAR_MX + tile, swaps);
+            ++swaps;
+            return mine[(half ^ 1) * 128 + r];
+        };
+        uint32_t c = 0;  // blocks of this tile so far
+        Item it;
         bool ok = true;
-        for (int j = fb; ok && j < eb; ++j) {
-            const uint32_t jp = static_cast<uint32_t>(j - fb) & 1u;
-            if (!(ok = wait_warp(CF::BAR_SF + tile, jp)))
-                break;
-            tc_fence_after_sync();
-            const int key0 = j * CF::BN;
-            uint32_t sv[128];
-            tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-            tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-            tmem_load_wait();
-            tmem_load_32cols(s_addr + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
-            tmem_load_32cols(s_addr + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
-            // tanh of the capped scores, or biased scores in log2 units, in place of the raw ones
-            const float dist0 = static_cast<float>(pos - key0);
-            auto transform = [&](int half) {
+        for (int t = 0; ok && take_item(t, &it); ++t) {
+            const int fb = tile ? it.fb[1] : it.fb[0], eb = tile ? it.eb[1] : it.eb[0];
+            const int row = it.q0 + tile * CF::BM + r;  // query index
+            const int32_t *docs = p.mask.doc_offsets
+                                      ? p.mask.doc_offsets + static_cast<int64_t>(it.b) * (p.mask.num_docs + 1) : nullptr;
+            const int2 seen = visible_keys(p.mask, docs, it.b, row);
+            const float slope2 = BIAS ? __ldg(p.score.slopes + it.h) * 1.4426950408889634f : 0.0f;
+            const int pos = p.mask.q_offset + row;
+            // m: the reference maximum of the row's weights (log2 units); l: sum of this half's weights against m
+            float m = -INFINITY, l = 0.0f;
+            for (int j = fb; j < eb; ++j, ++c) {
+                if (!(ok = wait_warp(CF::BAR_SF + tile, c)))
+                    break;
+                tc_fence_after_sync();
+                const int key0 = j * CF::BN + HN * half;
+                uint32_t sv[HN];
+                tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                tmem_load_wait();
+                if constexpr (CF::SEPARATE_P) {
+                    // S_i is in registers: its columns may take the next block's
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(CF::BAR_SE + tile));
+                }
+                // tanh of the capped scores, or biased scores in log2 units, in place of the raw ones
                 if constexpr (CAP)
-                    tanh_scores<64>(sv + 64 * half, p.score.cap_arg);
-                if constexpr (!BIAS)
-                    return;
+                    tanh_scores<HN>(sv, p.score.cap_arg);
+                const float to_log2 = CAP ? p.score.cap_log2 : p.score.scale_log2;  // of a score without a bias
+                if constexpr (BIAS) {
+                    const float dist0 = static_cast<float>(pos - key0);
 #pragma unroll
-                for (int e = 64 * half; e < 64 * half + 64; e += 2) {
-                    float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
-                                     splat2(CAP ? p.score.cap_log2 : p.score.scale_log2));
-                    if constexpr (BIAS) {
+                    for (int e = 0; e < HN; e += 2) {
+                        float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), splat2(to_log2));
                         const float2 dist = fadd2(splat2(dist0), make_float2(-static_cast<float>(e), -static_cast<float>(e + 1)));
                         x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
+                        sv[e] = __float_as_uint(x.x);
+                        sv[e + 1] = __float_as_uint(x.y);
                     }
-                    sv[e] = __float_as_uint(x.x);
-                    sv[e + 1] = __float_as_uint(x.y);
                 }
-            };
-            if constexpr (CAP || BIAS)
-                transform(0);
-            float t[16];  // maxima of groups of 8 scores
-            auto maxima = [&](int g0, int g1) {
+                const int nlo = seen.x - key0, nhi = seen.y - key0;
+                if (!__all_sync(0xffffffffu, nlo <= 0 && nhi >= HN)) {
+                    // keys outside the row's interval count neither in the maximum nor in the weights
 #pragma unroll
-                for (int g = g0; g < g1; ++g) {
-                    const float *f = reinterpret_cast<const float *>(&sv[8 * g]);
-                    t[g] = fmax3(fmax3(f[0], f[1], f[2]), fmax3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+                    for (int e = 0; e < HN; ++e)
+                        if (e < nlo || e >= nhi)
+                            sv[e] = __float_as_uint(-INFINITY);
                 }
-            };
-            maxima(0, 8);
-            tmem_load_wait();
-            if constexpr (CAP || BIAS)
-                transform(1);
-            const int nlo = seen.x - key0, nhi = seen.y - key0;
-            if (!__all_sync(0xffffffffu, nlo <= 0 && nhi >= CF::BN)) {
-                // keys outside the row's interval count neither in the maximum nor in the weights
+                float g[8];  // maxima of groups of 8 scores
 #pragma unroll
-                for (int e = 0; e < 128; ++e)
-                    if (e < nlo || e >= nhi)
-                        sv[e] = __float_as_uint(-INFINITY);
-                maxima(0, 8);
-            }
-            maxima(8, 16);
+                for (int i = 0; i < 8; ++i) {
+                    const float *f = reinterpret_cast<const float *>(&sv[8 * i]);
+                    g[i] = fmax3(fmax3(f[0], f[1], f[2]), fmax3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+                }
+                float mx = fmax3(fmax3(g[0], g[1], g[2]), fmax3(g[3], g[4], g[5]), fmaxf(g[6], g[7]));
+                mx = fmaxf(mx, other_half(mx, &ok));
+                if (!ok)
+                    break;
+                if constexpr (!BIAS)
+                    mx *= to_log2;
+                // move the reference maximum only when the weights would exceed 2^8
+                const bool resc = mx > m + CF::RESCALE_LOG2;
+                const float m_new = resc ? mx : m;
+                const float m_ref = m_new == -INFINITY ? 0.0f : m_new;  // no visible key yet: all weights 0
+                const float alpha = resc ? exp2_approx_ftz(m - m_ref) : 1.0f;  // 0 when m is -inf
+                if constexpr (CF::SEPARATE_P) {
+                    // P_i's columns are free once the last P V has read them
+                    if (j > fb && !(ok = wait_warp(CF::BAR_PV + tile, c - 1)))
+                        break;
+                    tc_fence_after_sync();
+                }
+                const float2 negm2 = splat2(-m_ref);
+                float2 part[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
-                t[g] = fmaxf(t[g], t[g + 8]);
-            float mx = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
-            const float to_log2 = CAP ? p.score.cap_log2 : p.score.scale_log2;  // of a score without a bias
-            if constexpr (!BIAS)
-                mx *= to_log2;
-            // move the reference maximum only when the weights would exceed 2^8
-            const bool resc = mx > m + CF::RESCALE_LOG2;
-            const float m_new = resc ? mx : m;
-            const float m_ref = m_new == -INFINITY ? 0.0f : m_new;  // no visible key yet: all weights 0
-            const float alpha = resc ? exp2_approx_ftz(m - m_ref) : 1.0f;  // 0 when m is -inf
-            const float2 negm2 = splat2(-m_ref);
-            float2 part[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int e2 = 0; e2 < 32; ++e2) {
-                    const int e = 64 * g + 2 * e2;
+                for (int e = 0; e < HN; e += 2) {
                     const float2 s = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                     const float2 x = BIAS ? fadd2(s, negm2) : ffma2(s, splat2(to_log2), negm2);
                     const float2 w = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
-                    part[e2 & 3] = fadd2(part[e2 & 3], w);
-                    pk[e2] = pack2<DT>(w.x, w.y);  // keys 2 e2, 2 e2 + 1 of this half: one 32-bit column
+                    part[(e >> 1) & 3] = fadd2(part[(e >> 1) & 3], w);
+                    sv[e / 2] = pack2<DT>(w.x, w.y);  // keys e, e + 1: one 32-bit column
                 }
-                tmem_store_32cols(s_addr + 32 * g, pk);
-            }
-            const float2 ps = fadd2(fadd2(part[0], part[1]), fadd2(part[2], part[3]));
-            l = l * alpha + (ps.x + ps.y);
-            m = m_new;
-            // rows whose maximum moved take O_i down by alpha (O_i holds the
-            // blocks before j, so their P V has to be complete)
-            if (j > fb && __any_sync(0xffffffffu, resc)) {
-                if (!(ok = wait_warp(CF::BAR_PV + tile, jp ^ 1u)))
-                    break;
-                tc_fence_after_sync();
+                tmem_store_32cols(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                const float2 ps = fadd2(fadd2(part[0], part[1]), fadd2(part[2], part[3]));
+                l = l * alpha + (ps.x + ps.y);
+                m = m_new;
+                // rows whose maximum moved take O_i down by alpha, each half its columns.  O_i holds the blocks before
+                // j: with P over S, S(j) was issued behind their P V; else that has just been waited for.
+                if (j > fb && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_load_32cols(o_addr + 32 * c, o);
-                    tmem_load_wait();
+                    for (int k = 0; k < D / 64; ++k) {
+                        uint32_t o[32];
+                        tmem_load_32cols(o_addr + 32 * k, o);
+                        tmem_load_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    tmem_store_32cols(o_addr + 32 * c, o);
-                }
-            }
-            tmem_store_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar(CF::BAR_PF + tile));
-        }
-        // output: O_i / l once the last P V has landed; rows that see no key get 0 and lse -inf
-        if (ok && eb > fb)
-            ok = wait_warp(CF::BAR_PV + tile, static_cast<uint32_t>(eb - fb - 1) & 1u);
-        if (ok) {
-            tc_fence_after_sync();
-            const bool live = row < p.mask.Sq;
-            const bool empty = seen.y <= seen.x || l == 0.0f;
-            const float inv = empty ? 0.0f : 1.0f / l;
-            uint16_t *orow = p.O + b * p.o_batch + h * p.o_head + static_cast<int64_t>(row) * p.o_row;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                if (eb > fb) {
-                    tmem_load_32cols(o_addr + 32 * c, o);
-                    tmem_load_wait();
-                }
-                if (live) {
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (!empty) {
-                            w.x = pack2<DT>(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
-                            w.y = pack2<DT>(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv);
-                            w.z = pack2<DT>(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
-                            w.w = pack2<DT>(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
-                        }
-                        reinterpret_cast<uint4 *>(orow + 32 * c)[v] = w;
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_store_32cols(o_addr + 32 * k, o);
                     }
                 }
+                tmem_store_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(CF::BAR_PF + tile));
             }
-            if (p.lse && live)
-                p.lse[static_cast<int64_t>(bh) * p.mask.Sq + row] =
+            // output: O_i / l once the last P V has landed; rows that see no key get 0 and lse -inf
+            if (ok && eb > fb) {
+                l += other_half(l, &ok);
+                ok = ok && wait_warp(CF::BAR_PV + tile, c - 1);
+            }
+            if (!ok)
+                break;
+            tc_fence_after_sync();
+            const bool empty = seen.y <= seen.x || l == 0.0f;
+            const float inv = empty ? 0.0f : 1.0f / l;
+            const int row0 = it.q0 + tile * CF::BM + (warp & 3) * 32;  // this warp's first row
+#pragma unroll 1
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t o[16];
+                if (eb > fb) {
+                    tmem_load_16cols(o_addr + 16 * k, o);
+                    tmem_load_wait();
+                    if (k + 1 == D / 32) {  // in registers: the next item's O_i may begin
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar(CF::BAR_OE + tile));
+                    }
+                }
+                if (row0 >= p.mask.Sq)
+                    continue;
+                // 32 rows x 16 columns through this warp's buffer; rows behind the tensor's are not written
+                if (lane == 0)
+                    bulk_wait_group_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (!empty) {
+                        w.x = pack2<DT>(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
+                        w.y = pack2<DT>(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv);
+                        w.z = pack2<DT>(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
+                        w.w = pack2<DT>(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
+                    }
+                    out_buf[2 * lane + v] = w;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_4d(&tmap_o, smem_addr(out_buf), half * (D / 2) + 16 * k, row0, it.h, it.b);
+                    bulk_commit_group();
+                }
+            }
+            if (p.lse && half == 0 && row < p.mask.Sq)
+                p.lse[(static_cast<int64_t>(it.b) * p.H + it.h) * p.mask.Sq + row] =
                     empty ? -INFINITY : m * 0.69314718055994531f + logf(l);
         }
+        if (lane == 0)
+            bulk_wait_group<0>();
+        __syncwarp();
     }
 
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 0 && lane == 0 && *abort_flag) {
-        if (q_issued)
-            wait_drain(bar(CF::BAR_Q), 0, timeout);
+        if (issued & 1u)
+            wait_drain(bar(CF::BAR_QF), parity & 1u, timeout);
         for (int s = 0; s < KS; ++s) {
-            if (k_issued & (1u << s))
-                wait_drain(bar(CF::BAR_KF + s), (k_par >> s) & 1u, timeout);
-            if (v_issued & (1u << s))
-                wait_drain(bar(CF::BAR_VF + s), (v_par >> s) & 1u, timeout);
+            if (issued & (1u << (8 + s)))
+                wait_drain(bar(CF::BAR_KF + s), (parity >> (8 + s)) & 1u, timeout);
+            if (issued & (1u << (16 + s)))
+                wait_drain(bar(CF::BAR_VF + s), (parity >> (16 + s)) & 1u, timeout);
         }
     }
     __syncthreads();
