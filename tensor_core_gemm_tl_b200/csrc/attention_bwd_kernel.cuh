@@ -368,13 +368,11 @@ __global__ void __launch_bounds__(640, 1)
             };
             int st = 0;
             uint32_t ph = 0, xph = 0;
-            int4 tl, after;
-            bool ok = next_tile(0, &after);
-            for (int t = 0; ok; ++t) {
-                tl = after;
-                // the next tile is taken before this one's loads wait for room
-                if (tl.x < 0 || !(ok = next_tile(t + 1, &after)))
-                    break;
+            int4 tl;
+            bool ok = next_tile(0, &tl);
+            // The next tile is taken when this one's last loads are out: taken at its start, tiles would be dealt out
+            // regardless of who finishes first.
+            for (int t = 0; ok && tl.x >= 0; ok = ok && next_tile(t + 1, &tl), ++t) {
                 if (tl.w == 0)
                     continue;
                 const int b = tl.y / heads, head = tl.y - b * heads;

@@ -139,47 +139,64 @@ struct ScoreParams {
     const float *slopes;  // [heads], or null
 };
 
-// The N raw scores v to tanh(arg v), in place, N a multiple of 4.
+// t = x p(x^2) of N scores in place, p of degree M - 1 with coefficients c, x = arg v
+template <int N, int M>
+__device__ __forceinline__ void odd_polynomial(uint32_t *v, float arg, const float (&c)[M])
+{
+    float2 k[M];  // coefficients in powers of the raw score: c_i arg^(2 i + 1)
+    float power = arg;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        k[i] = splat2(c[i] * power);
+        power *= arg * arg;
+    }
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 x = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        const float2 u = fmul2(x, x);
+        float2 t = ffma2(u, k[M - 1], k[M - 2]);
+#pragma unroll
+        for (int i = M - 3; i >= 0; --i)
+            t = ffma2(u, t, k[i]);
+        t = fmul2(t, x);
+        v[e] = __float_as_uint(t.x);
+        v[e + 1] = __float_as_uint(t.y);
+    }
+}
+
+// The N raw scores v to tanh(arg v), in place, N a multiple of 4; arg > 0.
 //
-// Where the warp's |arg v| are all at most 1 -- scores inside the cap, the usual
-// case -- tanh x = x p(x^2) with p of degree 6, the minimax fit of csrc/fit_tanh.py
-// (relative error 5e-8): 4.5 multiply-adds a score, two to an instruction, and no
-// special-function operation.  Otherwise tanh x = 1 - 2 / (1 + 2^(2 log2(e) x)),
-// one 2^x a score and one reciprocal for two, of the product of their
-// denominators; the exponent is held below 2^60 (tanh is 1 to 2^-59 there) so that
-// the product stays finite.  Both are absolutely exact to about 2^-22, which is
-// what a score needs: a cap of 50 leaves 1e-5.  The second form alone made a
-// capped forward of 16 heads x 4096^2 x 128 take 150 us.
+// Where the warp's |arg v| are all at most 1/2 -- scores well inside the cap, the
+// usual case -- or at most 1, tanh x = x p(x^2) with p of degree 4 or 6, the
+// minimax fits of csrc/fit_tanh.py (relative errors 1.3e-8 and 5e-8): 3 or 4
+// multiply-adds a score, two to an instruction, and no special-function
+// operation.  Otherwise tanh x = 1 - 2 / (1 + 2^(2 log2(e) x)), one 2^x a score and
+// one reciprocal for two, of the product of their denominators; the exponent is
+// held below 2^60 (tanh is 1 to 2^-59 there) so that the product stays finite.  All
+// are absolutely exact to about 2^-22, which is what a score needs: a cap of 50
+// leaves 1e-5.  (The powers of arg stay in range: a score inside the cap times arg
+// is at most 1, and a cap so far from the scores that arg^13 underflows leaves
+// tanh x = x, which the vanishing coefficients give.)
 template <int N>
 __device__ __forceinline__ void tanh_scores(uint32_t *v, float arg)
 {
     float top = 0.0f;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-        const float2 x = fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), splat2(arg));
-        v[e] = __float_as_uint(x.x);
-        v[e + 1] = __float_as_uint(x.y);
-        top = fmax3(top, fabsf(x.x), fabsf(x.y));
-    }
-    if (__all_sync(0xffffffffu, top <= 1.0f)) {
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-            const float2 x = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-            const float2 u = fmul2(x, x);
-            float2 t = ffma2(u, splat2(0.001041022636f), splat2(-0.006203379112f));
-            t = ffma2(u, t, splat2(0.02028998043f));
-            t = ffma2(u, t, splat2(-0.05345702957f));
-            t = ffma2(u, t, splat2(0.1332520408f));
-            t = ffma2(u, t, splat2(-0.3333283915f));
-            t = ffma2(u, t, splat2(0.9999999502f));
-            t = fmul2(t, x);
-            v[e] = __float_as_uint(t.x);
-            v[e + 1] = __float_as_uint(t.y);
-        }
+    for (int e = 0; e < N; e += 2)
+        top = fmax3(top, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
+    top *= arg;
+    if (__all_sync(0xffffffffu, top <= 0.5f)) {
+        const float c[5] = {0.9999999869f, -0.3333306939f, 0.1332477932f, -0.05298607529f, 0.01713500663f};
+        odd_polynomial<N>(v, arg, c);
+    } else if (__all_sync(0xffffffffu, top <= 1.0f)) {
+        const float c[7] = {0.9999999502f, -0.3333283915f, 0.1332520408f, -0.05345702957f, 0.02028998043f,
+                            -0.006203379112f, 0.001041022636f};
+        odd_polynomial<N>(v, arg, c);
     } else {
+        const float2 arg2 = splat2(2.8853900817779268f * arg);
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-            const float2 z = fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), splat2(2.8853900817779268f));
+            const float2 z = fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), arg2);
             const float2 d = fadd2(make_float2(exp2_approx_ftz(fmin_nan(z.x, 60.0f)), exp2_approx_ftz(fmin_nan(z.y, 60.0f))),
                                    splat2(1.0f));
             const float r = -2.0f * rcp_approx(d.x * d.y);

@@ -76,7 +76,7 @@ using ExFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnEx
 
 struct ExEntry {
     ExFn fn[2][2][2];  // [dtype][capped][biased]
-    int smem, launch_regs;
+    int smem, threads, launch_regs;
 };
 
 template <int D>
@@ -87,7 +87,7 @@ ExEntry make_ex()
               {attention_ex_kernel<CF, 0, true, false>, attention_ex_kernel<CF, 0, true, true>}},
              {{attention_ex_kernel<CF, 1, false, false>, attention_ex_kernel<CF, 1, false, true>},
               {attention_ex_kernel<CF, 1, true, false>, attention_ex_kernel<CF, 1, true, true>}}},
-            CF::SMEM_BYTES, CF::LAUNCH_REGS};
+            CF::SMEM_BYTES, CF::THREADS, CF::LAUNCH_REGS};
 }
 
 const ExEntry kEx64 = make_ex<64>();
@@ -114,7 +114,7 @@ tl_status attention_ex_impl(const void *Q, const void *K, const void *V, void *O
     if (!encode_heads(&tq, Q, dtype, batch, heads, seq_q, head_dim, c.q, 128) ||
         !encode_heads(&tk, K, dtype, batch, c.kv_heads, seq_k, head_dim, c.k, 128) ||
         !encode_heads(&tv, V, dtype, batch, c.kv_heads, seq_k, head_dim, c.v, 128) ||
-        !encode_heads_out(&to, O, dtype, batch, heads, seq_q, head_dim, c.o, 32, 16))
+        !encode_heads_out(&to, O, dtype, batch, heads, seq_q, head_dim, c.o, 32, 32))
         return TL_ERR_CUDA;
     AttnExParams p{};
     p.mask = c.mask;
@@ -125,7 +125,7 @@ tl_status attention_ex_impl(const void *Q, const void *K, const void *V, void *O
     p.num_pairs = static_cast<int32_t>(ceil_div(seq_q, 256));
     p.lse = lse;
     p.timeout_ns = kDefaultTimeoutNs;
-    return launch_overlapped(fn, p.num_pairs * batch * heads, 640, e.smem, stream, tq, tk, tv, to, p);
+    return launch_overlapped(fn, p.num_pairs * batch * heads, e.threads, e.smem, stream, tq, tk, tv, to, p);
 }
 
 } // namespace

@@ -5,28 +5,29 @@
 //     O_i = sum_j w_ij V_j,   w_ij = exp(y_ij - lse_i),   lse_i = log sum_j exp(y_ij)
 //
 // An item is a pair of 128-row query tiles of one head against one stream of
-// 128-key blocks, the tiles in ping-pong: while one tile's scores become weights,
-// the tensor core works on the other.  Tensor Memory holds, per tile, S_i (128
-// fp32 columns) and O_i (D columns); the 16-bit weights P_i are written over S_i
-// (D = 128) or into columns of their own (D = 64, so that the next S_i need not
-// wait for P V).  Each tile visits only the blocks that some of its rows see;
-// inside, only blocks that cut a row's interval pay for masking.
+// 128-key blocks.  A warpgroup turns a tile's scores into weights, a row a thread
+// and 64 keys a step: Tensor Memory holds, per tile, two sets of 64 score columns
+// (the 16-bit weights P are written over the first half of a set) and the sums O
+// (D columns).  While step n becomes weights, the tensor core computes step n + 1's
+// scores and adds step n - 1's P V, so the warpgroup never waits for a product;
+// with one set of 128 columns a tile it did, each block: 1970 clocks a tile and
+// block (and 2500 with two warpgroups a tile, which have to agree on the row's
+// maximum).  Each tile visits only the steps that some of its rows see; inside,
+// only steps that cut a row's interval pay for masking.
 //
-// Two warpgroups share a tile, 64 columns of a row a thread, and agree on the
-// row's maximum through shared memory: four warps on each scheduler hide one
-// another's latencies, which two warps of 128 columns a thread did not (1970
-// clocks a tile and block against 1024 of products).  CTAs are persistent: a CTA
-// that has issued its item's loads takes over one that has not started yet
-// (cluster launch control), so set-up, the masks' ranges and the next item's loads
-// pass beside the work; a CTA an item spent 6 us on them, more than a short
-// document's attention takes.
+// CTAs are persistent: a CTA whose item's loads are out takes over one that has
+// not started yet (cluster launch control), so set-up, the masks' ranges and
+// the next item's loads pass beside the work; a CTA an item spent 6 us on them,
+// more than a short document's attention takes.
 //
-// What bounds it: 2 products of 128 x 128 x D a tile and block (1024 clocks with
-// D = 128 at 4096 multiply-adds a clock and SM) against one 2^x a pair at 16 a
-// clock (1024 clocks); capped scores add the multiply-adds of tanh_scores.
+// What bounds it: 2 products of 128 x 128 x D a tile and block, with D = 128 1024
+// clocks at 4096 multiply-adds a clock and SM (1376, as S in steps of 64 keys reads
+// 48 bytes of operands for every 32 clocks' worth of products), against one 2^x a
+// pair at 16 a clock (1024 clocks); capped scores add the multiply-adds of
+// tanh_scores.
 //
 // Warps: 0 items and TMA loads, 1 issues S (and allocates Tensor Memory), 2 issues
-// P V, 3 idle, 4..19 softmax.  Every wait is bounded.
+// P V, 3 idle, 4..7 softmax of tile 0, 8..11 of tile 1.  Every wait is bounded.
 #pragma once
 
 #include "attention_common.cuh"
@@ -54,36 +55,28 @@ struct AttnExConfig {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
     static constexpr int OFF_V = OFF_K + KS * KV_BYTES;
-    static constexpr int OFF_OUT = OFF_V + KS * KV_BYTES;  // [warp] 32 rows x 16 columns on their way out
-    static constexpr int OFF_BAR = OFF_OUT + 16 * 1024;
+    static constexpr int OFF_OUT = OFF_V + KS * KV_BYTES;  // [warp] 32 rows x 32 columns on their way out
+    static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
     static constexpr int BAR_QF = 0, BAR_QE = 1;
     static constexpr int BAR_KF = 2, BAR_KE = 2 + KS, BAR_VF = 2 + 2 * KS, BAR_VE = 2 + 3 * KS;
-    static constexpr int BAR_SF = 2 + 4 * KS;   // [tile]: S_i in Tensor Memory
-    static constexpr int BAR_SE = BAR_SF + 2;   // [tile]: S_i read into registers (8 warps; separate P only)
-    static constexpr int BAR_PF = BAR_SE + 2;   // [tile]: P_i in Tensor Memory (8 warps)
-    static constexpr int BAR_PV = BAR_PF + 2;   // [tile]: O_i += P_i V completed
-    static constexpr int BAR_MX = BAR_PV + 2;   // [tile]: both halves' maxima (or sums) are in shared memory (8 warps)
-    static constexpr int BAR_OE = BAR_MX + 2;   // [tile]: O_i has been read (8 warps)
+    static constexpr int BAR_SF = 2 + 4 * KS;   // [tile][set]: S in Tensor Memory
+    static constexpr int BAR_PF = BAR_SF + 4;   // [tile][set]: P in Tensor Memory (4 warps)
+    static constexpr int BAR_PV = BAR_PF + 4;   // [tile][set]: O += P V completed
+    static constexpr int BAR_OE = BAR_PV + 4;   // [tile]: O has been read (4 warps)
     static constexpr int BAR_TF = BAR_OE + 2;   // [slot]: an item's description is in shared memory
-    static constexpr int BAR_TE = BAR_TF + 2;   // [slot]: and has been read (18: two MMA issuers, 16 warps)
+    static constexpr int BAR_TE = BAR_TF + 2;   // [slot]: and has been read (10: two MMA issuers, 8 warps)
     static constexpr int BAR_CLC = BAR_TE + 2;  // the answer to a request for another item
     static constexpr int BAR_DRAIN = BAR_CLC + 1;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
     static constexpr int OFF_CLC = OFF_MISC + 16;
-    static constexpr int OFF_ITEMS = OFF_CLC + 16;      // [slot] pair, head, first and end block of each tile
-    static constexpr int OFF_MX = OFF_ITEMS + 2 * 32;   // [block & 1][tile][half][128] floats
-    static constexpr int SMEM_BYTES = OFF_MX + 2 * 2 * 2 * 512 + 1024;
-    static constexpr int THREADS = 640;
-    static constexpr int REGS_CONTROL = 64, REGS_SOFTMAX = 104;
-    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 512 * REGS_SOFTMAX + THREADS - 1) / THREADS;
-    static constexpr bool SEPARATE_P = D == 64;
-    // Tensor Memory columns: S_i at 128 i, O_i at 256 + D i, separate P_i at 384 + 64 i
-    static constexpr int TMEM_S = 0, TMEM_O = 256, TMEM_P = 256 + 2 * D;
-    static_assert(!SEPARATE_P || TMEM_P + 128 <= 512, "Tensor Memory columns");
-    // 16 values of P take 8 columns; over S each half's 64 lie where its scores were
-    __host__ __device__ static constexpr int p_col(int k) { return SEPARATE_P ? 8 * k : (k >> 2) * 64 + (k & 3) * 8; }
-    __host__ __device__ static constexpr int p_tile(int i) { return SEPARATE_P ? TMEM_P + 64 * i : TMEM_S + 128 * i; }
+    static constexpr int OFF_ITEMS = OFF_CLC + 16;      // [slot] pair, head, first and end step of each tile
+    static constexpr int SMEM_BYTES = OFF_ITEMS + 2 * 32 + 1024;
+    static constexpr int THREADS = 384;
+    static constexpr int REGS_CONTROL = 104, REGS_SOFTMAX = 200;
+    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
+    static constexpr int BS = 64;               // keys a step
+    static constexpr int TMEM_S = 0, TMEM_O = 256;  // set h of tile i at 128 i + 64 h, O at 256 + D i
     static constexpr float RESCALE_LOG2 = 8.0f;     // m moves when a row maximum exceeds it by 2^8
     static_assert(D == 64 || D == 128, "head dim");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -116,7 +109,7 @@ __device__ __forceinline__ int clc_answer(uint32_t src)
 }
 
 template <class CF, int DT, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(640, 1)
+__global__ void __launch_bounds__(384, 1)
     attention_ex_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
                         const AttnExParams p)
@@ -136,7 +129,6 @@ __global__ void __launch_bounds__(640, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + CF::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int4 *item_slots = reinterpret_cast<int4 *>(smem + CF::OFF_ITEMS);
-    float *mx_smem = reinterpret_cast<float *>(smem + CF::OFF_MX);
 
     if (threadIdx.x == 0) {
         mbar_init(bar(CF::BAR_QF), 1);
@@ -148,14 +140,14 @@ __global__ void __launch_bounds__(640, 1)
             mbar_init(bar(CF::BAR_VE + s), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(CF::BAR_SF + i), 1);
-            mbar_init(bar(CF::BAR_SE + i), 8);
-            mbar_init(bar(CF::BAR_PF + i), 8);
-            mbar_init(bar(CF::BAR_PV + i), 1);
-            mbar_init(bar(CF::BAR_MX + i), 8);
-            mbar_init(bar(CF::BAR_OE + i), 8);
+            mbar_init(bar(CF::BAR_OE + i), 4);
             mbar_init(bar(CF::BAR_TF + i), 1);
-            mbar_init(bar(CF::BAR_TE + i), 18);
+            mbar_init(bar(CF::BAR_TE + i), 10);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(CF::BAR_SF + i), 1);
+            mbar_init(bar(CF::BAR_PF + i), 4);
+            mbar_init(bar(CF::BAR_PV + i), 1);
         }
         mbar_init(bar(CF::BAR_CLC), 1);
         mbar_init(bar(CF::BAR_DRAIN), 2);
@@ -181,24 +173,24 @@ __global__ void __launch_bounds__(640, 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // An item as every role sees it: the pair and head, and the key blocks
-    // [first, end) of each tile (empty: first = end = 0)
+    // An item as every role sees it: the pair and head, the steps of 64 keys
+    // [fs, es) each tile visits (empty: 0, 0) and the blocks of 128 that hold them
     struct Item {
-        int b, h, q0, fb[2], eb[2], j0, j1;
-        __device__ bool visits(int i, int j) const { return i ? j >= fb[1] && j < eb[1] : j >= fb[0] && j < eb[0]; }
+        int b, h, q0, fs[2], es[2], j0, j1;
+        __device__ bool visits(int i, int n) const { return i ? n >= fs[1] && n < es[1] : n >= fs[0] && n < es[0]; }
     };
     auto unpack = [&](const int4 &x, const int4 &y) {
         Item it;
         it.b = x.y / p.H;
         it.h = x.y - it.b * p.H;
         it.q0 = x.x * 2 * CF::BM;
-        it.fb[0] = x.z;
-        it.eb[0] = x.w;
-        it.fb[1] = y.x;
-        it.eb[1] = y.y;
+        it.fs[0] = x.z;
+        it.es[0] = x.w;
+        it.fs[1] = y.x;
+        it.es[1] = y.y;
         const bool e0 = x.w > x.z, e1 = y.y > y.x;
-        it.j0 = e0 && e1 ? min(x.z, y.x) : e0 ? x.z : y.x;
-        it.j1 = max(x.w, y.y);
+        it.j0 = (e0 && e1 ? min(x.z, y.x) : e0 ? x.z : y.x) >> 1;
+        it.j1 = (max(x.w, y.y) + 1) >> 1;
         return it;
     };
     auto take_item = [&](int t, Item *out) {
@@ -226,7 +218,7 @@ __global__ void __launch_bounds__(640, 1)
             auto wait = [&](int id, uint32_t par) {
                 return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_PRODUCER)) != 0;
             };
-            // Item `index` (-1: none) as the t-th: which blocks its tiles visit, for the others
+            // Item `index` (-1: none) as the t-th: which steps its tiles visit, for the others
             auto publish = [&](int t, int index, Item *out) {
                 if (t >= 2 && !wait(CF::BAR_TE + (t & 1), static_cast<uint32_t>(t >> 1) - 1))
                     return false;
@@ -252,12 +244,12 @@ __global__ void __launch_bounds__(640, 1)
                     const int lo0 = __shfl_sync(0xffffffffu, seen.x, 0), hi0 = __shfl_sync(0xffffffffu, seen.y, 1);
                     const int lo1 = __shfl_sync(0xffffffffu, seen.x, 2), hi1 = __shfl_sync(0xffffffffu, seen.y, 3);
                     if (hi0 > lo0) {
-                        x.z = lo0 / CF::BN;
-                        x.w = (hi0 + CF::BN - 1) / CF::BN;
+                        x.z = lo0 / CF::BS;
+                        x.w = (hi0 + CF::BS - 1) / CF::BS;
                     }
                     if (hi1 > lo1) {
-                        y.x = lo1 / CF::BN;
-                        y.y = (hi1 + CF::BN - 1) / CF::BN;
+                        y.x = lo1 / CF::BS;
+                        y.y = (hi1 + CF::BS - 1) / CF::BS;
                     }
                     *out = unpack(x, y);
                 }
@@ -274,13 +266,6 @@ __global__ void __launch_bounds__(640, 1)
             uint32_t ph = 0, qph = 0;
             bool ok = publish(0, static_cast<int>(blockIdx.x), &it);
             for (int t = 0; ok; ++t) {
-                // the request for the next item is under way while this one's loads go out
-                if (lane == 0) {
-                    fence_proxy_async_smem();
-                    mbar_arrive_expect_tx(bar(CF::BAR_CLC), 16);
-                    clc_request(clc_dst, bar(CF::BAR_CLC));
-                }
-                __syncwarp();
                 if (it.j0 < it.j1) {
                     const int hk = it.h / p.group;
                     if (lane == 0) {
@@ -321,9 +306,19 @@ __global__ void __launch_bounds__(640, 1)
                     qph ^= 1u;
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 }
-                // the answer is taken in even after a failed wait: it lands in this CTA's shared memory
+                if (!ok)
+                    break;
+                // The next item is asked for when this one's last loads are out: the ring's depth before its end, which
+                // covers the answer.  Asked for at its start, items would be dealt out regardless of who finishes first
+                // (16 capped causal heads x 4096 on 148 CTAs: 162 us against 120).
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(bar(CF::BAR_CLC), 16);
+                    clc_request(clc_dst, bar(CF::BAR_CLC));
+                }
+                __syncwarp();
                 const bool answered = __all_sync(0xffffffffu, wait_drain(bar(CF::BAR_CLC), static_cast<uint32_t>(t) & 1u, timeout));
-                if (!ok || !answered)
+                if (!answered)
                     break;
                 const int next = clc_answer(clc_dst);
                 ok = publish(t + 1, next, &it);
@@ -333,14 +328,14 @@ __global__ void __launch_bounds__(640, 1)
             // The two issuers' waits pass while the other's products run.  The whole
             // warp walks the loop and one elected lane issues: what the instructions
             // are made from stays uniform across the warp.
-            constexpr uint32_t IDESC_QK = mma_idesc_f16(DT, 128, 128, 0, 0);  // Q, K both K-major
+            constexpr uint32_t IDESC_QK = mma_idesc_f16(DT, 128, CF::BS, 0, 0);  // Q, K both K-major
             const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024), k_desc = smem_desc_sw128(sK, 16, 1024);
             auto kmaj = [](int k) { return static_cast<uint64_t>(((k >> 2) * CF::ATOM_BYTES + (k & 3) * 32) >> 4); };
             auto wait = [&](int id, uint32_t par) {
                 return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_MMA_DATA)) != 0;
             };
             Item it;
-            uint32_t count[2] = {0, 0}, busy = 0, kg = 0;  // blocks of each tile, items with blocks, blocks of K so far
+            uint32_t count[2][2] = {{0, 0}, {0, 0}}, busy = 0, kg = 0;  // steps of each tile and set, items with blocks, blocks of K so far
             bool ok = true;
             for (int t = 0; ok && take_item(t, &it); ++t) {
                 if (it.j0 >= it.j1)
@@ -350,25 +345,26 @@ __global__ void __launch_bounds__(640, 1)
                     const int st = static_cast<int>(kg % KS);
                     ok = wait(CF::BAR_KF + st, kg / KS);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ok || !it.visits(i, j))
+                    for (int q = 0; q < 4; ++q) {
+                        const int set = q >> 1, i = q & 1;
+                        if (!ok || !it.visits(i, 2 * j + set))
                             continue;
-                        // its columns are free: P_i has been read by P V, or S_i by the softmax
-                        const uint32_t c = count[i];
-                        if (c > 0 && !(ok = wait((CF::SEPARATE_P ? CF::BAR_SE : CF::BAR_PV) + i, c - 1)))
-                            break;
+                        // its columns are free: the P over them has been read by P V
+                        const uint32_t c = count[i][set];
+                        if (c > 0 && !(ok = wait(CF::BAR_PV + 2 * i + set, c - 1)))
+                            continue;
                         tc_fence_after_sync();
                         if (elect_one()) {
                             const uint64_t qd = q_desc + ((i * CF::Q_BYTES) >> 4);
-                            const uint64_t kd = k_desc + ((st * CF::KV_BYTES) >> 4);
+                            const uint64_t kd = k_desc + ((st * CF::KV_BYTES + set * CF::BS * 128) >> 4);
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k)
-                                tc_mma_f16(tmem_base + static_cast<uint32_t>(CF::TMEM_S + i * 128), qd + kmaj(k), kd + kmaj(k),
-                                           IDESC_QK, k != 0 ? 1u : 0u);
-                            tc_commit(bar(CF::BAR_SF + i));
+                                tc_mma_f16(tmem_base + static_cast<uint32_t>(CF::TMEM_S + i * 128 + set * CF::BS), qd + kmaj(k),
+                                           kd + kmaj(k), IDESC_QK, k != 0 ? 1u : 0u);
+                            tc_commit(bar(CF::BAR_SF + 2 * i + set));
                         }
                         __syncwarp();
-                        count[i] = c + 1;
+                        count[i][set] = c + 1;
                     }
                     if (ok && elect_one()) {
                         tc_commit(bar(CF::BAR_KE + st));
@@ -391,34 +387,35 @@ __global__ void __launch_bounds__(640, 1)
                 return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_MMA_ACC)) != 0;
             };
             Item it;
-            uint32_t count[2] = {0, 0}, busy[2] = {0, 0}, vg = 0;  // blocks and items of each tile, blocks of V so far
+            uint32_t count[2][2] = {{0, 0}, {0, 0}}, busy[2] = {0, 0}, vg = 0;  // steps and items of each tile, blocks of V so far
             bool ok = true;
             for (int t = 0; ok && take_item(t, &it); ++t) {
                 for (int j = it.j0; ok && j < it.j1; ++j, ++vg) {
                     const int st = static_cast<int>(vg % KS);
                     ok = wait(CF::BAR_VF + st, vg / KS);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ok || !it.visits(i, j))
+                    for (int q = 0; q < 4; ++q) {
+                        const int set = q >> 1, i = q & 1;
+                        if (!ok || !it.visits(i, 2 * j + set))
                             continue;
-                        const uint32_t c = count[i];
-                        const bool first = j == it.fb[i];
-                        // the last item's O_i has been read before this one's begins
+                        const uint32_t c = count[i][set];
+                        const bool first = 2 * j + set == it.fs[i];
+                        // the last item's O has been read before this one's begins
                         if ((first && busy[i] > 0 && !(ok = wait(CF::BAR_OE + i, busy[i] - 1))) ||
-                            !(ok = wait(CF::BAR_PF + i, c)))
-                            break;
+                            !(ok = wait(CF::BAR_PF + 2 * i + set, c)))
+                            continue;
                         tc_fence_after_sync();
                         if (elect_one()) {
-                            const uint64_t vd = v_desc + ((st * CF::KV_BYTES) >> 4);
+                            const uint64_t vd = v_desc + ((st * CF::KV_BYTES + set * CF::BS * 128) >> 4);
 #pragma unroll
-                            for (int k = 0; k < CF::BN / 16; ++k)
+                            for (int k = 0; k < CF::BS / 16; ++k)
                                 tc_mma_f16_ts(tmem_base + static_cast<uint32_t>(CF::TMEM_O + i * D),
-                                              tmem_base + static_cast<uint32_t>(CF::p_tile(i) + CF::p_col(k)),
+                                              tmem_base + static_cast<uint32_t>(CF::TMEM_S + i * 128 + set * CF::BS + 8 * k),
                                               vd + ((2048 * k) >> 4), IDESC_PV, (!first || k > 0) ? 1u : 0u);
-                            tc_commit(bar(CF::BAR_PV + i));
+                            tc_commit(bar(CF::BAR_PV + 2 * i + set));
                         }
                         __syncwarp();
-                        count[i] = c + 1;
+                        count[i][set] = c + 1;
                         busy[i] += first ? 1u : 0u;
                     }
                     if (ok && elect_one())
@@ -435,59 +432,41 @@ __global__ void __launch_bounds__(640, 1)
     } else {
         regs_increase<CF::REGS_SOFTMAX>();
         // ------------------------------------------------------------ softmax and output of one tile
-        constexpr int HN = 64;
-        const int wgi = (warp - 4) >> 2;
-        const int tile = wgi & 1, half = wgi >> 1;
+        constexpr int HN = CF::BS;
+        const int tile = (warp - 4) >> 2;
         const int r = (warp & 3) * 32 + lane;  // row of the tile (Tensor Memory lane)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + tile * 128 + HN * half);
-        const uint32_t p_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::p_tile(tile) + CF::p_col(4 * half));
-        const uint32_t o_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + tile * D + half * (D / 2));
-        uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 1024);
+        const uint32_t s_addr0 = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + tile * 128);
+        const uint32_t o_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + tile * D);
+        uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 2048);
         auto wait_warp = [&](int id, uint32_t par) -> bool {
             return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_EPILOGUE));
         };
-        // this thread's value and its row's in the other half
-        uint32_t swaps = 0;
-        auto other_half = [&](float v, bool *good) {
-            float *mine = mx_smem + (swaps & 1u) * 512 + tile * 256;
-            mine[half * 128 + r] = v;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar(CF::BAR_MX + tile));
-            *good = wait_warp(CF::BAR_MX + tile, swaps);
-            ++swaps;
-            return mine[(half ^ 1) * 128 + r];
-        };
-        uint32_t c = 0;  // blocks of this tile so far
+        uint32_t count[2] = {0, 0};  // steps of this tile so far, by set
         Item it;
         bool ok = true;
         for (int t = 0; ok && take_item(t, &it); ++t) {
-            const int fb = tile ? it.fb[1] : it.fb[0], eb = tile ? it.eb[1] : it.eb[0];
+            const int fs = tile ? it.fs[1] : it.fs[0], es = tile ? it.es[1] : it.es[0];
             const int row = it.q0 + tile * CF::BM + r;  // query index
             const int32_t *docs = p.mask.doc_offsets
                                       ? p.mask.doc_offsets + static_cast<int64_t>(it.b) * (p.mask.num_docs + 1) : nullptr;
             const int2 seen = visible_keys(p.mask, docs, it.b, row);
             const float slope2 = BIAS ? __ldg(p.score.slopes + it.h) * 1.4426950408889634f : 0.0f;
             const int pos = p.mask.q_offset + row;
-            // m: the reference maximum of the row's weights (log2 units); l: sum of this half's weights against m
+            // m: the reference maximum of the row's weights (log2 units); l: sum of the weights against m
             float m = -INFINITY, l = 0.0f;
-            for (int j = fb; j < eb; ++j, ++c) {
-                if (!(ok = wait_warp(CF::BAR_SF + tile, c)))
+            for (int n = fs; n < es; ++n) {
+                const int set = n & 1;
+                const uint32_t c = set ? count[1] : count[0];
+                if (!(ok = wait_warp(CF::BAR_SF + 2 * tile + set, c)))
                     break;
                 tc_fence_after_sync();
-                const int key0 = j * CF::BN + HN * half;
+                const uint32_t s_addr = s_addr0 + static_cast<uint32_t>(CF::BS * set);
+                const int key0 = n * CF::BS;
                 uint32_t sv[HN];
                 tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
                 tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                 tmem_load_wait();
-                if constexpr (CF::SEPARATE_P) {
-                    // S_i is in registers: its columns may take the next block's
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar(CF::BAR_SE + tile));
-                }
                 // tanh of the capped scores, or biased scores in log2 units, in place of the raw ones
                 if constexpr (CAP)
                     tanh_scores<HN>(sv, p.score.cap_arg);
@@ -518,9 +497,6 @@ __global__ void __launch_bounds__(640, 1)
                     g[i] = fmax3(fmax3(f[0], f[1], f[2]), fmax3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
                 }
                 float mx = fmax3(fmax3(g[0], g[1], g[2]), fmax3(g[3], g[4], g[5]), fmaxf(g[6], g[7]));
-                mx = fmaxf(mx, other_half(mx, &ok));
-                if (!ok)
-                    break;
                 if constexpr (!BIAS)
                     mx *= to_log2;
                 // move the reference maximum only when the weights would exceed 2^8
@@ -528,12 +504,6 @@ __global__ void __launch_bounds__(640, 1)
                 const float m_new = resc ? mx : m;
                 const float m_ref = m_new == -INFINITY ? 0.0f : m_new;  // no visible key yet: all weights 0
                 const float alpha = resc ? exp2_approx_ftz(m - m_ref) : 1.0f;  // 0 when m is -inf
-                if constexpr (CF::SEPARATE_P) {
-                    // P_i's columns are free once the last P V has read them
-                    if (j > fb && !(ok = wait_warp(CF::BAR_PV + tile, c - 1)))
-                        break;
-                    tc_fence_after_sync();
-                }
                 const float2 negm2 = splat2(-m_ref);
                 float2 part[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
 #pragma unroll
@@ -544,15 +514,18 @@ __global__ void __launch_bounds__(640, 1)
                     part[(e >> 1) & 3] = fadd2(part[(e >> 1) & 3], w);
                     sv[e / 2] = pack2<DT>(w.x, w.y);  // keys e, e + 1: one 32-bit column
                 }
-                tmem_store_32cols(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                tmem_store_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
                 const float2 ps = fadd2(fadd2(part[0], part[1]), fadd2(part[2], part[3]));
                 l = l * alpha + (ps.x + ps.y);
                 m = m_new;
-                // rows whose maximum moved take O_i down by alpha, each half its columns.  O_i holds the blocks before
-                // j: with P over S, S(j) was issued behind their P V; else that has just been waited for.
-                if (j > fb && __any_sync(0xffffffffu, resc)) {
+                // rows whose maximum moved take O down by alpha once it holds all steps before n (those before
+                // n - 1 are in it: S(n - 1) was issued behind the P V of n - 3, S(n) behind that of n - 2)
+                if (n > fs && __any_sync(0xffffffffu, resc)) {
+                    if (!(ok = wait_warp(CF::BAR_PV + 2 * tile + (set ^ 1), (set ? count[0] : count[1]) - 1)))
+                        break;
+                    tc_fence_after_sync();
 #pragma unroll 1
-                    for (int k = 0; k < D / 64; ++k) {
+                    for (int k = 0; k < D / 32; ++k) {
                         uint32_t o[32];
                         tmem_load_32cols(o_addr + 32 * k, o);
                         tmem_load_wait();
@@ -566,13 +539,17 @@ __global__ void __launch_bounds__(640, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar(CF::BAR_PF + tile));
+                    mbar_arrive(bar(CF::BAR_PF + 2 * tile + set));
+                if (set)
+                    ++count[1];
+                else
+                    ++count[0];
             }
-            // output: O_i / l once the last P V has landed; rows that see no key get 0 and lse -inf
-            if (ok && eb > fb) {
-                l += other_half(l, &ok);
-                ok = ok && wait_warp(CF::BAR_PV + tile, c - 1);
-            }
+            // output: O / l once the last P V of both sets have landed; rows that see no key get 0 and lse -inf
+#pragma unroll
+            for (int set = 0; set < 2; ++set)
+                if (ok && count[set] > 0)
+                    ok = wait_warp(CF::BAR_PV + 2 * tile + set, count[set] - 1);
             if (!ok)
                 break;
             tc_fence_after_sync();
@@ -581,11 +558,11 @@ __global__ void __launch_bounds__(640, 1)
             const int row0 = it.q0 + tile * CF::BM + (warp & 3) * 32;  // this warp's first row
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
-                uint32_t o[16];
-                if (eb > fb) {
-                    tmem_load_16cols(o_addr + 16 * k, o);
+                uint32_t o[32];
+                if (es > fs) {
+                    tmem_load_32cols(o_addr + 32 * k, o);
                     tmem_load_wait();
-                    if (k + 1 == D / 32) {  // in registers: the next item's O_i may begin
+                    if (k + 1 == D / 32) {  // in registers: the next item's O may begin
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0)
@@ -594,12 +571,12 @@ __global__ void __launch_bounds__(640, 1)
                 }
                 if (row0 >= p.mask.Sq)
                     continue;
-                // 32 rows x 16 columns through this warp's buffer; rows behind the tensor's are not written
+                // 32 rows x 32 columns through this warp's buffer; rows behind the tensor's are not written
                 if (lane == 0)
                     bulk_wait_group_read<0>();
                 __syncwarp();
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
+                for (int v = 0; v < 4; ++v) {
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (!empty) {
                         w.x = pack2<DT>(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
@@ -607,16 +584,16 @@ __global__ void __launch_bounds__(640, 1)
                         w.z = pack2<DT>(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
                         w.w = pack2<DT>(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
                     }
-                    out_buf[2 * lane + v] = w;
+                    out_buf[4 * lane + v] = w;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_4d(&tmap_o, smem_addr(out_buf), half * (D / 2) + 16 * k, row0, it.h, it.b);
+                    tma_store_4d(&tmap_o, smem_addr(out_buf), 32 * k, row0, it.h, it.b);
                     bulk_commit_group();
                 }
             }
-            if (p.lse && half == 0 && row < p.mask.Sq)
+            if (p.lse && row < p.mask.Sq)
                 p.lse[(static_cast<int64_t>(it.b) * p.H + it.h) * p.mask.Sq + row] =
                     empty ? -INFINITY : m * 0.69314718055994531f + logf(l);
         }
