@@ -109,6 +109,32 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
     const int b = bh / p.H, h = bh % p.H;
     if (blockIdx.x == 0 && threadIdx.x < 2)
         p.next[threadIdx.x] = 0;
+    // all of a thread's words first: 2 rows x D / 64 words of O and of dO in flight
+    constexpr int RN = kBwdCols / 32, WN = D / 64;
+    float top = 0.0f;
+    const int sub = threadIdx.x & 7;
+    uint4 wo[RN][WN], wg[RN][WN];
+    float l[RN];
+#pragma unroll
+    for (int k = 0; k < RN; ++k) {
+        const int i = qb * kBwdCols + (threadIdx.x >> 3) + 32 * k;
+        l[k] = -INFINITY;
+        if (i < p.mask.Sq) {
+            const uint16_t *o = p.O + b * p.so[0] + h * p.so[1] + static_cast<int64_t>(i) * p.so[2];
+            const uint16_t *g = p.dO + b * p.sdo[0] + h * p.sdo[1] + static_cast<int64_t>(i) * p.sdo[2];
+#pragma unroll
+            for (int c = 0; c < WN; ++c) {
+                wo[k][c] = __ldg(reinterpret_cast<const uint4 *>(o + 64 * c + 8 * sub));
+                wg[k][c] = __ldg(reinterpret_cast<const uint4 *>(g + 64 * c + 8 * sub));
+            }
+            if (sub == 0)
+                l[k] = p.lse[static_cast<int64_t>(bh) * p.mask.Sq + i];
+        } else {
+#pragma unroll
+            for (int c = 0; c < WN; ++c)
+                wo[k][c] = wg[k][c] = make_uint4(0, 0, 0, 0);
+        }
+    }
     const int32_t *docs = p.mask.doc_offsets
                               ? p.mask.doc_offsets + static_cast<int64_t>(b) * (p.mask.num_docs + 1) : nullptr;
     if (h == 0) {
@@ -139,39 +165,30 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
         if (threadIdx.x == 0)
             p.ranges[static_cast<int64_t>(b) * p.nqb + qb] = make_int4(red[0], red[1], red[2], red[3]);
     }
-    float top = 0.0f;
-    const int sub = threadIdx.x & 7;
 #pragma unroll
-    for (int r = threadIdx.x >> 3; r < kBwdCols; r += 32) {
-        const int i = qb * kBwdCols + r;
+    for (int k = 0; k < RN; ++k) {
         float sum = 0.0f;
-        if (i < p.mask.Sq) {
-            const uint16_t *o = p.O + b * p.so[0] + h * p.so[1] + static_cast<int64_t>(i) * p.so[2];
-            const uint16_t *g = p.dO + b * p.sdo[0] + h * p.sdo[1] + static_cast<int64_t>(i) * p.sdo[2];
 #pragma unroll
-            for (int c = sub * 8; c < D; c += 64) {
-                const uint4 wo = __ldg(reinterpret_cast<const uint4 *>(o + c));
-                const uint4 wg = __ldg(reinterpret_cast<const uint4 *>(g + c));
-                const uint32_t ao[4] = {wo.x, wo.y, wo.z, wo.w}, ag[4] = {wg.x, wg.y, wg.z, wg.w};
+        for (int c = 0; c < WN; ++c) {
+            const uint32_t ao[4] = {wo[k][c].x, wo[k][c].y, wo[k][c].z, wo[k][c].w};
+            const uint32_t ag[4] = {wg[k][c].x, wg[k][c].y, wg[k][c].z, wg[k][c].w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float g0 = to_float<DT>(static_cast<uint16_t>(ag[e] & 0xFFFFu));
-                    const float g1 = to_float<DT>(static_cast<uint16_t>(ag[e] >> 16));
-                    sum = fmaf(g0, to_float<DT>(static_cast<uint16_t>(ao[e] & 0xFFFFu)), sum);
-                    sum = fmaf(g1, to_float<DT>(static_cast<uint16_t>(ao[e] >> 16)), sum);
-                    if constexpr (DT == 0)
-                        top = fmaxf(top, fmaxf(fabsf(g0), fabsf(g1)));
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float g0 = to_float<DT>(static_cast<uint16_t>(ag[e] & 0xFFFFu));
+                const float g1 = to_float<DT>(static_cast<uint16_t>(ag[e] >> 16));
+                sum = fmaf(g0, to_float<DT>(static_cast<uint16_t>(ao[e] & 0xFFFFu)), sum);
+                sum = fmaf(g1, to_float<DT>(static_cast<uint16_t>(ao[e] >> 16)), sum);
+                if constexpr (DT == 0)
+                    top = fmaxf(top, fmaxf(fabsf(g0), fabsf(g1)));
             }
         }
 #pragma unroll
         for (int off = 4; off > 0; off >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (sub == 0) {
-            const float l = i < p.mask.Sq ? p.lse[static_cast<int64_t>(bh) * p.mask.Sq + i] : -INFINITY;
-            float *rows = p.rows + (static_cast<int64_t>(bh) * p.nqb + qb) * 2 * kBwdCols;
-            rows[r] = l == -INFINITY ? -INFINITY : kPShift<DT> - l * 1.4426950408889634f;
-            rows[kBwdCols + r] = l == -INFINITY ? 0.0f : -sum;
+            float *rows = p.rows + (static_cast<int64_t>(bh) * p.nqb + qb) * 2 * kBwdCols + (threadIdx.x >> 3) + 32 * k;
+            rows[0] = l[k] == -INFINITY ? -INFINITY : kPShift<DT> - l[k] * 1.4426950408889634f;
+            rows[kBwdCols] = l[k] == -INFINITY ? 0.0f : -sum;
         }
     }
     if constexpr (DT == 0) {

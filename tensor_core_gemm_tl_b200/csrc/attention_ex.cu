@@ -74,8 +74,11 @@ namespace {
 
 using ExFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnExParams);
 
+using JoinFn = void (*)(AttnJoinParams);
+
 struct ExEntry {
     ExFn fn[2][2][2];  // [dtype][capped][biased]
+    JoinFn join[2];    // [dtype]
     int smem, threads, launch_regs;
 };
 
@@ -87,6 +90,7 @@ ExEntry make_ex()
               {attention_ex_kernel<CF, 0, true, false>, attention_ex_kernel<CF, 0, true, true>}},
              {{attention_ex_kernel<CF, 1, false, false>, attention_ex_kernel<CF, 1, false, true>},
               {attention_ex_kernel<CF, 1, true, false>, attention_ex_kernel<CF, 1, true, true>}}},
+            {attention_join_kernel<0, D>, attention_join_kernel<1, D>},
             CF::SMEM_BYTES, CF::THREADS, CF::LAUNCH_REGS};
 }
 
@@ -125,7 +129,50 @@ tl_status attention_ex_impl(const void *Q, const void *K, const void *V, void *O
     p.num_pairs = static_cast<int32_t>(ceil_div(seq_q, 256));
     p.lse = lse;
     p.timeout_ns = kDefaultTimeoutNs;
-    return launch_overlapped(fn, p.num_pairs * batch * heads, e.threads, e.smem, stream, tq, tk, tv, to, p);
+    const int64_t items = p.num_pairs * batch * heads;
+    // Split the keys where at most half the SMs would have an item and the longest has four blocks at least: a block
+    // takes a CTA about 2 us, the joining of the splits about 4 (measured: 8 items of 9 blocks 30 -> 15 us; with one
+    // item to two SMs and 4 blocks both ways take the same time).  Causal items differ in length and the longest decides
+    // as long as there is one SM for each: two splits then (measured: 96 items of up to 8 blocks 31 -> 27 us).
+    const int64_t blocks = ceil_div(seq_k, 128);
+    p.splits = 1;
+    if (2 * items <= d->num_sms && blocks >= 4) {
+        const int64_t most = d->num_sms / items;
+        p.splits = static_cast<int32_t>(most < blocks ? most : blocks);
+    } else if (items <= d->num_sms && c.mask.causal && blocks >= 8) {
+        p.splits = 2;
+    }
+    if (p.splits == 1)
+        return launch_overlapped(fn, items, e.threads, e.smem, stream, tq, tk, tv, to, p);
+    const int64_t slots = items * p.splits * 2;
+    const int64_t o_bytes = slots * head_dim * 128 * 4;
+    if ((st = ensure_pool(d)) != TL_OK)
+        return st;
+    void *ws = nullptr;
+    if (cudaMallocFromPoolAsync(&ws, static_cast<size_t>(o_bytes + slots * 128 * 8), d->pool, stream) != cudaSuccess)
+        return TL_ERR_CUDA;
+    p.part_o = static_cast<float4 *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + o_bytes);
+    AttnJoinParams j{};
+    j.H = p.H;
+    j.Sq = c.mask.Sq;
+    j.num_pairs = p.num_pairs;
+    j.BH = static_cast<int32_t>(batch * heads);
+    j.splits = p.splits;
+    j.causal = c.mask.causal;
+    j.part_o = p.part_o;
+    j.part_ml = p.part_ml;
+    j.O = static_cast<uint16_t *>(O);
+    j.o_batch = c.o.s[0];
+    j.o_head = c.o.s[1];
+    j.o_row = c.o.s[2];
+    j.lse = lse;
+    st = launch_overlapped(fn, items * p.splits, e.threads, e.smem, stream, tq, tk, tv, to, p);
+    if (st == TL_OK)
+        st = launch_overlapped(e.join[dtype], items * 8, 256, 0, stream, j);
+    if (cudaFreeAsync(ws, stream) != cudaSuccess && st == TL_OK)
+        st = TL_ERR_CUDA;
+    return st;
 }
 
 } // namespace

@@ -20,6 +20,11 @@
 // the next item's loads pass beside the work; a CTA an item spent 6 us on them,
 // more than a short document's attention takes.
 //
+// Where items are few (a short chunk of a long prompt) the blocks of each are split
+// over several CTAs, which leave fp32 sums with their maxima and
+// attention_join_kernel adds in the order of the keys: 8 heads, 77 queries x 1101
+// keys, went from 30 to 15 us.
+//
 // What bounds it: 2 products of 128 x 128 x D a tile and block, with D = 128 1024
 // clocks at 4096 multiply-adds a clock and SM (1376, as S in steps of 64 keys reads
 // 48 bytes of operands for every 32 clocks' worth of products), against one 2^x a
@@ -39,6 +44,9 @@ struct AttnExParams {
     ScoreParams score;
     int32_t B, H, group;     // batch, query heads, query heads per key/value head
     int32_t num_pairs;       // pairs of 128-row query tiles
+    int32_t splits;          // CTAs the keys of an item are split over
+    float4 *part_o;          // splits > 1: [item][split][tile][D / 4][128]
+    float2 *part_ml;         // [item][split][tile][128]: maximum (log2 units), sum
     float *lse;              // [B][H][Sq] natural log, or null
     uint64_t timeout_ns;
 };
@@ -176,7 +184,7 @@ __global__ void __launch_bounds__(384, 1)
     // An item as every role sees it: the pair and head, the steps of 64 keys
     // [fs, es) each tile visits (empty: 0, 0) and the blocks of 128 that hold them
     struct Item {
-        int b, h, q0, fs[2], es[2], j0, j1;
+        int b, h, q0, slot, fs[2], es[2], j0, j1;  // slot: of its partial sums
         __device__ bool visits(int i, int n) const { return i ? n >= fs[1] && n < es[1] : n >= fs[0] && n < es[0]; }
     };
     auto unpack = [&](const int4 &x, const int4 &y) {
@@ -188,6 +196,7 @@ __global__ void __launch_bounds__(384, 1)
         it.es[0] = x.w;
         it.fs[1] = y.x;
         it.es[1] = y.y;
+        it.slot = y.z;
         const bool e0 = x.w > x.z, e1 = y.y > y.x;
         it.j0 = (e0 && e1 ? min(x.z, y.x) : e0 ? x.z : y.x) >> 1;
         it.j1 = (max(x.w, y.y) + 1) >> 1;
@@ -224,6 +233,9 @@ __global__ void __launch_bounds__(384, 1)
                     return false;
                 int4 x = make_int4(-1, 0, 0, 0), y = make_int4(0, 0, 0, 0);
                 if (index >= 0) {
+                    y.z = index;
+                    const int split = index % p.splits;
+                    index /= p.splits;
                     // CTAs start in the order of their index.  Causal: every head's last (heaviest) pair of tiles
                     // first; else the pairs of one head together, so that those running side by side share its K and V.
                     x.x = p.mask.causal ? p.num_pairs - 1 - index / BH : index % p.num_pairs;
@@ -251,7 +263,23 @@ __global__ void __launch_bounds__(384, 1)
                         y.x = lo1 / CF::BS;
                         y.y = (hi1 + CF::BS - 1) / CF::BS;
                     }
+                    if (p.splits > 1) {
+                        // this CTA's share of the blocks that hold either tile's steps
+                        const Item all = unpack(x, y);
+                        const int blocks = all.j1 - all.j0;
+                        const int first = 2 * (all.j0 + static_cast<int>(static_cast<int64_t>(split) * blocks / p.splits));
+                        const int end = 2 * (all.j0 + static_cast<int>(static_cast<int64_t>(split + 1) * blocks / p.splits));
+                        auto clip = [&](int &a, int &b) {
+                            a = max(a, first);
+                            b = min(b, end);
+                            if (b <= a)
+                                a = b = 0;
+                        };
+                        clip(x.z, x.w);
+                        clip(y.x, y.y);
+                    }
                     *out = unpack(x, y);
+                    index = 0;
                 }
                 if (lane == 0) {
                     item_slots[2 * (t & 1)] = x;
@@ -553,6 +581,28 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok)
                 break;
             tc_fence_after_sync();
+            if (p.splits > 1) {
+                const int64_t at = (static_cast<int64_t>(it.slot) * 2 + tile) * 128 + r;
+                p.part_ml[at] = make_float2(m, l);
+                float4 *part = p.part_o + (static_cast<int64_t>(it.slot) * 2 + tile) * (D / 4) * 128 + r;
+#pragma unroll 1
+                for (int k = 0; k < D / 32 && es > fs; ++k) {
+                    uint32_t o[32];
+                    tmem_load_32cols(o_addr + 32 * k, o);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        part[(8 * k + v) * 128] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                              __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                }
+                if (es > fs) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(CF::BAR_OE + tile));
+                }
+                continue;
+            }
             const bool empty = seen.y <= seen.x || l == 0.0f;
             const float inv = empty ? 0.0f : 1.0f / l;
             const int row0 = it.q0 + tile * CF::BM + (warp & 3) * 32;  // this warp's first row
@@ -618,6 +668,71 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after_sync();
     if (warp == 1)
         tmem_dealloc(tmem_base, 512);
+}
+
+struct AttnJoinParams {
+    int32_t H, Sq, num_pairs, BH, splits, causal;
+    const float4 *part_o;
+    const float2 *part_ml;
+    uint16_t *O;
+    int64_t o_batch, o_head, o_row;
+    float *lse;
+};
+
+// Adds the splits of each row in the order of the keys: a row a lane, D / 8
+// columns a warp (256 threads), a CTA for 32 rows.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttnJoinParams p)
+{
+    constexpr int C4 = D / 32;  // groups of four columns a warp
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bx = static_cast<int>(blockIdx.x);
+    const int quarter = bx & 3, tile = (bx >> 2) & 1, item = bx >> 3;
+    // the item's pair and head, as the forward numbers them
+    const int pair = p.causal ? p.num_pairs - 1 - item / p.BH : item % p.num_pairs;
+    const int bh = p.causal ? item % p.BH : item / p.num_pairs;
+    const int r = 32 * quarter + lane;
+    const int row = (2 * pair + tile) * 128 + r;
+    if (row >= p.Sq)
+        return;
+    auto slot = [&](int s) { return (static_cast<int64_t>(item) * p.splits + s) * 2 + tile; };
+    float M = -INFINITY, L = 0.0f, acc[4 * C4];
+#pragma unroll
+    for (int v = 0; v < 4 * C4; ++v)
+        acc[v] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s)
+        M = fmaxf(M, p.part_ml[slot(s) * 128 + r].x);
+#pragma unroll 2
+    for (int s = 0; s < p.splits; ++s) {
+        const float2 x = p.part_ml[slot(s) * 128 + r];
+        if (x.x == -INFINITY && x.y == 0.0f)
+            continue;  // saw no key: its sums may not even be there
+        const float f = exp2_approx_ftz(x.x - M);
+        L = fmaf(x.y, f, L);
+        const float4 *part = p.part_o + (slot(s) * (D / 4) + warp * C4) * 128 + r;
+#pragma unroll
+        for (int v = 0; v < C4; ++v) {
+            const float4 w = part[v * 128];
+            acc[4 * v] = fmaf(w.x, f, acc[4 * v]);
+            acc[4 * v + 1] = fmaf(w.y, f, acc[4 * v + 1]);
+            acc[4 * v + 2] = fmaf(w.z, f, acc[4 * v + 2]);
+            acc[4 * v + 3] = fmaf(w.w, f, acc[4 * v + 3]);
+        }
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int b = bh / p.H, h = bh - b * p.H;
+    uint16_t *orow = p.O + b * p.o_batch + h * p.o_head + static_cast<int64_t>(row) * p.o_row + warp * 4 * C4;
+#pragma unroll
+    for (int v = 0; v < C4; v += 2)
+        *reinterpret_cast<uint4 *>(orow + 4 * v) =
+            make_uint4(pack2<DT>(acc[4 * v] * inv, acc[4 * v + 1] * inv), pack2<DT>(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv),
+                       pack2<DT>(acc[4 * v + 4] * inv, acc[4 * v + 5] * inv),
+                       pack2<DT>(acc[4 * v + 6] * inv, acc[4 * v + 7] * inv));
+    if (p.lse && warp == 0)
+        p.lse[static_cast<int64_t>(bh) * p.Sq + row] = L == 0.0f ? -INFINITY : M * 0.69314718055994531f + logf(L);
 }
 
 } // namespace tl

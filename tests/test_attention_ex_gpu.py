@@ -72,6 +72,10 @@ CASES = {
     "prefix": dict(shape=(3, 2, 1, 290, 290, 128), causal=True, prefix=[[0], [150], [1000]]),
     "prefix_documents": dict(shape=(1, 4, 2, 400, 400, 64), causal=True, docs=[[0, 150, 390]], prefix=[[40, 500]], cap=30.0,
                              bias=True, q_scale=3.0),
+    # more items than SMs: CTAs go on to further items; as many as SMs, causal: two splits of each
+    "many_items": dict(shape=(2, 80, 40, 270, 640, 64), causal=True, offset=370, docs=[[0, 200, 500, 630], [0, 5, 640, 640]]),
+    "many_items_128": dict(shape=(1, 160, 32, 200, 300, 128), bias=True),
+    "as_many_items_as_sms": dict(shape=(1, 100, 50, 150, 1100, 64), causal=True, offset=950, cap=10.0, q_scale=4.0),
     "many_blocks": dict(shape=(1, 2, 1, 260, 1500, 128), causal=True, offset=1240, q_scale=3.0),
 }
 
