@@ -12,7 +12,10 @@ at most
 the bias and the maximum's subtraction a few 2^-23 of their size; 2^x is good to
 2^-22; the capped form to 2^-21 of the cap).  A weight exp(y) / sum exp(y) is then
 off by 2 delta relatively, and by r once it is rounded to 16 bits (fp16 weights
-under 2^-14 of the row's largest: by 2^-25 of it instead).
+under 2^-14 of the row's largest: by 2^-25 of it instead).  2^x is flushed to 0
+below 2^-126, so a weight P may lose 2^-126, and with it dX = P g as much times |g|;
+a dX of its own below 2^-126, bf16's and fp32's smallest normal number, may go to 0:
+2^-126 (1 + |g|) in all, which a far key under a steep bias does lose.
 """
 from __future__ import annotations
 
@@ -113,8 +116,9 @@ class Plain:
         err = (r + 4 * self.delta) * w * g * self.c + w * self.c * kappa + 2.0 ** -19 * w * g
         err_q = err + (2 * r + 4 * self.delta) * w * self.c * zeta
         tiny = 2.0 ** -27 * do.abs().amax() if self.fp16 else 0.0  # fp16's smallest step of the scaled dX
-        err, err_q = err + tiny * see, err_q + tiny * see * (1 + zeta)
-        ab_p = (r + 4 * self.delta) * w + (2.0 ** -35 * see if self.fp16 else 0.0)
+        flushed = 2.0 ** -126 * see
+        err, err_q = err + tiny * see + flushed * (1 + g), err_q + tiny * see * (1 + zeta) + flushed * (1 + g + zeta)
+        ab_p = (r + 4 * self.delta) * w + (2.0 ** -35 * see if self.fp16 else 0.0) + flushed
         f = 1 + 2.0 ** -6
 
         def per_kv(t):
