@@ -12,7 +12,7 @@ using CombineFn = void (*)(TreeParams, int);
 
 struct TreeEntry {
     TreeFn fn[2][2][2];  // [dtype][capped][biased]
-    CombineFn combine[2];
+    CombineFn combine[2][2];  // [dtype][warps share a tile's pieces]
     int smem_fixed, smem_max, tile_bytes, most_slots;
 };
 
@@ -24,7 +24,8 @@ TreeEntry make_tree()
               {tree_attention_kernel<CF, 0, true, false>, tree_attention_kernel<CF, 0, true, true>}},
              {{tree_attention_kernel<CF, 1, false, false>, tree_attention_kernel<CF, 1, false, true>},
               {tree_attention_kernel<CF, 1, true, false>, tree_attention_kernel<CF, 1, true, true>}}},
-            {tree_combine_kernel<0, D>, tree_combine_kernel<1, D>},
+            {{tree_combine_kernel<0, D, 1>, tree_combine_kernel<0, D, 8>},
+             {tree_combine_kernel<1, D, 1>, tree_combine_kernel<1, D, 8>}},
             CF::SMEM_FIXED,
             CF::SMEM_MAX,
             CF::TILE_BYTES,
@@ -153,9 +154,11 @@ tl_status tree_attention_impl(const void *Q, const void *K, const void *V, const
     p.part_o = static_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + o_bytes);
     st = launch_overlapped(fn, grid, 384, smem, stream, tq, tk, tv, p);
+    // few tiles: many pieces each, so warps share them; with a tile an SM a tile has three pieces at most
+    const int64_t rows32 = batch * units * ceil_div(tile_tokens * group, 32);
+    const bool shared_pieces = batch * units * 4 <= d->num_sms;
     if (st == TL_OK)
-        st = launch_overlapped(e.combine[dtype], batch * units * ceil_div(tile_tokens * group, 32), 256, 0, stream, p,
-                               grid);
+        st = launch_overlapped(e.combine[dtype][shared_pieces], rows32 * (shared_pieces ? 8 : 1), 256, 0, stream, p, grid);
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == TL_OK)
         st = TL_ERR_CUDA;
     return st;

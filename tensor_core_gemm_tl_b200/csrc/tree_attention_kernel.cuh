@@ -106,8 +106,11 @@ struct TreeConfig {
     // behind the Q tiles, the K slots and the V slots:
     static constexpr int OFF_MISC = (NUM_BARS * 8 + 15) / 16 * 16;        // TMEM address, abort flag
     static constexpr int OFF_ML = OFF_MISC + 16;                          // [piece & 1][stream][128] float2
-    static constexpr int OFF_TREE = OFF_ML + 2 * 2 * 128 * 8;             // [piece & 1][64] masks, then depths
-    static constexpr int OFF_PARENT = OFF_TREE + 2 * kTreeMaxTokens * 12;  // [warp][64]
+    static constexpr int OFF_TREE = OFF_ML + 2 * 2 * 128 * 8;             // [piece & 1][64] masks
+    // [piece & 1][320] floats: where the keys around the context's end lie, counted from it
+    static constexpr int PLACES = 320, PLACE0 = 128;
+    static constexpr int OFF_PLACE = OFF_TREE + 2 * kTreeMaxTokens * 8;
+    static constexpr int OFF_PARENT = OFF_PLACE + 2 * PLACES * 4;         // [warp][64]
     static constexpr int OFF_CUM = OFF_PARENT + 2 * kTreeMaxTokens * 4;   // [batch]: blocks of the requests before
     static constexpr int SMEM_FIXED = OFF_CUM + 1024;                     // + 4 (batch + 1), Q tiles, slots
     static constexpr int THREADS = 384;
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(384, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float2 *ml = reinterpret_cast<float2 *>(fixed + CF::OFF_ML);
     uint64_t *tree_mask = reinterpret_cast<uint64_t *>(fixed + CF::OFF_TREE);
-    int32_t *tree_depth = reinterpret_cast<int32_t *>(fixed + CF::OFF_TREE + 2 * kTreeMaxTokens * 8);
+    float *tree_place = reinterpret_cast<float *>(fixed + CF::OFF_PLACE);
     int32_t *parent_smem = reinterpret_cast<int32_t *>(fixed + CF::OFF_PARENT);
     int32_t *cum = reinterpret_cast<int32_t *>(fixed + CF::OFF_CUM);
 
@@ -438,7 +441,15 @@ __global__ void __launch_bounds__(384, 1)
                 if (live < kTreeMaxTokens)
                     mask &= live > 0 ? (1ull << live) - 1 : 0ull;
                 tree_mask[buf * kTreeMaxTokens + t] = mask;
-                tree_depth[buf * kTreeMaxTokens + t] = depth;
+                if constexpr (BIAS) {
+                    // context keys at their index, drafted ones at their depth; what lies behind is hidden
+                    float *place = tree_place + buf * CF::PLACES;
+                    place[CF::PLACE0 + t] = static_cast<float>(depth);
+                    place[t] = static_cast<float>(t - CF::PLACE0);
+                    place[64 + t] = static_cast<float>(64 + t - CF::PLACE0);
+                    place[CF::PLACE0 + 64 + t] = 0.0f;
+                    place[CF::PLACE0 + 128 + t] = 0.0f;
+                }
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(CF::BAR_TF + buf));
@@ -495,11 +506,11 @@ __global__ void __launch_bounds__(384, 1)
                 break;
             const uint64_t mask = valid ? tree_mask[buf * kTreeMaxTokens + tok] : 0ull;
             float slope2 = 0.0f;
-            int pos = 0;
+            float pos_f = 0.0f;  // the token's place, counted from the context's end: its depth
             if constexpr (BIAS) {
                 if (valid) {
                     slope2 = __ldg(p.score.slopes + head) * 1.4426950408889634f;
-                    pos = rq.context + tree_depth[buf * kTreeMaxTokens + tok];
+                    pos_f = tree_place[buf * CF::PLACES + CF::PLACE0 + tok];
                 }
             }
             float m = -INFINITY, l = 0.0f;
@@ -531,23 +542,19 @@ __global__ void __launch_bounds__(384, 1)
                             if (!(see & (1u << e)))
                                 sv[e] = __float_as_uint(value);
                     };
-                    // with a bias: the scores in log2 units
+                    // with a bias: the scores in log2 units, less slope2 times the distance
                     auto biased = [&](int q) {
-                        const float dist0 = static_cast<float>(pos - key0 - 32 * q);
+                        const float dist0 = pos_f - static_cast<float>(key0 + 32 * q - rq.context);
+                        const float *place = tree_place + buf * CF::PLACES + CF::PLACE0 + (key0 + 32 * q - rq.context);
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), splat2(to_log2));
-                            float2 dist = make_float2(dist0 - static_cast<float>(e), dist0 - static_cast<float>(e + 1));
-                            if (!context_only) {
-                                // a drafted key lies at the context's end plus its depth
-                                const int a = key0 + 32 * q + e - rq.context;
-                                const int32_t *dep = tree_depth + buf * kTreeMaxTokens;
-                                if (a >= 0)
-                                    dist.x = static_cast<float>(pos - rq.context - dep[min(a, kTreeMaxTokens - 1)]);
-                                if (a + 1 >= 0)
-                                    dist.y = static_cast<float>(pos - rq.context - dep[min(a + 1, kTreeMaxTokens - 1)]);
-                            }
-                            x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
+                            float2 dist;
+                            if (context_only)
+                                dist = fadd2(splat2(dist0), make_float2(-static_cast<float>(e), -static_cast<float>(e + 1)));
+                            else
+                                dist = make_float2(fabsf(pos_f - place[e]), fabsf(pos_f - place[e + 1]));
+                            const float2 x = ffma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                                                   splat2(to_log2), fmul2(dist, splat2(-slope2)));
                             sv[e] = __float_as_uint(x.x);
                             sv[e + 1] = __float_as_uint(x.y);
                         }
@@ -572,6 +579,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         scores(q, CAP && BIAS);
+                        if constexpr (BIAS)  // the second pass finds them as they are here
+                            tmem_store_32cols(s_addr + 32 * q, sv);
                         const float *f = reinterpret_cast<const float *>(sv);
                         float t[4];
 #pragma unroll
@@ -587,6 +596,8 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     if constexpr (!BIAS)
                         mx *= to_log2;
+                    else
+                        tmem_store_wait();
                     const bool resc = mx > m + CF::RESCALE_LOG2;
                     const float m_new = resc ? mx : m;
                     const float m_ref = m_new == -INFINITY ? 0.0f : m_new;
@@ -595,7 +606,12 @@ __global__ void __launch_bounds__(384, 1)
                     float2 part[2] = {splat2(0.0f), splat2(0.0f)};
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
-                        scores(q, CAP);
+                        if constexpr (BIAS) {
+                            tmem_load_32cols(s_addr + 32 * q, sv);
+                            tmem_load_wait();
+                        } else {
+                            scores(q, CAP);
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const float2 v = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
@@ -733,17 +749,26 @@ __global__ void __launch_bounds__(384, 1)
         tmem_dealloc(tmem_base, 512);
 }
 
-// Joins the pieces of each tile whose blocks fell to several CTAs: a row a lane,
-// D / 8 columns a warp.  The pieces are added in the order of the keys.
-template <int DT, int D>
+// Joins the pieces of each tile whose blocks fell to several CTAs: a row a lane.
+// The loads of one piece wait for the L2 (about half a microsecond), so what counts is how
+// many pieces are read one after the other.  With W = 1 the block's 8 warps take
+// D / 8 columns each and read every piece; with W = 8 a block takes D / 8 columns
+// of the tile, its warps every eighth piece each, joined through shared memory
+// (8000 keys of 4 heads, 37 pieces a tile: 34 -> 16 us for the whole call).
+// The order of the sums depends on the lengths and the number of SMs only.
+template <int DT, int D, int W>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams p, int grid)
 {
     constexpr int C4 = D / 32;  // groups of four columns a warp
+    __shared__ float4 join_o[W == 1 ? 1 : C4 * W * 32];
+    __shared__ float2 join_ml[W == 1 ? 1 : W * 32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row_groups = (p.tile_tokens * p.group + 31) / 32;
-    const int rb = static_cast<int>(blockIdx.x % row_groups), bu = static_cast<int>(blockIdx.x / row_groups);
+    const int tile_rows = static_cast<int>(W == 1 ? blockIdx.x : blockIdx.x / 8);
+    const int columns = W == 1 ? warp : static_cast<int>(blockIdx.x % 8);  // which eighth of them
+    const int rb = tile_rows % row_groups, bu = tile_rows / row_groups;
     const int unit = bu % p.units, b = bu / p.units;
     int before = 0, all = 0;
     TreeRequest rq{0, 0, 0};
@@ -775,41 +800,77 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams p, i
     const int hk = unit / p.row_tiles, rt = unit - hk * p.row_tiles;
     const int rows = min(p.tile_tokens, rq.tokens - rt * p.tile_tokens) * p.group;
     const int r = 32 * rb + lane;
-    if (r >= rows)
+    if (32 * rb >= rows)
         return;
+    const bool valid = r < rows;
     auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)); };
-    const float4 *parts = reinterpret_cast<const float4 *>(p.part_o) + warp * C4 * 128 + r;
-    float M = -INFINITY, L = 0.0f, acc[4 * C4];
+    const float4 *parts = reinterpret_cast<const float4 *>(p.part_o) + columns * C4 * 128 + r;
+    float M = -INFINITY, L = 0.0f;
+    float4 acc[C4];
 #pragma unroll
-    for (int v = 0; v < 4 * C4; ++v)
-        acc[v] = 0.0f;
+    for (int v = 0; v < C4; ++v)
+        acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float4 &to, const float4 &x, float f) {
+        to.x = fmaf(x.x, f, to.x);
+        to.y = fmaf(x.y, f, to.y);
+        to.z = fmaf(x.z, f, to.z);
+        to.w = fmaf(x.w, f, to.w);
+    };
+    const int own = W == 1 ? 0 : warp;
+    if (valid) {
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c)
-        M = fmaxf(M, p.part_ml[slot(c) * 128 + r].x);
-#pragma unroll 2
-    for (int c = c0; c <= c1; ++c) {
-        const float2 x = p.part_ml[slot(c) * 128 + r];
-        const float f = x.x == -INFINITY ? 0.0f : exp2_approx_ftz(x.x - M);
-        L = fmaf(x.y, f, L);
+        for (int c = c0 + own; c <= c1; c += W)
+            M = fmaxf(M, p.part_ml[slot(c) * 128 + r].x);
+#pragma unroll 4
+        for (int c = c0 + own; c <= c1; c += W) {
+            const float2 x = p.part_ml[slot(c) * 128 + r];
+            const float f = x.x == -INFINITY ? 0.0f : exp2_approx_ftz(x.x - M);
+            L = fmaf(x.y, f, L);
 #pragma unroll
-        for (int v = 0; v < C4; ++v) {
-            const float4 w = parts[(slot(c) * (D / 4) + v) * 128];
-            acc[4 * v] = fmaf(w.x, f, acc[4 * v]);
-            acc[4 * v + 1] = fmaf(w.y, f, acc[4 * v + 1]);
-            acc[4 * v + 2] = fmaf(w.z, f, acc[4 * v + 2]);
-            acc[4 * v + 3] = fmaf(w.w, f, acc[4 * v + 3]);
+            for (int v = 0; v < C4; ++v)
+                add(acc[v], parts[(slot(c) * (D / 4) + v) * 128], f);
         }
     }
+    if constexpr (W > 1) {
+        // the warps' sums, joined by the first warps: a warp a group of four columns
+        join_ml[warp * 32 + lane] = make_float2(M, L);
+#pragma unroll
+        for (int v = 0; v < C4; ++v)
+            join_o[(v * W + warp) * 32 + lane] = acc[v];
+        __syncthreads();
+        if (warp >= C4)
+            return;
+        M = -INFINITY;
+        L = 0.0f;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            M = fmaxf(M, join_ml[i * 32 + lane].x);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float2 x = join_ml[i * 32 + lane];
+            const float f = x.x == -INFINITY ? 0.0f : exp2_approx_ftz(x.x - M);
+            L = fmaf(x.y, f, L);
+            add(sum, join_o[(warp * W + i) * 32 + lane], f);
+        }
+        acc[0] = sum;
+    }
+    if (!valid)
+        return;
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int tok = rt * p.tile_tokens + r / p.group, head = hk * p.group + r % p.group;
-    uint16_t *orow = p.O + b * p.o_batch + head * p.o_head + static_cast<int64_t>(tok) * p.o_row + warp * 4 * C4;
+    uint16_t *orow = p.O + b * p.o_batch + head * p.o_head + static_cast<int64_t>(tok) * p.o_row + columns * 4 * C4;
+    auto pack4 = [&](const float4 &x) { return make_uint2(pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv)); };
+    if constexpr (W > 1) {
+        reinterpret_cast<uint2 *>(orow)[warp] = pack4(acc[0]);
+    } else {
 #pragma unroll
-    for (int v = 0; v < C4; v += 2)
-        *reinterpret_cast<uint4 *>(orow + 4 * v) =
-            make_uint4(pack2<DT>(acc[4 * v] * inv, acc[4 * v + 1] * inv), pack2<DT>(acc[4 * v + 2] * inv, acc[4 * v + 3] * inv),
-                       pack2<DT>(acc[4 * v + 4] * inv, acc[4 * v + 5] * inv),
-                       pack2<DT>(acc[4 * v + 6] * inv, acc[4 * v + 7] * inv));
-    if (p.lse && warp == 0)
+        for (int v = 0; v < C4; v += 2) {
+            const uint2 lo = pack4(acc[v]), hi = pack4(acc[v + 1]);
+            reinterpret_cast<uint4 *>(orow)[v / 2] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+    }
+    if (p.lse && warp == 0 && columns == 0)
         p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + tok] =
             L == 0.0f ? -INFINITY : M * 0.69314718055994531f + logf(L);
 }
