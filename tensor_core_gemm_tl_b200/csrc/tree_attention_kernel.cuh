@@ -146,6 +146,17 @@ __device__ __forceinline__ TreePiece tree_piece(const int32_t *cum, int B, int u
     return s;
 }
 
+// The lengths of a piece's request.  They are read again here, so they are held to what the work was laid out
+// from: lengths that are written while the call runs (a caller's missing wait between streams) give wrong
+// results, but no access out of bounds.
+__device__ __forceinline__ TreeRequest tree_request(const TreeParams &p, const TreePiece &s)
+{
+    TreeRequest r = tree_request(p, s.b);
+    r.keys = min(max(r.keys, (s.blocks - 1) * 128 + 1), s.blocks * 128);
+    r.context = min(max(r.context, r.keys - kTreeMaxTokens), r.keys);
+    return r;
+}
+
 template <class CF, int DT, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(384, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(384, 1)
             };
             for (int g = g0; ok && g < g1; ++seg) {
                 const TreePiece s = tree_piece(cum, p.B, p.units, g, g1);
-                const TreeRequest rq = tree_request(p, s.b);
+                const TreeRequest rq = tree_request(p, s);
                 const int hk = s.unit / p.row_tiles, rt = s.unit - hk * p.row_tiles;
                 const int32_t *table = p.block_table + s.b * p.table_row;
                 // this lane's box of block j: its page and the row in it
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int total = g1 - g0;
                 TreePiece s1 = tree_piece(cum, p.B, p.units, g0, g1), s2 = s1;  // of block n + 1, of block n
                 int seg1 = 0, seg2 = 0, i1 = 0, i2 = 0;                          // their numbers, blocks done in them
-                int keys2 = tree_request(p, s2.b).keys;
+                int keys2 = tree_request(p, s2).keys;
                 int st1 = 0, st2 = 0;
                 uint32_t ph1 = 0, ph2 = 0, zeroed = 0;  // zeroed: parity of each V slot's zeroings
                 for (int n = -1; n < total; ++n) {
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(384, 1)
                         }
                         if (++i2 == s2.len && n + 1 < total) {
                             s2 = tree_piece(cum, p.B, p.units, g0 + n + 1, g1);
-                            keys2 = tree_request(p, s2.b).keys;
+                            keys2 = tree_request(p, s2).keys;
                             ++seg2;
                             i2 = 0;
                         }
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t tails = 0;
             for (int g = g0; ok && g < g1; ++seg) {
                 const TreePiece s = tree_piece(cum, p.B, p.units, g, g1);
-                const TreeRequest rq = tree_request(p, s.b);
+                const TreeRequest rq = tree_request(p, s);
                 const int buf = seg & 1;
                 if (seg >= 2 && !(ok = __all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_OE + buf),
                                                                             static_cast<uint32_t>((seg >> 1) - 1) & 1u,
@@ -495,7 +506,7 @@ __global__ void __launch_bounds__(384, 1)
         int seg = 0, n0 = 0;
         for (int g = g0; ok && g < g1; ++seg) {
             const TreePiece s = tree_piece(cum, p.B, p.units, g, g1);
-            const TreeRequest rq = tree_request(p, s.b);
+            const TreeRequest rq = tree_request(p, s);
             const int hk = s.unit / p.row_tiles, rt = s.unit - hk * p.row_tiles;
             const int tok = rt * p.tile_tokens + r_token;
             const bool valid = r_token < p.tile_tokens && tok < rq.tokens;
