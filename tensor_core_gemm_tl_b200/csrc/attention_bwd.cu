@@ -1,17 +1,21 @@
 // attention_bwd.cu -- host side of tl_attention_bwd: argument checks, the
-// workspace, tensor maps and the three launches.
+// workspace, tensor maps and the launches.
 #include "attention_host.h"
 #include "attention_bwd_kernel.cuh"
+
+#include <algorithm>
 
 namespace tl {
 namespace {
 
 using BwdFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnBwdParams);
 using RowsFn = void (*)(AttnBwdRowsParams);
+using JoinFn = void (*)(AttnBwdJoinParams);
 
 struct BwdEntry {
     BwdFn fn[2][2][2][2];  // [dtype][dK and dV][capped][biased]
     RowsFn rows[2];        // [dtype]
+    JoinFn join[2][2];     // [dtype][dK and dV]
     int smem, threads, launch_regs;
 };
 
@@ -27,6 +31,8 @@ void fill_bwd(BwdEntry &e)
     e.fn[DT][1][1][0] = attention_bwd_kernel<CF, DT, true, true, false>;
     e.fn[DT][1][1][1] = attention_bwd_kernel<CF, DT, true, true, true>;
     e.rows[DT] = attention_bwd_rows_kernel<DT, CF::D>;
+    e.join[DT][0] = attention_bwd_join_kernel<DT, CF::D, false>;
+    e.join[DT][1] = attention_bwd_join_kernel<DT, CF::D, true>;
 }
 
 template <int D>
@@ -44,6 +50,34 @@ BwdEntry make_bwd()
 
 const BwdEntry kBwd64 = make_bwd<64>();
 const BwdEntry kBwd128 = make_bwd<128>();
+
+// How a pass's tiles are cut.  A tile's blocks run one after another, so where there are few tiles, or causal ones
+// of very different lengths, the longest decides.  In blocks (about 1 us each): a piece costs its own and about 8
+// more, the joining of the pieces 8; an SM gets its share of the pieces and, as they end at different times, half a
+// piece more (measured: 84 tiles of up to 98 blocks 125 -> 82 us, joining included; 150 tiles of up to 56 blocks
+// 76 us either way).  The sums of eight pieces an SM are the most that is kept in memory.
+struct Pieces {
+    int32_t chunk, splits;
+};
+
+Pieces cut_tiles(int64_t items, int64_t longest, double seen, int num_sms)
+{
+    Pieces c{0x7FFFFFFF, 1};
+    const double work = static_cast<double>(items) * longest * seen;
+    double best = 0.85 * (std::max(static_cast<double>(longest), (work + 8.0 * items) / num_sms) + 8.0);
+    for (int k = 2; k <= 32 && longest >= 4 * k && items * k <= 8ll * num_sms; ++k) {
+        const int64_t chunk = ceil_div(longest, k);
+        const double pieces = items * (seen * longest / chunk + 0.5);
+        const double share = pieces <= num_sms ? 0.0 : (work + 8.0 * pieces) / num_sms + 0.5 * (chunk + 8);
+        const double t = std::max(chunk + 8.0, share) + 8.0;
+        if (t < best) {
+            best = 0.97 * t;
+            c.chunk = static_cast<int32_t>(chunk);
+            c.splits = static_cast<int32_t>(ceil_div(longest, chunk));
+        }
+    }
+    return c;
+}
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -100,8 +134,21 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     const int64_t range_bytes = round256(batch * nqb * 16);
     if ((st = ensure_pool(d)) != TL_OK)
         return st;
+    // both passes' tiles and the most blocks one has
+    const int64_t q_tiles = ceil_div(seq_q, 128), k_tiles = ceil_div(seq_k, 128);
+    const int64_t q_items = q_tiles * batch * heads, k_items = k_tiles * batch * c.kv_heads;
+    const int64_t keys = c.mask.causal && !c.mask.prefix ? std::min(seq_k, c.mask.q_offset + seq_q) : seq_k;
+    const double seen = c.mask.causal ? std::min(1.0, (c.mask.q_offset + 0.5 * seq_q) / keys) : 1.0;
+    const Pieces cut_q = cut_tiles(q_items, ceil_div(keys, kBwdCols), seen, d->num_sms);
+    const Pieces cut_k = cut_tiles(k_items, nqb * (heads / c.kv_heads), seen, d->num_sms);
+    // what the pieces leave: the passes use the same memory one after the other
+    const int64_t q_slots = cut_q.splits > 1 ? q_items * cut_q.splits : 0, k_slots = cut_k.splits > 1 ? k_items * cut_k.splits : 0;
+    const int64_t slots = std::max(q_slots, k_slots);
+    const int64_t piece_bytes = slots ? round256(std::max(q_items, k_items) * 4) : 0;
+    const int64_t part_bytes = slots * 2 * head_dim * 128 * 4;
+    const int64_t own_bytes = rows_bytes + interval_bytes + range_bytes + 256;
     void *ws = nullptr;
-    if (cudaMallocFromPoolAsync(&ws, static_cast<size_t>(rows_bytes + interval_bytes + range_bytes + 256), d->pool,
+    if (cudaMallocFromPoolAsync(&ws, static_cast<size_t>(own_bytes + piece_bytes + part_bytes + q_slots * 128 * 4), d->pool,
                                 stream) != cudaSuccess)
         return TL_ERR_CUDA;
     uint8_t *at = static_cast<uint8_t *>(ws);
@@ -136,8 +183,17 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     AttnBwdParams pk = p, pq = p;
     pq.next = rp.next;
     pk.next = rp.next + 1;
-    pk.tiles = static_cast<int32_t>(ceil_div(seq_k, 128));
-    pq.tiles = static_cast<int32_t>(ceil_div(seq_q, 128));
+    pk.tiles = static_cast<int32_t>(k_tiles);
+    pq.tiles = static_cast<int32_t>(q_tiles);
+    auto cut = [&](AttnBwdParams &a, const Pieces &by) {
+        a.chunk = by.chunk;
+        a.splits = by.splits;
+        a.pieces = by.splits > 1 ? reinterpret_cast<int32_t *>(at + own_bytes) : nullptr;
+        a.part = reinterpret_cast<float4 *>(at + own_bytes + piece_bytes);
+        a.part_e = reinterpret_cast<float *>(at + own_bytes + piece_bytes + part_bytes);
+    };
+    cut(pq, cut_q);
+    cut(pk, cut_k);
     for (int i = 0; i < 3; ++i) {
         rp.so[i] = c.o.s[i];
         rp.sdo[i] = sdo.s[i];
@@ -146,17 +202,40 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
         st = TL_ERR_CUDA;
     if (st == TL_OK)
         st = launch_overlapped(e.rows[dtype], nqb * batch * heads, 256, 0, stream, rp);
-    // persistent CTAs, one an SM; they take tiles from the passes' counters
-    auto launch = [&](BwdFn fn, const CUtensorMap &x1, const CUtensorMap &x2, const CUtensorMap &y1,
+    // persistent CTAs, one an SM; they take pieces from the passes' counters
+    auto launch = [&](int dkv_pass, const CUtensorMap &x1, const CUtensorMap &x2, const CUtensorMap &y1,
                       const CUtensorMap &y2, const CUtensorMap &o0, const CUtensorMap &o1, int64_t items,
-                      const AttnBwdParams &a) {
-        return launch_overlapped(fn, items < d->num_sms ? items : d->num_sms, e.threads, e.smem, stream, x1, x2, y1, y2,
-                                 o0, o1, a);
+                      const AttnBwdParams &a, void *out0, const Strides &s0, void *out1, const Strides &s1) {
+        const int64_t pieces = items * a.splits;
+        tl_status r = launch_overlapped(dkv_pass ? dkv : dq, pieces < d->num_sms ? pieces : d->num_sms, e.threads, e.smem,
+                                        stream, x1, x2, y1, y2, o0, o1, a);
+        if (r != TL_OK || a.splits == 1)
+            return r;
+        AttnBwdJoinParams j{};
+        j.mask = a.mask;
+        j.H = a.H;
+        j.heads = dkv_pass ? a.Hk : a.H;
+        j.tiles = a.tiles;
+        j.BH = a.B * j.heads;
+        j.splits = a.splits;
+        j.nqb = a.nqb;
+        j.pieces = a.pieces;
+        j.part = a.part;
+        j.part_e = a.part_e;
+        j.rows = rp.rows;
+        j.intervals = a.intervals;
+        j.out0 = static_cast<uint16_t *>(out0);
+        j.out1 = static_cast<uint16_t *>(out1);
+        for (int i = 0; i < 3; ++i) {
+            j.s0[i] = s0.s[i];
+            j.s1[i] = s1.s[i];
+        }
+        return launch_overlapped(e.join[dtype][dkv_pass], items * 4, 256, 0, stream, j);
     };
     if (st == TL_OK)
-        st = launch(dq, tq, tdo, bk, bv, out_q, out_q, pq.tiles * batch * heads, pq);
+        st = launch(0, tq, tdo, bk, bv, out_q, out_q, q_items, pq, dQ, sdq, dQ, sdq);
     if (st == TL_OK)
-        st = launch(dkv, tk, tv, bq, bdo, out_k, out_v, pk.tiles * batch * c.kv_heads, pk);
+        st = launch(1, tk, tv, bq, bdo, out_k, out_v, k_items, pk, dK, sdk, dV, sdv);
     if (cudaFreeAsync(ws, stream) != cudaSuccess && st == TL_OK)
         st = TL_ERR_CUDA;
     return st;

@@ -7,7 +7,7 @@
 //     dQ_i  = scale sum_j dX_ij K_j,   dK_j = scale sum_i dX_ij Q_i
 //
 // with i running over every query head that shares the key/value head.  Three
-// launches, none of which adds with atomics, so results repeat bit for bit:
+// launches (and two that join pieces), none of which adds with atomics, so results repeat bit for bit:
 //
 //   attention_bwd_rows_kernel      delta from O, lse in log2 units, each row's interval
 //   attention_bwd_kernel<!DKV>     a CTA holds 128 queries and runs over the keys:
@@ -45,6 +45,10 @@
 // of a row a thread held up every other memory operation of the SM, the products'
 // issue included: 5000 clocks a tile).
 //
+// Few tiles of many blocks are cut into pieces along the blocks (attention_bwd.cu
+// says when): each piece leaves fp32 sums, and attention_bwd_join_kernel adds them
+// in their order, taking dQ's correction by the whole e.
+//
 // What bounds it: 4 products of 128 x 64 x D a block, with D = 128 1024 clocks at
 // 4096 multiply-adds a clock and SM, 1400 as S and dP read 48 bytes of shared
 // memory operands for every 32 clocks' worth of products, against one 2^x a score
@@ -78,9 +82,33 @@ struct AttnBwdParams {
     const int32_t *intervals;  // [B][nqb][3][64]: first and end key of each query; 0.0f where it sees one key, else 1.0f
     const int4 *ranges;        // [B][nqb]: least first, largest end, largest first, least end of the block's queries
     const unsigned *amax;      // fp16: bits of the largest |dO|, else null
-    int32_t *next;             // counter that tiles are taken from, 0 at the start
+    int32_t *next;             // counter that pieces are taken from, 0 at the start
+    int32_t chunk, splits;     // a piece is up to `chunk` blocks of a tile, a tile `splits` pieces at most
+    int32_t *pieces;           // [tiles of all heads]: how many a tile has; null where every tile is one
+    float4 *part;              // [tiles][splits][2][D / 4][128]: a row a lane, so a warp's rows lie side by side
+    float *part_e;             // dQ: [tiles][splits][128]: e
     uint64_t timeout_ns;
 };
+
+struct AttnBwdJoinParams {
+    MaskParams mask;
+    int32_t H, heads, tiles, BH, splits, nqb;  // heads: of the tiles
+    const int32_t *pieces;
+    const float4 *part;
+    const float *part_e;
+    float *rows;               // dQ: as the passes'
+    const int32_t *intervals;
+    uint16_t *out0, *out1;     // dQ, or dK and dV
+    int64_t s0[3], s1[3];
+};
+
+// The tile and batch * heads index of item i: causal: the heaviest tiles first (the first keys, the last queries);
+// else one head's tiles together
+template <bool DKV>
+__device__ __forceinline__ int2 bwd_tile(int i, int tiles, int BH, bool causal)
+{
+    return causal ? make_int2(DKV ? i / BH : tiles - 1 - i / BH, i % BH) : make_int2(i % tiles, i / tiles);
+}
 
 struct AttnBwdRowsParams {
     MaskParams mask;
@@ -228,8 +256,10 @@ struct AttnBwdConfig {
     static constexpr int BAR_DRAIN = BAR_TE + 2;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
-    static constexpr int OFF_TILES = OFF_MISC + 16;  // [slot] x0, batch entry * heads + head, first block, blocks
-    static constexpr int OFF_EPS = OFF_TILES + 32;   // [tile & 1][warpgroup][128] floats
+    // [slot] x0, batch entry * heads + head, first block, blocks of a head; then the piece: its first block, its
+    // blocks, where its sums go (-1: to the result)
+    static constexpr int OFF_TILES = OFF_MISC + 16;
+    static constexpr int OFF_EPS = OFF_TILES + 64;   // [tile & 1][warpgroup][128] floats
     static constexpr int OFF_OUT = (OFF_EPS + 4096 + 127) / 128 * 128;  // [warp] 32 rows x 16 columns on their way out
     static constexpr int SMEM_BYTES = OFF_OUT + 16 * 1024 + 1024;
     static constexpr int THREADS = 640;  // 4 control warps, 4 warpgroups for P and dX
@@ -258,7 +288,7 @@ __global__ void __launch_bounds__(640, 1)
     const int lane = threadIdx.x & 31;
     const int heads = DKV ? p.Hk : p.H;
     const int BH = p.B * heads;
-    const int items = p.tiles * BH;
+    const int items = p.tiles * BH * p.splits;
 
     const uint32_t sX = smem_addr(smem + CF::OFF_X);
     const uint32_t sY = smem_addr(smem + CF::OFF_Y);
@@ -318,12 +348,13 @@ __global__ void __launch_bounds__(640, 1)
 
     // The tiles this CTA takes, one after another: every role reads the same
     // descriptions, two of them ahead at most.
-    auto take_tile = [&](int t, int4 *out) {
+    auto take_tile = [&](int t, int4 *out, int4 *piece) {
         const bool w = __all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_TF + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u,
                                                             abort_flag, timeout, ERR_EPILOGUE));
         if (!w)
             return false;
-        *out = tile_slots[t & 1];
+        *out = tile_slots[2 * (t & 1)];
+        *piece = tile_slots[2 * (t & 1) + 1];
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bar(CF::BAR_TE + (t & 1)));
@@ -337,20 +368,24 @@ __global__ void __launch_bounds__(640, 1)
             // ------------------------------------------------------------ tiles and loads
             // Takes tile t from the counter, works out which blocks it visits and
             // leaves its description for the others.
-            auto next_tile = [&](int t, int4 *out) {
+            auto next_tile = [&](int t, int4 *out, int4 *piece) {
                 if (t >= 2 && !__all_sync(0xffffffffu, wait_bounded(bar(CF::BAR_TE + (t & 1)),
                                                                     static_cast<uint32_t>((t >> 1) - 1) & 1u, abort_flag,
                                                                     timeout, ERR_PRODUCER)))
                     return false;
-                int item = 0;
-                if (lane == 0)
-                    item = atomicAdd(p.next, 1);
-                item = __shfl_sync(0xffffffffu, item, 0);
-                int4 tl = make_int4(-1, 0, 0, 0);
-                if (item < items) {
-                    // causal: the heaviest tiles first (the first keys, the last queries); else one head's tiles together
-                    const int tile = p.mask.causal ? (DKV ? item / BH : p.tiles - 1 - item / BH) : item % p.tiles;
-                    const int bh = p.mask.causal ? item % BH : item / p.tiles;
+                int4 tl, pc;
+                do {
+                    int item = 0;
+                    if (lane == 0)
+                        item = atomicAdd(p.next, 1);
+                    item = __shfl_sync(0xffffffffu, item, 0);
+                    tl = make_int4(-1, 0, 0, 0);
+                    pc = make_int4(0, 0, -1, 0);
+                    if (item >= items)
+                        break;
+                    const int i = item / p.splits, s = item - i * p.splits;
+                    const int2 at = bwd_tile<DKV>(i, p.tiles, BH, p.mask.causal);
+                    const int tile = at.x, bh = at.y;
                     const int b = bh / heads, x0 = tile * CF::BM;
                     const int4 *rg = p.ranges + static_cast<int64_t>(b) * p.nqb;
                     int first = 0x7FFFFFFF, end = 0;
@@ -373,24 +408,40 @@ __global__ void __launch_bounds__(640, 1)
                             end = max(end, (v.y + CF::BN - 1) / CF::BN);
                         }
                     }
-                    tl = make_int4(x0, bh, first, end > first ? end - first : 0);
-                }
+                    // a piece of the blocks, those of the heads that share the keys one after another; a tile
+                    // without blocks is one empty piece
+                    const int blocks = end > first ? end - first : 0, all = DKV ? blocks * p.group : blocks;
+                    const int n0 = s * p.chunk;
+                    if (n0 >= all && s > 0)
+                        continue;  // (tl.x is -1: the next one)
+                    tl = make_int4(x0, bh, first, blocks);
+                    pc = make_int4(n0, min(p.chunk, all - n0), all > p.chunk ? item : -1, 0);
+                    if (p.pieces && s == 0 && lane == 0)
+                        p.pieces[i] = (all + p.chunk - 1) / p.chunk;
+                    if (!DKV) {
+                        tl.z += n0;
+                        tl.w = pc.y;
+                        pc.x = 0;
+                    }
+                } while (tl.x < 0);
                 if (lane == 0) {
-                    tile_slots[t & 1] = tl;
+                    tile_slots[2 * (t & 1)] = tl;
+                    tile_slots[2 * (t & 1) + 1] = pc;
                     mbar_arrive(bar(CF::BAR_TF + (t & 1)));
                 }
                 __syncwarp();
                 *out = tl;
+                *piece = pc;
                 return true;
             };
             int st = 0;
             uint32_t ph = 0, xph = 0;
-            int4 tl;
-            bool ok = next_tile(0, &tl);
+            int4 tl, pc;
+            bool ok = next_tile(0, &tl, &pc);
             // The next tile is taken when this one's last loads are out: taken at its start, tiles would be dealt out
             // regardless of who finishes first.
-            for (int t = 0; ok && tl.x >= 0; ok = ok && next_tile(t + 1, &tl), ++t) {
-                if (tl.w == 0)
+            for (int t = 0; ok && tl.x >= 0; ok = ok && next_tile(t + 1, &tl, &pc), ++t) {
+                if (pc.y == 0)
                     continue;
                 const int b = tl.y / heads, head = tl.y - b * heads;
                 if (lane == 0) {
@@ -406,8 +457,9 @@ __global__ void __launch_bounds__(640, 1)
                         parity = (parity & ~1u) | xph;
                     }
                     // DKV: over the heads that share the keys, one after another
-                    int yb = tl.z, yh = DKV ? head * p.group : head / p.group;
-                    const int n_total = DKV ? tl.w * p.group : tl.w;
+                    int yb = DKV ? tl.z + pc.x % tl.w : tl.z;
+                    int yh = DKV ? head * p.group + pc.x / tl.w : head / p.group;
+                    const int n_total = pc.y;
                     for (int n = 0; ok && n < n_total; ++n) {
                         if (!(ok = wait_bounded(bar(CF::BAR_YE + st), ph ^ 1u, abort_flag, timeout, ERR_PRODUCER)))
                             break;
@@ -496,12 +548,12 @@ __global__ void __launch_bounds__(640, 1)
                 __syncwarp();
             };
             uint32_t g = 0, busy = 0;  // blocks and tiles with blocks so far
-            int4 tl;
+            int4 tl, pc;
             bool ok = true;
             // Every wait follows each phase of its barrier in turn, so no two phases
             // can be mistaken.
-            for (int t = 0; ok && take_tile(t, &tl); ++t) {
-                const int n_total = DKV ? tl.w * p.group : tl.w;
+            for (int t = 0; ok && take_tile(t, &tl, &pc); ++t) {
+                const int n_total = pc.y;
                 if (n_total == 0)
                     continue;
                 if (warp < 3) {
@@ -573,12 +625,12 @@ __global__ void __launch_bounds__(640, 1)
         constexpr float p_undo = DT == 0 ? 1.0f / 1024.0f : 1.0f;
         uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 1024);
         uint32_t g0 = 0, busy = 0;  // blocks and tiles with blocks so far
-        int4 tl;
+        int4 tl, pc;
         bool ok = true;
-        for (int t = 0; ok && take_tile(t, &tl); ++t) {
+        for (int t = 0; ok && take_tile(t, &tl, &pc); ++t) {
             const int b = tl.y / heads, head = tl.y - b * heads, x0 = tl.x;
             const int row = x0 + r;
-            const int n_total = DKV ? tl.w * p.group : tl.w;
+            const int n_total = pc.y;
             int2 seen = make_int2(0, 0);                   // dQ: the row's interval
             float row_nlse = -INFINITY, row_ndelta = 0.0f;
             float2 eps = splat2(0.0f);                     // dQ: this thread's part of e (times P's factor)
@@ -598,7 +650,7 @@ __global__ void __launch_bounds__(640, 1)
                 slope2 = __ldg(p.score.slopes + head) * 1.4426950408889634f;
             // this team's blocks; where they lie, and DKV: in which head
             const int n_first = static_cast<int>((static_cast<uint32_t>(team) - g0) & 1u);
-            int yb = tl.z + n_first, yh = head * p.group;
+            int yb = tl.z + (DKV ? pc.x : 0) + n_first, yh = head * p.group;
             auto carry = [&]() {
                 while (yb >= tl.z + tl.w) {
                     yb -= tl.w;
@@ -772,10 +824,34 @@ __global__ void __launch_bounds__(640, 1)
             const float e_mul = -e_row * p.scale * p_undo;
             const bool none = n_total == 0 || (!DKV && seen.y - seen.x <= 1);  // nothing comes through
             if constexpr (!DKV) {
-                if (group == 0 && row_stats)
-                    row_stats[CF::BN] = row_ndelta - e_row;
+                if (group == 0) {
+                    if (pc.z >= 0)
+                        p.part_e[static_cast<int64_t>(pc.z) * 128 + r] = e_row;
+                    else if (row_stats)
+                        row_stats[CF::BN] = row_ndelta - e_row;
+                }
             }
             const int c0 = DKV ? (group >> 1) * (D / 32) : group * (D / 64), c1 = c0 + (DKV ? D / 32 : D / 64);  // of 16 columns
+            if (pc.z >= 0) {
+                // one of several pieces: its sums as they are; dQ's B beside them
+                float4 *part = p.part + static_cast<int64_t>(pc.z) * (2 * D / 4) * 128 + r;
+#pragma unroll 1
+                for (int k = DKV ? c0 : 2 * c0; k < (DKV ? c1 : 2 * c1); ++k) {
+                    const int m = DKV ? (second ? 1 : 0) : k & 1, col = 16 * (DKV ? k : k >> 1);
+                    uint32_t o[16];
+                    tmem_load_16cols((DKV || m == 0 ? acc : acc0) + col, o);
+                    tmem_load_wait();
+                    const float by = DKV || m == 0 ? mul : p.scale * p_undo;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        part[(m * (D / 4) + col / 4 + v) * 128] =
+                            make_float4(__uint_as_float(o[4 * v]) * by, __uint_as_float(o[4 * v + 1]) * by,
+                                        __uint_as_float(o[4 * v + 2]) * by, __uint_as_float(o[4 * v + 3]) * by);
+                }
+                arrive(CF::BAR_ACCE);
+                ++busy;
+                continue;
+            }
 #pragma unroll 1
             for (int cc = c0; cc < c1; ++cc) {
                 uint32_t o[16];
@@ -846,6 +922,77 @@ __global__ void __launch_bounds__(640, 1)
     tc_fence_after_sync();
     if (warp == 1)
         tmem_dealloc(tmem_base, 512);
+}
+
+// Adds the pieces of each tile that has several, in their order: a row a lane,
+// D / 8 columns a warp, a CTA for 32 rows.
+template <int DT, int D, bool DKV>
+__global__ void __launch_bounds__(256) attention_bwd_join_kernel(const AttnBwdJoinParams p)
+{
+    constexpr int C4 = D / 32;  // groups of four columns a warp
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int item = static_cast<int>(blockIdx.x >> 2);
+    const int pieces = p.pieces[item];
+    if (pieces <= 1)
+        return;
+    const int2 at = bwd_tile<DKV>(item, p.tiles, p.BH, p.mask.causal);
+    const int r = 32 * static_cast<int>(blockIdx.x & 3) + lane, row = at.x * 128 + r;
+    if (row >= (DKV ? p.mask.Sk : p.mask.Sq))
+        return;
+    const int b = at.y / p.heads, h = at.y - b * p.heads;
+    const int64_t slot0 = static_cast<int64_t>(item) * p.splits;
+    float4 sum[2][C4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int v = 0; v < C4; ++v)
+            sum[m][v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float e = 0.0f;
+    const float4 *part = p.part + (slot0 * (2 * D / 4) + warp * C4) * 128 + r;
+#pragma unroll 2
+    for (int s = 0; s < pieces; ++s) {
+        if constexpr (!DKV)
+            e += p.part_e[(slot0 + s) * 128 + r];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int v = 0; v < C4; ++v) {
+                const float4 x = part[(static_cast<int64_t>(s) * (2 * D / 4) + m * (D / 4) + v) * 128];
+                sum[m][v].x += x.x;
+                sum[m][v].y += x.y;
+                sum[m][v].z += x.z;
+                sum[m][v].w += x.w;
+            }
+    }
+    if constexpr (!DKV) {
+        const int64_t block = row / kBwdCols;
+        const int32_t *iv = p.intervals + (static_cast<int64_t>(b) * p.nqb + block) * 3 * kBwdCols + row % kBwdCols;
+        const bool none = iv[kBwdCols] - iv[0] <= 1;
+#pragma unroll
+        for (int v = 0; v < C4; ++v) {
+            float4 &x = sum[0][v];
+            const float4 y = sum[1][v];
+            x = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                     : make_float4(fmaf(-e, y.x, x.x), fmaf(-e, y.y, x.y), fmaf(-e, y.z, x.z), fmaf(-e, y.w, x.w));
+        }
+        if (warp == 0) {
+            float *stats = p.rows + ((static_cast<int64_t>(b) * p.H + h) * p.nqb + block) * 2 * kBwdCols + row % kBwdCols;
+            stats[kBwdCols] -= e;
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < (DKV ? 2 : 1); ++m) {
+        const int64_t *st = m ? p.s1 : p.s0;
+        uint16_t *out = (m ? p.out1 : p.out0) + b * st[0] + h * st[1] + row * st[2] + warp * 4 * C4;
+#pragma unroll
+        for (int v = 0; v < C4; v += 2) {
+            const float4 x = sum[m][v], y = sum[m][v + 1];
+            reinterpret_cast<uint4 *>(out)[v / 2] =
+                make_uint4(pack2<DT>(x.x, x.y), pack2<DT>(x.z, x.w), pack2<DT>(y.x, y.y), pack2<DT>(y.z, y.w));
+        }
+    }
 }
 
 } // namespace tl

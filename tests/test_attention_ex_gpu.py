@@ -76,6 +76,13 @@ CASES = {
     "many_items": dict(shape=(2, 80, 40, 270, 640, 64), causal=True, offset=370, docs=[[0, 200, 500, 630], [0, 5, 640, 640]]),
     "many_items_128": dict(shape=(1, 160, 32, 200, 300, 128), bias=True),
     "as_many_items_as_sms": dict(shape=(1, 100, 50, 150, 1100, 64), causal=True, offset=950, cap=10.0, q_scale=4.0),
+    # few tiles of many blocks: the backward cuts them into pieces, along the keys for dq, the queries of all heads for
+    # dk and dv; pieces that see nothing of a document, rows that see one key or none
+    "pieces_of_keys": dict(shape=(1, 2, 1, 300, 2300, 128), causal=True, offset=2000, docs=[[0, 5, 2001, 2002, 2290]], bias=True),
+    "pieces_of_queries": dict(shape=(1, 6, 1, 900, 900, 64), causal=True, cap=10.0, q_scale=3.0, rows_first=True),
+    "pieces_of_both": dict(shape=(2, 3, 1, 1500, 1500, 64), causal=True, docs=[[0, 1, 1400, 1490], [20, 700, 710, 1500]],
+                           prefix=[[0, 900, 0], [50, 3, 2000]]),
+    "pieces_all_keys": dict(shape=(1, 3, 1, 260, 2100, 128), cap=20.0, q_scale=4.0),
     "many_blocks": dict(shape=(1, 2, 1, 260, 1500, 128), causal=True, offset=1240, q_scale=3.0),
 }
 
