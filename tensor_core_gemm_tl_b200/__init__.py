@@ -163,17 +163,30 @@ def attention(q, k, v, causal: bool = False, scale: float = 0.0, out=None, lse=N
 # are written to cost little: each tensor's strides are read once, the option
 # structs are packed in one go, the device is only switched when it has to be.
 
-def _rows(name, t, device, dtype, shape):
-    """The strides of (outer, middle, row) of a 4-D CUDA tensor, for the C ABI;
-    ValueError unless it lies on `device`, has `dtype` and `shape`, a contiguous
-    last dimension, positive strides in multiples of 8 elements and a 16-byte
-    aligned base."""
-    if t.device != device or not t.is_cuda:
+def _refuse(name, t, device, dtype, shape):
+    if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _empty_like(t, stream):
+    """An output laid out like `t`, its memory taken for the stream that writes it."""
+    import torch
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
+def _rows(name, t, device, dtype, shape):
+    """The strides of (outer, middle, row) of a 4-D CUDA tensor, for the C ABI;
+    ValueError unless it lies on the CUDA device `device`, has `dtype` and `shape`, a contiguous
+    last dimension, positive strides in multiples of 8 elements and a 16-byte
+    aligned base."""
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _refuse(name, t, device, dtype, shape)
     st = t.stride()
     s0, s1, s2, s3 = st
     if s3 != 1 or s0 <= 0 or s1 <= 0 or s2 <= 0 or (s0 | s1 | s2) & 7:
@@ -190,12 +203,8 @@ def _rows(name, t, device, dtype, shape):
 
 def _flat(name, t, device, dtype, shape):
     """ValueError unless `t` is a contiguous CUDA tensor on `device` of `dtype` and `shape`."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _refuse(name, t, device, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -213,15 +222,16 @@ def _score_arguments(scale, score_cap, slopes, heads, device):
     return slopes.data_ptr()
 
 
-def _launch(device, stream, call, what):
-    """Runs call(raw stream) with `device` current, on `stream` or torch's current one; raises TLError."""
+def _launch(device, stream, what, call, *args):
+    """call(*args but the options, raw stream, options) with `device` current, on `stream` or torch's current one;
+    raises TLError."""
     import torch
     raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        st = call(raw)
+    if torch._C._cuda_getDevice() == device.index:
+        st = call(*args[:-1], raw, args[-1])
     else:
         with torch.cuda.device(device):
-            st = call(raw)
+            st = call(*args[:-1], raw, args[-1])
     if st != 0:
         raise TLError(st, what)
 
@@ -289,11 +299,11 @@ def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap
         _flat("lse", lse, dev, torch.float32, (B, H, Sq))
         lse_ptr = lse.data_ptr()
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     so = _rows("out", out, dev, q.dtype, q.shape)
     opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *_DENSE, *_DENSE, *_DENSE, *_DENSE)
-    _launch(dev, stream, lambda s: tl_attention_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_ptr, B,
-                                                   H, Sq, k.shape[2], D, dt, s, opt), "tl_attention_ex")
+    _launch(dev, stream, "tl_attention_ex", tl_attention_ex, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+            lse_ptr, B, H, Sq, k.shape[2], D, dt, opt)
     return out
 
 
@@ -315,19 +325,16 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: 
     grads = []
     for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         grads.append((g, None if g is None else _rows(name, g, dev, dtype, like.shape), name, like))
-    grads = [(g, sg) if g is not None else _new_rows(name, like) for g, sg, name, like in grads]
+    grads = [(g, sg) if g is not None else _new_rows(name, like, stream) for g, sg, name, like in grads]
     (dq, sdq), (dk, sdk), (dv, sdv) = grads
     opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *sdo, *sdq, *sdk, *sdv)
-    _launch(dev, stream, lambda s: tl_attention_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                                    out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                                    dv.data_ptr(), B, H, Sq, k.shape[2], D, dt, s, opt),
-            "tl_attention_bwd")
+    _launch(dev, stream, "tl_attention_bwd", tl_attention_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Sq, k.shape[2], D, dt, opt)
     return dq, dk, dv
 
 
-def _new_rows(name, like):
-    import torch
-    g = torch.empty_like(like)
+def _new_rows(name, like, stream):
+    g = _empty_like(like, stream)
     return g, _rows(name, g, like.device, like.dtype, like.shape)
 
 
@@ -377,21 +384,19 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
         _flat("lse", lse, dev, torch.float32, (B, H, T))
         lse_ptr = lse.data_ptr()
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     so = _rows("out", out, dev, dtype, q.shape)
     opt = TREE_OPTIONS.pack(scale, score_cap, slopes_ptr, 0, *sq, *so, *sk, *sv)
-    _launch(dev, stream, lambda s: tl_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                                     block_table.data_ptr(), context_lens.data_ptr(), parents_ptr,
-                                                     lens_ptr, out.data_ptr(), lse_ptr, B, H, Hk, T, pages, page_size,
-                                                     max_pages, D, dt, s, opt), "tl_tree_attention")
+    _launch(dev, stream, "tl_tree_attention", tl_tree_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), context_lens.data_ptr(), parents_ptr, lens_ptr, out.data_ptr(), lse_ptr, B, H, Hk, T,
+            pages, page_size, max_pages, D, dt, opt)
     return out
 
 
 def _rotary_rows(name, t, device, dtype, shape):
     """The strides of a 4-D tensor for rotary, any positive ones with a contiguous last dimension."""
-    if t.device != device or not t.is_cuda or t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _refuse(name, t, device, dtype, shape)
     s0, s1, s2, s3 = t.stride()
     if s0 <= 0 or s1 <= 0 or s2 <= 0:  # a dimension of one element takes any stride
         n = t.shape
@@ -446,18 +451,18 @@ def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float
     if out_k is not None:
         sok = _rotary_rows("out_k", out_k, dev, dtype, k.shape)
     if out_q is None:
-        out_q = torch.empty_like(q)
+        out_q = _empty_like(q, stream)
         soq = _rotary_rows("out_q", out_q, dev, dtype, q.shape)
     k_ptr = ok_ptr = 0
     if k is not None:
         if out_k is None:
-            out_k = torch.empty_like(k)
+            out_k = _empty_like(k, stream)
             sok = _rotary_rows("out_k", out_k, dev, dtype, k.shape)
         k_ptr, ok_ptr = k.data_ptr(), out_k.data_ptr()
     opt = ROTARY_OPTIONS.pack(1 if interleaved else 0, 1 if inverse else 0, scale, positions.dtype == torch.int64, shared,
                               0, *sq, *sk, *soq, *sok)
-    _launch(dev, stream, lambda s: tl_rotary(q.data_ptr(), k_ptr, out_q.data_ptr(), ok_ptr, positions.data_ptr(),
-                                             inv_freq.data_ptr(), B, H, Hk, S, D, 2 * half, dt, s, opt), "tl_rotary")
+    _launch(dev, stream, "tl_rotary", tl_rotary, q.data_ptr(), k_ptr, out_q.data_ptr(), ok_ptr, positions.data_ptr(),
+            inv_freq.data_ptr(), B, H, Hk, S, D, 2 * half, dt, opt)
     return out_q, out_k
 
 

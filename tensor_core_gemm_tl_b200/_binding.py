@@ -144,7 +144,7 @@ _lib = load()
 
 def _options(o):
     """An options argument: a Structure, packed bytes, or None."""
-    return ctypes.byref(o) if isinstance(o, ctypes.Structure) else o
+    return o if o.__class__ is bytes or o is None else ctypes.byref(o)
 
 
 def _check(st: int, what: str) -> None:
@@ -180,7 +180,7 @@ def tl_attention_fwd(Q, K, V, O, lse, batch, heads, seq_q, seq_k, head_dim, dtyp
 def tl_attention_ex(Q, K, V, O, lse, batch, heads, seq_q, seq_k, head_dim, dtype, stream=0,
                     options: AttentionOptions | bytes | None = None) -> int:
     """Attention forward with masks, caps, bias and shared heads on device pointers; returns the tl_status code."""
-    return _lib.tl_attention_ex(Q, K, V, O, lse or None, batch, heads, seq_q, seq_k, head_dim, dtype, stream or None,
+    return _lib.tl_attention_ex(Q, K, V, O, lse, batch, heads, seq_q, seq_k, head_dim, dtype, stream,
                                 _options(options))
 
 
@@ -188,24 +188,24 @@ def tl_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, batch, heads, seq_q, seq_k
                      options: AttentionOptions | bytes | None = None) -> int:
     """The gradients of tl_attention_ex on device pointers; returns the tl_status code."""
     return _lib.tl_attention_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, batch, heads, seq_q, seq_k, head_dim, dtype,
-                                 stream or None, _options(options))
+                                 stream, _options(options))
 
 
 def tl_tree_attention(Q, K_cache, V_cache, block_table, context_lens, parents, tree_lens, O, lse, batch, heads,
                       kv_heads, tokens, num_pages, page_size, max_pages, head_dim, dtype, stream=0,
                       options: TreeOptions | bytes | None = None) -> int:
     """New tokens against a paged cache, on device pointers; returns the tl_status code."""
-    return _lib.tl_tree_attention(Q, K_cache, V_cache, block_table, context_lens, parents or None, tree_lens or None,
-                                  O, lse or None, batch, heads, kv_heads, tokens, num_pages, page_size, max_pages,
-                                  head_dim, dtype, stream or None,
+    return _lib.tl_tree_attention(Q, K_cache, V_cache, block_table, context_lens, parents, tree_lens,
+                                  O, lse, batch, heads, kv_heads, tokens, num_pages, page_size, max_pages,
+                                  head_dim, dtype, stream,
                                   _options(options))
 
 
 def tl_rotary(Q, K, Q_out, K_out, positions, inv_freq, batch, heads, kv_heads, seq, head_dim, rot_dim, dtype,
               stream=0, options: RotaryOptions | bytes | None = None) -> int:
     """Rotary positions of q and k on device pointers; returns the tl_status code."""
-    return _lib.tl_rotary(Q, K or None, Q_out, K_out or None, positions, inv_freq, batch, heads, kv_heads, seq,
-                          head_dim, rot_dim, dtype, stream or None,
+    return _lib.tl_rotary(Q, K, Q_out, K_out, positions, inv_freq, batch, heads, kv_heads, seq,
+                          head_dim, rot_dim, dtype, stream,
                           _options(options))
 
 
