@@ -151,7 +151,7 @@ def bound_of(w) -> str:
 
 # The files the GEMM kernel's code and launch are built from; a traffic figure
 # taken on other sources of these files no longer describes the kernel.
-GEMM_SOURCES = ("sm100.cuh", "gemm_kernel.cuh", "config_table.inc", "tl_gemm.cu")
+GEMM_SOURCES = ("sm100.cuh", "device_common.cuh", "gemm_kernel.cuh", "config_table.inc", "tl_gemm.cu")
 
 
 def kernel_source_hash() -> str:

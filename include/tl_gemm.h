@@ -19,16 +19,19 @@
  *
  * The result is rounded once, to nearest even, from float32 to the input
  * dtype (or kept as float32 with tl_gemm_ex's c_float32 option).  The library
- * also holds the tutorial's adjacent kernels: tl_attention_fwd,
- * tl_softmax_rows and tl_vector_add.  Sums are accumulated in float32 on the
+ * also holds the tutorial's adjacent kernels (tl_attention_fwd,
+ * tl_softmax_rows and tl_vector_add) and the attention of language models:
+ * tl_attention_ex with its gradients tl_attention_bwd, tl_tree_attention over
+ * a paged cache, and tl_rotary.  Sums are accumulated in float32 on the
  * tensor cores; the order of the sum is fixed by the kernel configuration and
  * the work split (tl_gemm_plan), so two calls with the same plan give
  * bit-identical results (the raster group changes only which tiles run
  * together).
  *
  * All calls are host functions.  None of them allocates memory that outlives
- * the call; a call that must re-lay out an operand, or whose last round of
- * tiles is cut along K (see tl_gemm), takes a stream-ordered temporary from a
+ * the call; a call that must re-lay out an operand, whose last round of
+ * tiles is cut along K (see tl_gemm), or that joins parts of a sum (the
+ * attention of language models) takes a stream-ordered temporary from a
  * library-owned CUDA memory pool and returns it on the same stream.
  *
  * Threads: every entry point may be called from several host threads at
@@ -241,10 +244,14 @@ TL_API tl_status tl_attention_fwd(const void *Q, const void *K, const void *V, v
  * head_dim is 64 or 128; seq_q, seq_k and q_offset + seq_q at most 2^31 - 257.
  * Pointers are 16-byte aligned; strides are positive multiples of 8 elements,
  * the last dimension is contiguous.  Rows of K and V that no query sees must
- * still be finite (a weight of 0 times NaN is NaN).  Sums and softmax
- * statistics are fp32; the weights are rounded to `dtype` before the product
- * with V and O is rounded once.  Asynchronous on `stream`; allocates nothing;
- * O must not overlap an input.
+ * still be finite (a weight of 0 times NaN is NaN).  With a cap, raw scores
+ * have to stay below 1e18; a cap is above 1e-30, softmax_scale / score_cap below
+ * 1e38.  Sums and softmax statistics are fp32; the weights
+ * are rounded to `dtype` before the product with V and O is rounded once.
+ * Where the batch has few rows the keys are split over the SMs and joined from
+ * a stream-ordered temporary, by a rule on the sizes: results repeat bit for
+ * bit on the same kind of device.  Asynchronous on `stream`; bounded waits
+ * report through tl_check_device; O must not overlap an input.
  */
 typedef struct {
     int32_t causal;              /* 1: query i sees keys j <= q_offset + i            */
@@ -278,8 +285,11 @@ TL_API tl_status tl_attention_ex(const void *Q, const void *K, const void *V, vo
  * by powers of two, dX by one taken from the largest |dO|); every sum is fp32
  * and has a fixed order, so results repeat bit for bit.  dO of queries that see
  * no key does not count, but must be finite.  dQ, dK and dV must overlap
- * neither the inputs nor one another.  The row sums and intervals live in a
- * stream-ordered temporary (about 8 bytes a query and head).
+ * neither the inputs nor one another.  A stream-ordered temporary holds the
+ * row sums and intervals (about 8 bytes a query and head) and, where few tiles
+ * are cut into pieces, the pieces' sums (at most eight pieces an SM, 1 KB a
+ * value of head_dim each).  Asynchronous on `stream`; bounded waits report
+ * through tl_check_device.
  */
 TL_API tl_status tl_attention_bwd(const void *dO, const void *Q, const void *K, const void *V, const void *O,
                            const float *lse, void *dQ, void *dK, void *dV,
@@ -314,8 +324,11 @@ TL_API tl_status tl_attention_bwd(const void *dO, const void *Q, const void *K, 
  * index outside the cache reads as zeros, table entries behind a request's last
  * key are not read, and rows of its last page behind that key may hold anything.
  * Works with any lengths for one captured graph: the host reads none of them.
- * Results repeat bit for bit on the same device.  The joined pieces of long
- * requests live in a stream-ordered temporary.  Asynchronous on `stream`.
+ * Results repeat bit for bit on the same kind of device.  The joined pieces of
+ * long requests live in a stream-ordered temporary (two an SM).  Lengths,
+ * tables and parents must not change while the call runs: that gives wrong
+ * results, though no access out of bounds.  Asynchronous on `stream`; bounded
+ * waits report through tl_check_device.
  */
 typedef struct {
     float softmax_scale;         /* > 0, or 0 for 1 / sqrt(head_dim)                 */

@@ -3,8 +3,10 @@
 The work runs in libtlgemm.so (hand-written tcgen05 / TMA kernels behind a C
 ABI, include/tl_gemm.h).  This package is its Python binding: the raw C-ABI
 calls (``tl_gemm``, ``tl_gemm_ex``, ``tl_check_device``, ``tl_gemm_plan`` ...)
-on device pointers, and ``gemm`` which takes torch CUDA tensors and passes
-their pointers and the current stream.  PyTorch only provides device memory
+on device pointers, and ``gemm``, ``attention``, ``attention_ex``,
+``attention_backward``, ``tree_attention``, ``rotary``, ``softmax`` and
+``vector_add``, which take torch CUDA tensors and pass their pointers and the
+current stream.  PyTorch only provides device memory
 and streams; nothing here computes.
 
 Importing the package fails if the library is not built -- there is no CPU

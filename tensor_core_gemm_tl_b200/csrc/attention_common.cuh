@@ -174,9 +174,9 @@ __device__ __forceinline__ void odd_polynomial(uint32_t *v, float arg, const flo
 // one reciprocal for two, of the product of their denominators; the exponent is
 // held below 2^60 (tanh is 1 to 2^-59 there) so that the product stays finite.  All
 // are absolutely exact to about 2^-22, which is what a score needs: a cap of 50
-// leaves 1e-5.  (The powers of arg stay in range: a score inside the cap times arg
-// is at most 1, and a cap so far from the scores that arg^13 underflows leaves
-// tanh x = x, which the vanishing coefficients give.)
+// leaves 1e-5.  (The polynomials' coefficients hold arg^13 at most: they are left to
+// arg <= 64, far above any cap in use, and where arg^13 underflows tanh x = x,
+// which the vanishing coefficients give.)
 template <int N>
 __device__ __forceinline__ void tanh_scores(uint32_t *v, float arg)
 {
@@ -184,7 +184,7 @@ __device__ __forceinline__ void tanh_scores(uint32_t *v, float arg)
 #pragma unroll
     for (int e = 0; e < N; e += 2)
         top = fmax3(top, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
-    top *= arg;
+    top = arg <= 64.0f ? top * arg : INFINITY;
     if (__all_sync(0xffffffffu, top <= 0.5f)) {
         const float c[5] = {0.9999999869f, -0.3333306939f, 0.1332477932f, -0.05298607529f, 0.01713500663f};
         odd_polynomial<N>(v, arg, c);

@@ -120,7 +120,9 @@ tl_status ready_kernel(DeviceState *d, Fn fn, int smem, int launch_regs)
 
 inline bool score_values_ok(float scale, float cap)
 {
-    return scale >= 0.0f && scale < INFINITY && cap >= 0.0f && cap < INFINITY;
+    // scale / cap is held in fp32 (times 2 log2 e)
+    return scale >= 0.0f && scale < INFINITY && cap >= 0.0f && cap < INFINITY && (cap == 0.0f || scale / cap < 1e38f) &&
+           (cap == 0.0f || cap > 1e-30f);
 }
 
 inline ScoreParams score_params(float scale, float cap, const float *slopes)

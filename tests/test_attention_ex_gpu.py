@@ -184,6 +184,22 @@ def test_gradients_of_small_and_large_losses(scale):
         close(n, g, w, b)
 
 
+@pytest.mark.parametrize("cap,scale,q_scale", [(1e-3, 1.0, 1e-4), (1e-3, 8.0, 1e-6), (2e6, 0.125, 1.0), (1e-6, 0.125, 1.0)])
+def test_caps_far_from_the_scores(cap, scale, q_scale):
+    """Caps thousands of times below or above what is usual, scores inside and outside them."""
+    import tensor_core_gemm_tl_b200 as tg
+    q, k, v, do = tensors(1, 2, 1, 140, 200, 64, "bf16", 9, q_scale)
+    how = dict(score_cap=cap, scale=scale)
+    p = Plain(q, k, v, visible(1, 140, 200, False), scale, cap)
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = tg.attention_ex(q, k, v, lse=lse, **how)
+    close("out", out, p.out, p.out_bound())
+    close("lse", lse, p.lse, p.lse_bound())
+    want, bounds = p.gradients(do)
+    for n, g, w, b in zip(("dq", "dk", "dv"), tg.attention_backward(do, q, k, v, out, lse, **how), want, bounds):
+        close(n, g, w, b)
+
+
 def test_nan_stays_in_its_rows():
     """A NaN query spoils its own row, nothing else."""
     import tensor_core_gemm_tl_b200 as tg

@@ -28,6 +28,7 @@ ATTENTION = [
     (dict(dtype=2), {}, BAD), (dict(head_dim=96), {}, UNSUP), (dict(head_dim=0), {}, UNSUP),
     ({}, dict(kv_heads=3), BAD), ({}, dict(kv_heads=-1), BAD), ({}, dict(kv_heads=16), BAD),
     ({}, dict(softmax_scale=-1.0), BAD), ({}, dict(softmax_scale=math.inf), BAD), ({}, dict(softmax_scale=math.nan), BAD),
+    ({}, dict(score_cap=1e-20, softmax_scale=1e30), BAD), ({}, dict(score_cap=1e-35), BAD),
     ({}, dict(score_cap=-1.0), BAD), ({}, dict(score_cap=math.nan), BAD), ({}, dict(score_cap=math.inf), BAD),
     ({}, dict(causal=2), BAD), ({}, dict(q_offset=-1), BAD), ({}, dict(num_docs=-1), BAD),
     ({}, dict(num_docs=2), BAD), ({}, dict(doc_offsets=P), BAD),
