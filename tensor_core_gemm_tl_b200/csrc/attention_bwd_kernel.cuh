@@ -52,7 +52,10 @@
 // What bounds it: 4 products of 128 x 64 x D a block, with D = 128 1024 clocks at
 // 4096 multiply-adds a clock and SM, 1400 as S and dP read 48 bytes of shared
 // memory operands for every 32 clocks' worth of products, against one 2^x a score
-// (512 clocks; 2.5 times that with capped scores).
+// (512 clocks; 2.5 times that with capped scores).  Measured, 4 x 16 heads on 4 x 4096
+// x 4096 x 128, bf16: all three launches 1740 us, causal 900; with six documents a
+// sequence rows 25, dQ 171, dK and dV 215 us, the tensor pipe 50..53 % busy, the
+// warps waiting for Tensor Memory loads and barriers.
 //
 // 16-bit range: bf16 takes P and dX as they are.  fp16 holds P times 2^10 and
 // dX times 2^4 over the power of two above the largest |dO| (P of long rows

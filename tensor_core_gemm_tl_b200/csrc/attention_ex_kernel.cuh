@@ -29,7 +29,10 @@
 // clocks at 4096 multiply-adds a clock and SM (1376, as S in steps of 64 keys reads
 // 48 bytes of operands for every 32 clocks' worth of products), against one 2^x a
 // pair at 16 a clock (1024 clocks); capped scores add the multiply-adds of
-// tanh_scores.
+// tanh_scores.  Measured, 4 x 16 heads x 4096 x 4096, bf16: D = 128 435 us, 1265
+// TFLOP/s (causal 260); D = 64, 2 x 16 heads, 231 us, 595 TFLOP/s.  The warpgroup's
+// own latency bounds: two warps a scheduler, each 2^x, sum and pack in a chain
+// (the tensor pipe 32..75 % busy, the special-function pipe 32..51 %).
 //
 // Warps: 0 items and TMA loads, 1 issues S (and allocates Tensor Memory), 2 issues
 // P V, 3 idle, 4..7 softmax of tile 0, 8..11 of tile 1.  Every wait is bounded.
