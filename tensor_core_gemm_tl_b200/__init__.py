@@ -173,13 +173,15 @@ def _refuse(name, t, device, dtype, shape):
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _empty_like(t, stream):
-    """An output laid out like `t`, its memory taken for the stream that writes it."""
-    import torch
+def _new_like(torch, t, stream):
+    """An output laid out like `t`, its memory taken for the stream that writes it, and its strides."""
     if stream is None:
-        return torch.empty_like(t)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t)
+        y = torch.empty_like(t)
+    else:
+        with torch.cuda.stream(stream):
+            y = torch.empty_like(t)
+    s0, s1, s2, _ = y.stride()
+    return y, (s0, s1, s2)
 
 
 def _rows(name, t, device, dtype, shape):
@@ -187,7 +189,7 @@ def _rows(name, t, device, dtype, shape):
     ValueError unless it lies on the CUDA device `device`, has `dtype` and `shape`, a contiguous
     last dimension, positive strides in multiples of 8 elements and a 16-byte
     aligned base."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         _refuse(name, t, device, dtype, shape)
     st = t.stride()
     s0, s1, s2, s3 = st
@@ -205,7 +207,7 @@ def _rows(name, t, device, dtype, shape):
 
 def _flat(name, t, device, dtype, shape):
     """ValueError unless `t` is a contiguous CUDA tensor on `device` of `dtype` and `shape`."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         _refuse(name, t, device, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -224,10 +226,9 @@ def _score_arguments(scale, score_cap, slopes, heads, device):
     return slopes.data_ptr()
 
 
-def _launch(device, stream, what, call, *args):
+def _launch(torch, device, stream, what, call, *args):
     """call(*args but the options, raw stream, options) with `device` current, on `stream` or torch's current one;
     raises TLError."""
-    import torch
     raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == device.index:
         st = call(*args[:-1], raw, args[-1])
@@ -301,10 +302,11 @@ def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap
         _flat("lse", lse, dev, torch.float32, (B, H, Sq))
         lse_ptr = lse.data_ptr()
     if out is None:
-        out = _empty_like(q, stream)
-    so = _rows("out", out, dev, q.dtype, q.shape)
+        out, so = _new_like(torch, q, stream)
+    else:
+        so = _rows("out", out, dev, q.dtype, q.shape)
     opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *_DENSE, *_DENSE, *_DENSE, *_DENSE)
-    _launch(dev, stream, "tl_attention_ex", tl_attention_ex, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+    _launch(torch, dev, stream, "tl_attention_ex", tl_attention_ex, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
             lse_ptr, B, H, Sq, k.shape[2], D, dt, opt)
     return out
 
@@ -326,18 +328,13 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: 
     # every given tensor is checked before anything is allocated
     grads = []
     for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        grads.append((g, None if g is None else _rows(name, g, dev, dtype, like.shape), name, like))
-    grads = [(g, sg) if g is not None else _new_rows(name, like, stream) for g, sg, name, like in grads]
+        grads.append((g, None if g is None else _rows(name, g, dev, dtype, like.shape), like))
+    grads = [(g, sg) if g is not None else _new_like(torch, like, stream) for g, sg, like in grads]
     (dq, sdq), (dk, sdk), (dv, sdv) = grads
     opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *sdo, *sdq, *sdk, *sdv)
-    _launch(dev, stream, "tl_attention_bwd", tl_attention_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _launch(torch, dev, stream, "tl_attention_bwd", tl_attention_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
             out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Sq, k.shape[2], D, dt, opt)
     return dq, dk, dv
-
-
-def _new_rows(name, like, stream):
-    g = _empty_like(like, stream)
-    return g, _rows(name, g, like.device, like.dtype, like.shape)
 
 
 def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None, *, tree_lens=None,
@@ -386,10 +383,11 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
         _flat("lse", lse, dev, torch.float32, (B, H, T))
         lse_ptr = lse.data_ptr()
     if out is None:
-        out = _empty_like(q, stream)
-    so = _rows("out", out, dev, dtype, q.shape)
+        out, so = _new_like(torch, q, stream)
+    else:
+        so = _rows("out", out, dev, dtype, q.shape)
     opt = TREE_OPTIONS.pack(scale, score_cap, slopes_ptr, 0, *sq, *so, *sk, *sv)
-    _launch(dev, stream, "tl_tree_attention", tl_tree_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _launch(torch, dev, stream, "tl_tree_attention", tl_tree_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), context_lens.data_ptr(), parents_ptr, lens_ptr, out.data_ptr(), lse_ptr, B, H, Hk, T,
             pages, page_size, max_pages, D, dt, opt)
     return out
@@ -397,7 +395,7 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
 
 def _rotary_rows(name, t, device, dtype, shape):
     """The strides of a 4-D tensor for rotary, any positive ones with a contiguous last dimension."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         _refuse(name, t, device, dtype, shape)
     s0, s1, s2, s3 = t.stride()
     if s0 <= 0 or s1 <= 0 or s2 <= 0:  # a dimension of one element takes any stride
@@ -446,24 +444,21 @@ def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float
         raise ValueError(f"inv_freq has {half} frequencies for heads of {D} values")
     if not 0.0 < scale < float("inf"):
         raise ValueError("scale must be positive and finite")
-    soq = sq
     # every given tensor is checked before anything is allocated
     if out_q is not None:
         soq = _rotary_rows("out_q", out_q, dev, dtype, q.shape)
     if out_k is not None:
         sok = _rotary_rows("out_k", out_k, dev, dtype, k.shape)
     if out_q is None:
-        out_q = _empty_like(q, stream)
-        soq = _rotary_rows("out_q", out_q, dev, dtype, q.shape)
+        out_q, soq = _new_like(torch, q, stream)
     k_ptr = ok_ptr = 0
     if k is not None:
         if out_k is None:
-            out_k = _empty_like(k, stream)
-            sok = _rotary_rows("out_k", out_k, dev, dtype, k.shape)
+            out_k, sok = _new_like(torch, k, stream)
         k_ptr, ok_ptr = k.data_ptr(), out_k.data_ptr()
     opt = ROTARY_OPTIONS.pack(1 if interleaved else 0, 1 if inverse else 0, scale, positions.dtype == torch.int64, shared,
                               0, *sq, *sk, *soq, *sok)
-    _launch(dev, stream, "tl_rotary", tl_rotary, q.data_ptr(), k_ptr, out_q.data_ptr(), ok_ptr, positions.data_ptr(),
+    _launch(torch, dev, stream, "tl_rotary", tl_rotary, q.data_ptr(), k_ptr, out_q.data_ptr(), ok_ptr, positions.data_ptr(),
             inv_freq.data_ptr(), B, H, Hk, S, D, 2 * half, dt, opt)
     return out_q, out_k
 
