@@ -12,7 +12,11 @@
 // scores and adds step n - 1's P V, so the warpgroup never waits for a product;
 // with one set of 128 columns a tile it did, each block: 1970 clocks a tile and
 // block (and 2500 with two warpgroups a tile, which have to agree on the row's
-// maximum).  Each tile visits only the steps that some of its rows see; inside,
+// maximum).  With D = 64 Tensor Memory has room for sums of each set: each has a
+// warpgroup of its own (TWIN), which keep maxima of their own and join at the
+// item's end, so twice as many warps cover one another's latency (causal 2 x 16
+// heads x 4096: 111 -> 106 us, capped 191 -> 174, with cap and bias 237 -> 201).
+// Each tile visits only the steps that some of its rows see; inside,
 // only steps that cut a row's interval pay for masking.
 //
 // CTAs are persistent: a CTA whose item's loads are out takes over one that has
@@ -30,12 +34,14 @@
 // 48 bytes of operands for every 32 clocks' worth of products), against one 2^x a
 // pair at 16 a clock (1024 clocks); capped scores add the multiply-adds of
 // tanh_scores.  Measured, 4 x 16 heads x 4096 x 4096, bf16: D = 128 435 us, 1265
-// TFLOP/s (causal 260); D = 64, 2 x 16 heads, 231 us, 595 TFLOP/s.  The warpgroup's
-// own latency bounds: two warps a scheduler, each 2^x, sum and pack in a chain
-// (the tensor pipe 32..75 % busy, the special-function pipe 32..51 %).
+// TFLOP/s (causal 260); D = 64, 2 x 16 heads, 211 us, 652 TFLOP/s.  The chains' own
+// latency bounds: scores, 2^x, sum, pack, P V and the next scores follow one
+// another in each set (the tensor pipe 32..75 % busy, the special-function pipe
+// 32..56 %).
 //
 // Warps: 0 items and TMA loads, 1 issues S (and allocates Tensor Memory), 2 issues
-// P V, 3 idle, 4..7 softmax of tile 0, 8..11 of tile 1.  Every wait is bounded.
+// P V, 3 idle, 4..7 softmax of tile 0, 8..11 of tile 1 (TWIN: of set 0; 12..19 of
+// set 1).  Every wait is bounded.
 #pragma once
 
 #include "attention_common.cuh"
@@ -57,6 +63,8 @@ struct AttnExParams {
 template <int D_>
 struct AttnExConfig {
     static constexpr int D = D_;
+    static constexpr bool TWIN = D == 64;                  // a warpgroup for each set of a tile
+    static constexpr int WARPS = TWIN ? 16 : 8;            // of the softmax
     static constexpr int BM = 128, BN = 128;
     static constexpr int KS = D == 128 ? 2 : 4;            // K and V ring depth
     static constexpr int ATOM_BYTES = 128 * 128;           // 128 rows x 64 16-bit values
@@ -67,27 +75,30 @@ struct AttnExConfig {
     static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
     static constexpr int OFF_V = OFF_K + KS * KV_BYTES;
     static constexpr int OFF_OUT = OFF_V + KS * KV_BYTES;  // [warp] 32 rows x 32 columns on their way out
-    static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
+    static constexpr int OFF_ML = OFF_OUT + WARPS * 2048;  // TWIN: [item & 1][tile][set][128] float2
+    static constexpr int OFF_BAR = OFF_ML + (TWIN ? 2 * 2 * 2 * 128 * 8 : 0);
     static constexpr int BAR_QF = 0, BAR_QE = 1;
     static constexpr int BAR_KF = 2, BAR_KE = 2 + KS, BAR_VF = 2 + 2 * KS, BAR_VE = 2 + 3 * KS;
     static constexpr int BAR_SF = 2 + 4 * KS;   // [tile][set]: S in Tensor Memory
     static constexpr int BAR_PF = BAR_SF + 4;   // [tile][set]: P in Tensor Memory (4 warps)
     static constexpr int BAR_PV = BAR_PF + 4;   // [tile][set]: O += P V completed
-    static constexpr int BAR_OE = BAR_PV + 4;   // [tile]: O has been read (4 warps)
+    static constexpr int BAR_OE = BAR_PV + 4;   // [tile]: O has been read (its warps)
     static constexpr int BAR_TF = BAR_OE + 2;   // [slot]: an item's description is in shared memory
-    static constexpr int BAR_TE = BAR_TF + 2;   // [slot]: and has been read (10: two MMA issuers, 8 warps)
+    static constexpr int BAR_TE = BAR_TF + 2;   // [slot]: and has been read (two MMA issuers, the softmax warps)
     static constexpr int BAR_CLC = BAR_TE + 2;  // the answer to a request for another item
     static constexpr int BAR_DRAIN = BAR_CLC + 1;
-    static constexpr int NUM_BARS = BAR_DRAIN + 1;
+    static constexpr int BAR_ML = BAR_DRAIN + 1;  // TWIN: [tile]: both sets are complete, their statistics in shared memory (8 warps)
+    static constexpr int NUM_BARS = BAR_ML + 2;
     static constexpr int OFF_MISC = OFF_BAR + (NUM_BARS * 8 + 15) / 16 * 16;  // TMEM address, abort flag
     static constexpr int OFF_CLC = OFF_MISC + 16;
     static constexpr int OFF_ITEMS = OFF_CLC + 16;      // [slot] pair, head, first and end step of each tile
     static constexpr int SMEM_BYTES = OFF_ITEMS + 2 * 32 + 1024;
-    static constexpr int THREADS = 384;
-    static constexpr int REGS_CONTROL = 104, REGS_SOFTMAX = 200;
-    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 256 * REGS_SOFTMAX + THREADS - 1) / THREADS;
+    static constexpr int THREADS = 128 + 32 * WARPS;
+    static constexpr int REGS_CONTROL = TWIN ? 64 : 104, REGS_SOFTMAX = TWIN ? 104 : 200;
+    static constexpr int LAUNCH_REGS = (128 * REGS_CONTROL + 32 * WARPS * REGS_SOFTMAX + THREADS - 1) / THREADS;
     static constexpr int BS = 64;               // keys a step
-    static constexpr int TMEM_S = 0, TMEM_O = 256;  // set h of tile i at 128 i + 64 h, O at 256 + D i
+    // set h of tile i at 128 i + 64 h, its O at 256 + 128 i, TWIN: + 64 h (else one for both sets)
+    static constexpr int TMEM_S = 0, TMEM_O = 256;
     static constexpr float RESCALE_LOG2 = 8.0f;     // m moves when a row maximum exceeds it by 2^8
     static_assert(D == 64 || D == 128, "head dim");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -120,7 +131,7 @@ __device__ __forceinline__ int clc_answer(uint32_t src)
 }
 
 template <class CF, int DT, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(CF::THREADS, 1)
     attention_ex_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
                         const AttnExParams p)
@@ -151,9 +162,10 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(bar(CF::BAR_VE + s), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(CF::BAR_OE + i), 4);
+            mbar_init(bar(CF::BAR_OE + i), CF::WARPS / 2);
+            mbar_init(bar(CF::BAR_ML + i), CF::WARPS / 2);
             mbar_init(bar(CF::BAR_TF + i), 1);
-            mbar_init(bar(CF::BAR_TE + i), 10);
+            mbar_init(bar(CF::BAR_TE + i), 2 + CF::WARPS);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(CF::BAR_SF + i), 1);
@@ -430,7 +442,8 @@ __global__ void __launch_bounds__(384, 1)
                         if (!ok || !it.visits(i, 2 * j + set))
                             continue;
                         const uint32_t c = count[i][set];
-                        const bool first = 2 * j + set == it.fs[i];
+                        // its sums begin here: those of both sets, or (TWIN) of this one
+                        const bool first = CF::TWIN ? 2 * j + set < it.fs[i] + 2 : 2 * j + set == it.fs[i];
                         // the last item's O has been read before this one's begins
                         if ((first && busy[i] > 0 && !(ok = wait(CF::BAR_OE + i, busy[i] - 1))) ||
                             !(ok = wait(CF::BAR_PF + 2 * i + set, c)))
@@ -440,19 +453,21 @@ __global__ void __launch_bounds__(384, 1)
                             const uint64_t vd = v_desc + ((st * CF::KV_BYTES + set * CF::BS * 128) >> 4);
 #pragma unroll
                             for (int k = 0; k < CF::BS / 16; ++k)
-                                tc_mma_f16_ts(tmem_base + static_cast<uint32_t>(CF::TMEM_O + i * D),
+                                tc_mma_f16_ts(tmem_base + static_cast<uint32_t>(CF::TMEM_O + i * 128 + (CF::TWIN ? set * D : 0)),
                                               tmem_base + static_cast<uint32_t>(CF::TMEM_S + i * 128 + set * CF::BS + 8 * k),
                                               vd + ((2048 * k) >> 4), IDESC_PV, (!first || k > 0) ? 1u : 0u);
                             tc_commit(bar(CF::BAR_PV + 2 * i + set));
                         }
                         __syncwarp();
                         count[i][set] = c + 1;
-                        busy[i] += first ? 1u : 0u;
                     }
                     if (ok && elect_one())
                         tc_commit(bar(CF::BAR_VE + st));
                     __syncwarp();
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    busy[i] += it.es[i] > it.fs[i] ? 1u : 0u;
             }
             if (elect_one())
                 tc_commit(bar(CF::BAR_DRAIN));
@@ -463,12 +478,14 @@ __global__ void __launch_bounds__(384, 1)
     } else {
         regs_increase<CF::REGS_SOFTMAX>();
         // ------------------------------------------------------------ softmax and output of one tile
-        constexpr int HN = CF::BS;
-        const int tile = (warp - 4) >> 2;
+        constexpr int HN = CF::TWIN ? CF::BS / 2 : CF::BS;  // columns in registers at a time
+        const int tile = ((warp - 4) >> 2) & 1;
+        const int own = CF::TWIN ? (warp - 4) >> 3 : 0;  // TWIN: the set
         const int r = (warp & 3) * 32 + lane;  // row of the tile (Tensor Memory lane)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_addr0 = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_S + tile * 128);
-        const uint32_t o_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + tile * D);
+        const uint32_t o_addr = tmem_base + lane_base + static_cast<uint32_t>(CF::TMEM_O + tile * 128);
+        const uint32_t o_own = o_addr + static_cast<uint32_t>(own * D);
         uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 2048);
         auto wait_warp = [&](int id, uint32_t par) -> bool {
             return __all_sync(0xffffffffu, wait_bounded(bar(id), par & 1u, abort_flag, timeout, ERR_EPILOGUE));
@@ -486,48 +503,83 @@ __global__ void __launch_bounds__(384, 1)
             const int pos = p.mask.q_offset + row;
             // m: the reference maximum of the row's weights (log2 units); l: sum of the weights against m
             float m = -INFINITY, l = 0.0f;
-            for (int n = fs; n < es; ++n) {
-                const int set = n & 1;
+            const int n_first = CF::TWIN ? fs + ((fs ^ own) & 1) : fs;
+            for (int n = n_first; n < es; n += CF::TWIN ? 2 : 1) {
+                const int set = CF::TWIN ? own : n & 1;
                 const uint32_t c = set ? count[1] : count[0];
                 if (!(ok = wait_warp(CF::BAR_SF + 2 * tile + set, c)))
                     break;
                 tc_fence_after_sync();
                 const uint32_t s_addr = s_addr0 + static_cast<uint32_t>(CF::BS * set);
                 const int key0 = n * CF::BS;
-                uint32_t sv[HN];
-                tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-                tmem_load_wait();
-                // tanh of the capped scores, or biased scores in log2 units, in place of the raw ones
-                if constexpr (CAP)
-                    tanh_scores<HN>(sv, p.score.cap_arg);
                 const float to_log2 = CAP ? p.score.cap_log2 : p.score.scale_log2;  // of a score without a bias
-                if constexpr (BIAS) {
-                    const float dist0 = static_cast<float>(pos - key0);
-#pragma unroll
-                    for (int e = 0; e < HN; e += 2) {
-                        float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), splat2(to_log2));
-                        const float2 dist = fadd2(splat2(dist0), make_float2(-static_cast<float>(e), -static_cast<float>(e + 1)));
-                        x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
-                        sv[e] = __float_as_uint(x.x);
-                        sv[e + 1] = __float_as_uint(x.y);
-                    }
-                }
                 const int nlo = seen.x - key0, nhi = seen.y - key0;
-                if (!__all_sync(0xffffffffu, nlo <= 0 && nhi >= HN)) {
-                    // keys outside the row's interval count neither in the maximum nor in the weights
+                const bool cut = !__all_sync(0xffffffffu, nlo <= 0 && nhi >= CF::BS);
+                // keys outside the row's interval count neither in the maximum nor in the weights
+                auto hide = [&](uint32_t (&sv)[HN], int e0) {
+                    if (cut && CF::TWIN) {  // by bits: fewer registers
+                        const int lo = min(max(nlo - e0, 0), 32), hi = min(max(nhi - e0, 0), 32);
+                        const uint32_t see = static_cast<uint32_t>((1ull << hi) - 1ull) & ~static_cast<uint32_t>((1ull << lo) - 1ull);
 #pragma unroll
-                    for (int e = 0; e < HN; ++e)
-                        if (e < nlo || e >= nhi)
-                            sv[e] = __float_as_uint(-INFINITY);
-                }
-                float g[8];  // maxima of groups of 8 scores
+                        for (int e = 0; e < HN; ++e)
+                            if (!(see & (1u << (e & 31))))
+                                sv[e] = __float_as_uint(-INFINITY);
+                    } else if (cut) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float *f = reinterpret_cast<const float *>(&sv[8 * i]);
-                    g[i] = fmax3(fmax3(f[0], f[1], f[2]), fmax3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+                        for (int e = 0; e < HN; ++e)
+                            if (e0 + e < nlo || e0 + e >= nhi)
+                                sv[e] = __float_as_uint(-INFINITY);
+                    }
+                };
+                // columns e0 ..: tanh of the capped scores, or biased scores in log2 units, in place of the raw ones
+                auto scores = [&](uint32_t (&sv)[HN], int e0) {
+                    if constexpr (CAP)
+                        tanh_scores<HN>(sv, p.score.cap_arg);
+                    if constexpr (BIAS) {
+                        const float dist0 = static_cast<float>(pos - key0 - e0);
+#pragma unroll
+                        for (int e = 0; e < HN; e += 2) {
+                            float2 x = fmul2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), splat2(to_log2));
+                            const float2 dist = fadd2(splat2(dist0), make_float2(-static_cast<float>(e), -static_cast<float>(e + 1)));
+                            x = ffma2(make_float2(fabsf(dist.x), fabsf(dist.y)), splat2(-slope2), x);
+                            sv[e] = __float_as_uint(x.x);
+                            sv[e + 1] = __float_as_uint(x.y);
+                        }
+                    }
+                    hide(sv, e0);
+                };
+                auto top = [&](const uint32_t (&sv)[HN]) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < HN / 8; ++i) {
+                        const float *f = reinterpret_cast<const float *>(&sv[8 * i]);
+                        mx = fmax3(mx, fmax3(fmax3(f[0], f[1], f[2]), f[3], f[4]), fmax3(f[5], f[6], f[7]));
+                    }
+                    return mx;
+                };
+                uint32_t sv[HN], p1[CF::TWIN ? HN / 2 : 1];
+                float mx;
+                if constexpr (CF::TWIN) {
+                    // 32 columns at a time: the first half waits in Tensor Memory for its second reading
+                    tmem_load_32cols(s_addr, sv);
+                    tmem_load_wait();
+                    scores(sv, 0);
+                    mx = top(sv);
+                    if constexpr (CAP || BIAS)
+                        tmem_store_32cols(s_addr, sv);
+                    tmem_load_32cols(s_addr + HN, sv);
+                    tmem_load_wait();
+                    scores(sv, HN);
+                    mx = fmaxf(mx, top(sv));
+                    if constexpr (CAP || BIAS)
+                        tmem_store_wait();
+                } else {
+                    tmem_load_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    tmem_load_32cols(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[HN - 32]));
+                    tmem_load_wait();
+                    scores(sv, 0);
+                    mx = top(sv);
                 }
-                float mx = fmax3(fmax3(g[0], g[1], g[2]), fmax3(g[3], g[4], g[5]), fmaxf(g[6], g[7]));
                 if constexpr (!BIAS)
                     mx *= to_log2;
                 // move the reference maximum only when the weights would exceed 2^8
@@ -537,33 +589,49 @@ __global__ void __launch_bounds__(384, 1)
                 const float alpha = resc ? exp2_approx_ftz(m - m_ref) : 1.0f;  // 0 when m is -inf
                 const float2 negm2 = splat2(-m_ref);
                 float2 part[4] = {splat2(0.0f), splat2(0.0f), splat2(0.0f), splat2(0.0f)};
+                auto weights = [&](const uint32_t (&sv)[HN], uint32_t *out) {
 #pragma unroll
-                for (int e = 0; e < HN; e += 2) {
-                    const float2 s = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                    const float2 x = BIAS ? fadd2(s, negm2) : ffma2(s, splat2(to_log2), negm2);
-                    const float2 w = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
-                    part[(e >> 1) & 3] = fadd2(part[(e >> 1) & 3], w);
-                    sv[e / 2] = pack2<DT>(w.x, w.y);  // keys e, e + 1: one 32-bit column
+                    for (int e = 0; e < HN; e += 2) {
+                        const float2 s = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                        const float2 x = BIAS ? fadd2(s, negm2) : ffma2(s, splat2(to_log2), negm2);
+                        const float2 w = make_float2(exp2_approx_ftz(x.x), exp2_approx_ftz(x.y));
+                        part[(e >> 1) & 3] = fadd2(part[(e >> 1) & 3], w);
+                        out[e / 2] = pack2<DT>(w.x, w.y);  // keys e, e + 1: one 32-bit column
+                    }
+                };
+                if constexpr (CF::TWIN) {
+                    weights(sv, p1);
+                    tmem_load_32cols(s_addr, sv);
+                    tmem_load_wait();
+                    if constexpr (!(CAP || BIAS))
+                        hide(sv, 0);
+                    uint32_t p0[HN / 2];
+                    weights(sv, p0);
+                    tmem_store_16cols(s_addr, p0);
+                    tmem_store_16cols(s_addr + HN / 2, p1);
+                } else {
+                    weights(sv, sv);
+                    tmem_store_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
                 }
-                tmem_store_32cols(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
                 const float2 ps = fadd2(fadd2(part[0], part[1]), fadd2(part[2], part[3]));
                 l = l * alpha + (ps.x + ps.y);
                 m = m_new;
                 // rows whose maximum moved take O down by alpha once it holds all steps before n (those before
-                // n - 1 are in it: S(n - 1) was issued behind the P V of n - 3, S(n) behind that of n - 2)
-                if (n > fs && __any_sync(0xffffffffu, resc)) {
-                    if (!(ok = wait_warp(CF::BAR_PV + 2 * tile + (set ^ 1), (set ? count[0] : count[1]) - 1)))
+                // n - 1 are in it: S(n - 1) was issued behind the P V of n - 3, S(n) behind that of n - 2; TWIN: that
+                // was the set's last)
+                if (n > n_first && __any_sync(0xffffffffu, resc)) {
+                    if (!CF::TWIN && !(ok = wait_warp(CF::BAR_PV + 2 * tile + (set ^ 1), (set ? count[0] : count[1]) - 1)))
                         break;
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int k = 0; k < D / 32; ++k) {
                         uint32_t o[32];
-                        tmem_load_32cols(o_addr + 32 * k, o);
+                        tmem_load_32cols(o_own + 32 * k, o);
                         tmem_load_wait();
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_store_32cols(o_addr + 32 * k, o);
+                        tmem_store_32cols(o_own + 32 * k, o);
                     }
                 }
                 tmem_store_wait();
@@ -584,15 +652,60 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok)
                 break;
             tc_fence_after_sync();
-            if (p.splits > 1) {
-                const int64_t at = (static_cast<int64_t>(it.slot) * 2 + tile) * 128 + r;
-                p.part_ml[at] = make_float2(m, l);
-                float4 *part = p.part_o + (static_cast<int64_t>(it.slot) * 2 + tile) * (D / 4) * 128 + r;
-#pragma unroll 1
-                for (int k = 0; k < D / 32 && es > fs; ++k) {
-                    uint32_t o[32];
+            // TWIN: the sets' sums are joined, half the columns by each of their warpgroups
+            float f0 = 1.0f, f1 = 0.0f;
+            bool has0 = true, has1 = false;
+            if constexpr (CF::TWIN) {
+                float2 *ml = reinterpret_cast<float2 *>(smem + CF::OFF_ML) + ((t & 1) * 2 + tile) * 256 + r;
+                ml[own * 128] = make_float2(m, l);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(CF::BAR_ML + tile));
+                if (!(ok = wait_warp(CF::BAR_ML + tile, static_cast<uint32_t>(t))))
+                    break;
+                tc_fence_after_sync();
+                const float2 a = ml[0], c = ml[128];
+                m = fmaxf(a.x, c.x);
+                f0 = a.x == -INFINITY ? 0.0f : exp2_approx_ftz(a.x - m);
+                f1 = c.x == -INFINITY ? 0.0f : exp2_approx_ftz(c.x - m);
+                l = a.y * f0 + c.y * f1;
+                has0 = es - fs >= 2 || (fs & 1) == 0;
+                has1 = es - fs >= 2 || (fs & 1) == 1;
+            }
+            const int k0 = CF::TWIN ? own : 0, k1 = CF::TWIN ? own + 1 : D / 32;  // of 32 columns
+            auto load_sums = [&](int k, uint32_t (&o)[32]) {
+                if constexpr (CF::TWIN) {
                     tmem_load_32cols(o_addr + 32 * k, o);
                     tmem_load_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = has0 ? __float_as_uint(__uint_as_float(o[e]) * f0) : 0u;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t other[16];
+                        tmem_load_16cols(o_addr + D + 32 * k + 16 * c, other);
+                        tmem_load_wait();
+                        if (has1) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[16 * c + e] = __float_as_uint(fmaf(__uint_as_float(other[e]), f1, __uint_as_float(o[16 * c + e])));
+                        }
+                    }
+                } else {
+                    tmem_load_32cols(o_addr + 32 * k, o);
+                    tmem_load_wait();
+                }
+            };
+            if (p.splits > 1) {
+                const int64_t at = (static_cast<int64_t>(it.slot) * 2 + tile) * 128 + r;
+                if (own == 0)
+                    p.part_ml[at] = make_float2(m, l);
+                float4 *part = p.part_o + (static_cast<int64_t>(it.slot) * 2 + tile) * (D / 4) * 128 + r;
+#pragma unroll 1
+                for (int k = k0; k < k1 && es > fs; ++k) {
+                    uint32_t o[32];
+                    load_sums(k, o);
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
                         part[(8 * k + v) * 128] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
@@ -610,12 +723,11 @@ __global__ void __launch_bounds__(384, 1)
             const float inv = empty ? 0.0f : 1.0f / l;
             const int row0 = it.q0 + tile * CF::BM + (warp & 3) * 32;  // this warp's first row
 #pragma unroll 1
-            for (int k = 0; k < D / 32; ++k) {
+            for (int k = k0; k < k1; ++k) {
                 uint32_t o[32];
                 if (es > fs) {
-                    tmem_load_32cols(o_addr + 32 * k, o);
-                    tmem_load_wait();
-                    if (k + 1 == D / 32) {  // in registers: the next item's O may begin
+                    load_sums(k, o);
+                    if (k + 1 == k1) {  // in registers: the next item's O may begin
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0)
@@ -646,7 +758,7 @@ __global__ void __launch_bounds__(384, 1)
                     bulk_commit_group();
                 }
             }
-            if (p.lse && row < p.mask.Sq)
+            if (p.lse && own == 0 && row < p.mask.Sq)
                 p.lse[(static_cast<int64_t>(it.b) * p.H + it.h) * p.mask.Sq + row] =
                     empty ? -INFINITY : m * 0.69314718055994531f + logf(l);
         }
