@@ -102,3 +102,56 @@ def test_serving_gives_the_prefill_rows():
     tree = tg.tree_attention(tq, kc, vc, table, context, parents, score_cap=CAP)
     assert tg.check_device() == 0
     close("tree", tree[:, :, mine], p.out[:, :, n0:], p.out_bound()[:, :, n0:])
+
+
+def test_split_and_cut_calls_at_once_and_in_two_graphs():
+    """Calls whose work is split over CTAs and joined (few items, few tiles, one long request) on several streams at
+    once, then captured twice and replayed side by side: bit for bit the results of the same calls one at a time."""
+    import tensor_core_gemm_tl_b200 as tg
+    g = torch.Generator(device="cuda").manual_seed(11)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+    q, k, v, do = rand(1, 6, 900, 64), rand(1, 1, 900, 64), rand(1, 1, 900, 64), rand(1, 6, 900, 64)
+    qt, cache = rand(2, 8, 3, 128), rand(2 * 160, 16, 2, 128)
+    table = torch.randperm(320, generator=g, device="cuda").to(torch.int32).view(2, 160)
+    context = torch.tensor([2500, 700], device="cuda", dtype=torch.int32)
+
+    def step(stream=None):
+        lse = torch.empty((1, 6, 900), device="cuda")
+        if stream is not None:
+            lse.record_stream(stream)
+        o = tg.attention_ex(q, k, v, causal=True, lse=lse, stream=stream)
+        grads = tg.attention_backward(do, q, k, v, o, lse, causal=True, stream=stream)
+        few = tg.attention_ex(q[:, :2, :50], k, v, q_offset=850, causal=True, stream=stream)
+        t = tg.tree_attention(qt, cache, cache, table, context, stream=stream)
+        return [o, lse, *grads, few, t]
+
+    want = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [step(streams[i % 3]) for i in range(12)]
+    torch.cuda.synchronize()
+    assert tg.check_device() == 0
+    for r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+    graphs, outs = [], []
+    for s in streams[:2]:
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs.append(step())
+        graphs.append(graph)
+    for n in range(5):
+        for r in outs:
+            for t in r:
+                t.zero_()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for r in outs:
+            assert all(torch.equal(a, b) for a, b in zip(r, want)), n
+    assert tg.check_device() == 0
