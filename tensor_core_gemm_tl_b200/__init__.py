@@ -316,7 +316,8 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: 
                        stream=None):
     """Gradients (dq, dk, dv) of attention_ex, from its inputs, its ``out`` and
     ``lse`` and the gradient ``dout`` of out; the options are the forward's.
-    dk and dv are summed over the heads that share them.  Results repeat bit
+    dk and dv are summed over the heads that share them.  What no query sees, and
+    queries that see nothing, do not count but must be finite.  Results repeat bit
     for bit."""
     import torch
     head, strides, dt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
