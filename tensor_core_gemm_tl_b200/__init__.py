@@ -33,13 +33,18 @@ __all__ = [
 ]
 
 
+_DTYPE_CODES = {}  # torch's dtypes: filled at the first call, as torch is imported late
+
+
 def _dtype_code(t):
-    import torch
-    if t.dtype == torch.float16:
-        return TL_F16
-    if t.dtype == torch.bfloat16:
-        return TL_BF16
-    raise TypeError(f"expected float16 or bfloat16, got {t.dtype}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        import torch
+        _DTYPE_CODES.update({torch.float16: TL_F16, torch.bfloat16: TL_BF16})
+        code = _DTYPE_CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"expected float16 or bfloat16, got {t.dtype}")
+    return code
 
 
 _EPILOGUES = {None: TL_EPI_NONE, "none": TL_EPI_NONE, "bias_gelu": TL_EPI_BIAS_GELU,
@@ -191,6 +196,10 @@ def _rows(name, t, device, dtype, shape):
     aligned base."""
     if t.dtype is not dtype or t.shape != shape or t.device != device:
         _refuse(name, t, device, dtype, shape)
+    return _strides(name, t)
+
+
+def _strides(name, t):
     st = t.stride()
     s0, s1, s2, s3 = st
     if s3 != 1 or s0 <= 0 or s1 <= 0 or s2 <= 0 or (s0 | s1 | s2) & 7:
@@ -226,15 +235,14 @@ def _score_arguments(scale, score_cap, slopes, heads, device):
     return slopes.data_ptr()
 
 
-def _launch(torch, device, stream, what, call, *args):
-    """call(*args but the options, raw stream, options) with `device` current, on `stream` or torch's current one;
-    raises TLError."""
+def _launch(torch, device, stream, options, what, call, *args):
+    """call(*args, raw stream, options) with `device` current, on `stream` or torch's current one; raises TLError."""
     raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == device.index:
-        st = call(*args[:-1], raw, args[-1])
+        st = call(*args, raw, options)
     else:
         with torch.cuda.device(device):
-            st = call(*args[:-1], raw, args[-1])
+            st = call(*args, raw, options)
     if st != 0:
         raise TLError(st, what)
 
@@ -254,8 +262,11 @@ def _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets,
         raise ValueError("q must be a CUDA tensor")
     dt = _dtype_code(q)
     dev, dtype = q.device, q.dtype
-    strides = _rows("q", q, dev, dtype, q.shape) + _rows("k", k, dev, dtype, k.shape) + \
-        _rows("v", v, dev, dtype, v.shape)
+    if k.dtype is not dtype or k.device != dev:
+        _refuse("k", k, dev, dtype, k.shape)
+    if v.dtype is not dtype or v.device != dev:
+        _refuse("v", v, dev, dtype, v.shape)
+    strides = _strides("q", q) + _strides("k", k) + _strides("v", v)
     slopes_ptr = _score_arguments(scale, score_cap, slopes, H, dev)
     docs = docs_ptr = prefix_ptr = 0
     if doc_offsets is not None:
@@ -306,8 +317,8 @@ def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap
     else:
         so = _rows("out", out, dev, q.dtype, q.shape)
     opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *_DENSE, *_DENSE, *_DENSE, *_DENSE)
-    _launch(torch, dev, stream, "tl_attention_ex", tl_attention_ex, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-            lse_ptr, B, H, Sq, k.shape[2], D, dt, opt)
+    _launch(torch, dev, stream, opt, "tl_attention_ex", tl_attention_ex, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            out.data_ptr(), lse_ptr, B, H, Sq, k.shape[2], D, dt)
     return out
 
 
@@ -333,8 +344,9 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: 
     grads = [(g, sg) if g is not None else _new_like(torch, like, stream) for g, sg, like in grads]
     (dq, sdq), (dk, sdk), (dv, sdv) = grads
     opt = ATTENTION_OPTIONS.pack(*head, *strides, *so, *sdo, *sdq, *sdk, *sdv)
-    _launch(torch, dev, stream, "tl_attention_bwd", tl_attention_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Sq, k.shape[2], D, dt, opt)
+    _launch(torch, dev, stream, opt, "tl_attention_bwd", tl_attention_bwd, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Sq,
+            k.shape[2], D, dt)
     return dq, dk, dv
 
 
@@ -364,9 +376,11 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
         raise ValueError("q must be a CUDA tensor")
     dt = _dtype_code(q)
     dev, dtype, i32 = q.device, q.dtype, torch.int32
-    sq = _rows("q", q, dev, dtype, q.shape)
-    sk = _rows("k_cache", k_cache, dev, dtype, k_cache.shape)
-    sv = _rows("v_cache", v_cache, dev, dtype, v_cache.shape)
+    if k_cache.dtype is not dtype or k_cache.device != dev:
+        _refuse("k_cache", k_cache, dev, dtype, k_cache.shape)
+    if v_cache.dtype is not dtype or v_cache.device != dev:
+        _refuse("v_cache", v_cache, dev, dtype, v_cache.shape)
+    sq, sk, sv = _strides("q", q), _strides("k_cache", k_cache), _strides("v_cache", v_cache)
     if block_table.dim() != 2 or block_table.shape[1] < 1:
         raise ValueError(f"block_table must be (batch, pages), got {tuple(block_table.shape)}")
     max_pages = block_table.shape[1]
@@ -388,9 +402,9 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
     else:
         so = _rows("out", out, dev, dtype, q.shape)
     opt = TREE_OPTIONS.pack(scale, score_cap, slopes_ptr, 0, *sq, *so, *sk, *sv)
-    _launch(torch, dev, stream, "tl_tree_attention", tl_tree_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_table.data_ptr(), context_lens.data_ptr(), parents_ptr, lens_ptr, out.data_ptr(), lse_ptr, B, H, Hk, T,
-            pages, page_size, max_pages, D, dt, opt)
+    _launch(torch, dev, stream, opt, "tl_tree_attention", tl_tree_attention, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), parents_ptr, lens_ptr, out.data_ptr(), lse_ptr, B, H, Hk, T,
+            pages, page_size, max_pages, D, dt)
     return out
 
 
@@ -398,6 +412,10 @@ def _rotary_rows(name, t, device, dtype, shape):
     """The strides of a 4-D tensor for rotary, any positive ones with a contiguous last dimension."""
     if t.dtype is not dtype or t.shape != shape or t.device != device:
         _refuse(name, t, device, dtype, shape)
+    return _rotary_strides(name, t)
+
+
+def _rotary_strides(name, t):
     s0, s1, s2, s3 = t.stride()
     if s0 <= 0 or s1 <= 0 or s2 <= 0:  # a dimension of one element takes any stride
         n = t.shape
@@ -425,7 +443,7 @@ def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float
     dt = _dtype_code(q)
     B, H, S, D = q.shape
     dev, dtype = q.device, q.dtype
-    sq, sk, sok, Hk = _rotary_rows("q", q, dev, dtype, q.shape), _DENSE, _DENSE, 0
+    sq, sk, sok, Hk = _rotary_strides("q", q), _DENSE, _DENSE, 0
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k must be 4-D")
@@ -459,8 +477,8 @@ def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float
         k_ptr, ok_ptr = k.data_ptr(), out_k.data_ptr()
     opt = ROTARY_OPTIONS.pack(1 if interleaved else 0, 1 if inverse else 0, scale, positions.dtype == torch.int64, shared,
                               0, *sq, *sk, *soq, *sok)
-    _launch(torch, dev, stream, "tl_rotary", tl_rotary, q.data_ptr(), k_ptr, out_q.data_ptr(), ok_ptr, positions.data_ptr(),
-            inv_freq.data_ptr(), B, H, Hk, S, D, 2 * half, dt, opt)
+    _launch(torch, dev, stream, opt, "tl_rotary", tl_rotary, q.data_ptr(), k_ptr, out_q.data_ptr(), ok_ptr,
+            positions.data_ptr(), inv_freq.data_ptr(), B, H, Hk, S, D, 2 * half, dt)
     return out_q, out_k
 
 
