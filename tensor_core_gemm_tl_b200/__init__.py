@@ -403,8 +403,8 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
         so = _rows("out", out, dev, dtype, q.shape)
     opt = TREE_OPTIONS.pack(scale, score_cap, slopes_ptr, 0, *sq, *so, *sk, *sv)
     _launch(torch, dev, stream, opt, "tl_tree_attention", tl_tree_attention, q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), parents_ptr, lens_ptr, out.data_ptr(), lse_ptr, B, H, Hk, T,
-            pages, page_size, max_pages, D, dt)
+            v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), parents_ptr, lens_ptr, out.data_ptr(),
+            lse_ptr, B, H, Hk, T, pages, page_size, max_pages, D, dt)
     return out
 
 
