@@ -231,7 +231,8 @@ TL_API tl_status tl_attention_fwd(const void *Q, const void *K, const void *V, v
  * over the keys j that query i sees: with doc_offsets those of the document
  * that holds p_i (documents cut the keys at ascending offsets
  * o_0 <= o_1 <= ..., document d is [o_d, o_(d+1)), empty ones are fine;
- * positions outside [o_0, o_num_docs) -- a padded end -- belong to none), with
+ * positions outside [o_0, o_num_docs) -- a padded end -- belong to none; what of
+ * a document lies at or past seq_k has no keys), with
  * `causal` only j <= p_i and, with prefix_lens, the first prefix_lens keys of
  * the document (of the sequence, without documents) besides.  A query that
  * sees no key gets O = 0 and lse = -inf.  Offsets and prefixes live on the

@@ -262,12 +262,17 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
                     // row's end: lanes 2 i and 2 i + 1 look up tile i's first and last row that lie in a document.
                     int i0 = x.x * 2 * CF::BM + ((lane >> 1) & 1) * CF::BM, i1 = min(i0 + CF::BM, p.mask.Sq) - 1;
                     if (docs) {
-                        i0 = max(i0, docs[0] - p.mask.q_offset);
-                        i1 = min(i1, docs[p.mask.num_docs] - 1 - p.mask.q_offset);
+                        i0 = max(i0, max(docs[0], 0) - p.mask.q_offset);
+                        i1 = min(i1, max(docs[p.mask.num_docs], 0) - 1 - p.mask.q_offset);
                     }
+                    // A row of a document that begins past the keys sees none of them, and stands for their end: a
+                    // tile that begins there has none, one that ends there has rows that see them to the end.
                     int2 seen = make_int2(0, 0);
-                    if (lane < 4 && i0 <= i1)
+                    if (lane < 4 && i0 <= i1) {
                         seen = visible_keys(p.mask, docs, b, lane & 1 ? i1 : i0);
+                        if (seen.y <= seen.x)
+                            seen = make_int2(p.mask.Sk, p.mask.Sk);
+                    }
                     const int lo0 = __shfl_sync(0xffffffffu, seen.x, 0), hi0 = __shfl_sync(0xffffffffu, seen.y, 1);
                     const int lo1 = __shfl_sync(0xffffffffu, seen.x, 2), hi1 = __shfl_sync(0xffffffffu, seen.y, 3);
                     if (hi0 > lo0) {

@@ -1,0 +1,44 @@
+"""The attention operators where their ranges end, on the GPU against the plain 64-bit
+forms."""
+import os
+import sys
+
+import pytest
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+from attention_plain import close  # noqa: E402
+from test_attention_ex_gpu import problem  # noqa: E402
+
+# Documents that begin at or behind the last key: their queries see nothing, those before them in the same tile do
+PAST_THE_KEYS = {
+    "inside_a_tile": dict(shape=(1, 2, 1, 200, 100, 64), causal=True, docs=[[0, 50, 120, 200]]),
+    "at_the_end": dict(shape=(1, 2, 2, 130, 100, 128), docs=[[0, 100, 130]]),
+    "several_tiles": dict(shape=(2, 2, 2, 700, 300, 128), causal=True, rows_first=True, bias=True,
+                          docs=[[0, 100, 290, 310, 700], [0, 300, 301, 640, 700]]),
+    "both_ways": dict(shape=(2, 4, 2, 400, 260, 64), docs=[[0, 255, 256, 280, 400], [0, 259, 260, 260, 1 << 30]]),
+    "prefixes": dict(shape=(1, 2, 1, 390, 300, 64), causal=True, docs=[[0, 150, 299, 320, 390]], prefix=[[40, 500, 60, 9]]),
+    # the keys of the few tiles are split over CTAs
+    "split": dict(shape=(1, 1, 1, 200, 600, 128), causal=True, offset=500, docs=[[0, 550, 620, 700]], cap=20.0, q_scale=4.0),
+    "none_left": dict(shape=(1, 2, 1, 140, 90, 64), docs=[[90, 140, 230]], offset=90),
+}
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("name", list(PAST_THE_KEYS))
+def test_documents_that_begin_past_the_keys(name, dt):
+    import tensor_core_gemm_tl_b200 as tg
+    q, k, v, do, how, p = problem(PAST_THE_KEYS[name], dt, seed=len(name))
+    lse = torch.full(q.shape[:3], 7.0, device="cuda")
+    out = tg.attention_ex(q, k, v, lse=lse, **how)
+    grads = tg.attention_backward(do, q, k, v, out, lse, **how)
+    assert tg.check_device() == 0
+    close("out", out, p.out, p.out_bound())
+    close("lse", lse, p.lse, p.lse_bound())
+    want, bounds = p.gradients(do)
+    for n, g, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(n, g, w, b)
