@@ -283,14 +283,14 @@ TL_API tl_status tl_attention_ex(const void *Q, const void *K, const void *V, vo
  *   dQ = scale dX K, dK = scale dX^T Q, dK and dV summed over the heads that share them
  *
  * P and dX are rounded to `dtype` between the products (fp16 holds them scaled
- * by powers of two, dX by one taken from the largest |dO|); every sum is fp32
- * and has a fixed order, so results repeat bit for bit.  Q and dO of queries that
- * see no key do not count, but must be finite (0 times NaN is NaN).  dQ, dK and dV must overlap
- * neither the inputs nor one another.  A stream-ordered temporary holds the
- * row sums and intervals (about 8 bytes a query and head) and, where few tiles
- * are cut into pieces, the pieces' sums (at most eight pieces an SM, 1 KB a
- * value of head_dim each).  Asynchronous on `stream`; bounded waits report
- * through tl_check_device.
+ * by powers of two, dX by one taken from the largest |dO| of queries that see
+ * some key); every sum is fp32 and has a fixed order, so results repeat bit for
+ * bit.  Q and dO of queries that see no key do not count, but must be finite
+ * (0 times NaN is NaN).  dQ, dK and dV must overlap neither the inputs nor one
+ * another.  A stream-ordered temporary holds the row sums and intervals (about 8
+ * bytes a query and head) and, where few tiles are cut into pieces, the pieces'
+ * sums (at most eight pieces an SM, 1 KB a value of head_dim each).  Asynchronous
+ * on `stream`; bounded waits report through tl_check_device.
  */
 TL_API tl_status tl_attention_bwd(const void *dO, const void *Q, const void *K, const void *V, const void *O,
                            const float *lse, void *dQ, void *dK, void *dV,

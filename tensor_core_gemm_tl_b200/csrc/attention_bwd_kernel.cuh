@@ -84,7 +84,7 @@ struct AttnBwdParams {
                                // exponent of P's factor, -delta
     const int32_t *intervals;  // [B][nqb][3][64]: first and end key of each query; 0.0f where it sees one key, else 1.0f
     const int4 *ranges;        // [B][nqb]: least first, largest end, largest first, least end of the block's queries
-    const unsigned *amax;      // fp16: bits of the largest |dO|, else null
+    const unsigned *amax;      // fp16: bits of the largest |dO| of queries that see some key, else null
     int32_t *next;             // counter that pieces are taken from, 0 at the start
     int32_t chunk, splits;     // a piece is up to `chunk` blocks of a tile, a tile `splits` pieces at most
     int32_t *pieces;           // [tiles of all heads]: how many a tile has; null where every tile is one
@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
 #pragma unroll
     for (int k = 0; k < RN; ++k) {
         float sum = 0.0f;
+        // fp16: queries that see nothing have no part in the factor of dX
+        const bool counts = __shfl_sync(0xffffffffu, l[k], threadIdx.x & 24) != -INFINITY;
 #pragma unroll
         for (int c = 0; c < WN; ++c) {
             const uint32_t ao[4] = {wo[k][c].x, wo[k][c].y, wo[k][c].z, wo[k][c].w};
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
                 const float g1 = to_float<DT>(static_cast<uint16_t>(ag[e] >> 16));
                 sum = fmaf(g0, to_float<DT>(static_cast<uint16_t>(ao[e] & 0xFFFFu)), sum);
                 sum = fmaf(g1, to_float<DT>(static_cast<uint16_t>(ao[e] >> 16)), sum);
-                if constexpr (DT == 0)
+                if (DT == 0 && counts)
                     top = fmaxf(top, fmaxf(fabsf(g0), fabsf(g1)));
             }
         }

@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
 
-from attention_plain import close  # noqa: E402
+from attention_plain import Plain, close  # noqa: E402
 from test_attention_ex_gpu import problem  # noqa: E402
 
 # Documents that begin at or behind the last key: their queries see nothing, those before them in the same tile do
@@ -40,5 +40,31 @@ def test_documents_that_begin_past_the_keys(name, dt):
     close("out", out, p.out, p.out_bound())
     close("lse", lse, p.lse, p.lse_bound())
     want, bounds = p.gradients(do)
+    for n, g, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(n, g, w, b)
+
+
+# ------------------------------------------------------------------ fp16 gradients
+@pytest.mark.parametrize("how", [dict(docs=[[20, 150, 260]]), dict(docs=[[20, 150, 260]], causal=True),
+                                 dict(docs=[[20, 21, 150, 260]], causal=True, prefix=[[0, 30, 200]]),
+                                 dict(causal=True, offset=5, queries=140)])
+def test_fp16_gradients_beside_rows_that_do_not_count(how):
+    """Queries that see nothing and keys that nobody sees, left with large finite numbers, take nothing of the small
+    gradients' precision."""
+    import tensor_core_gemm_tl_b200 as tg
+    how = dict(how)
+    sq = how.pop("queries", 300)
+    q, k, v, do, how, p = problem(dict(shape=(1, 4, 2, sq, 300, 64), **how), "fp16", seed=8)
+    do = (do * 1e-3).half()
+    see = p.see.cpu()
+    queries, keys = see.any(2)[0].cuda(), see.any(1)[0].cuda()
+    assert not (queries.all() and keys.all())
+    p = Plain(q, k, v, see, p.scale)
+    want, bounds = p.gradients(do * queries[:, None])
+    q[:, :, ~queries], do[:, :, ~queries] = 1000.0, 60000.0
+    k[:, :, ~keys], v[:, :, ~keys] = 100.0, 60000.0
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = tg.attention_ex(q, k, v, lse=lse, **how)
+    grads = tg.attention_backward(do, q, k, v, out, lse, **how)
     for n, g, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
         close(n, g, w, b)
