@@ -283,8 +283,8 @@ TL_API tl_status tl_attention_ex(const void *Q, const void *K, const void *V, vo
  *   dQ = scale dX K, dK = scale dX^T Q, dK and dV summed over the heads that share them
  *
  * P and dX are rounded to `dtype` between the products (fp16 holds them scaled
- * by powers of two, dX by one taken from the largest |dO| of queries that see
- * some key); every sum is fp32 and has a fixed order, so results repeat bit for
+ * by powers of two, dX by one that the largest rows of dO and V that count cannot
+ * make too large); every sum is fp32 and has a fixed order, so results repeat bit for
  * bit.  Q and dO of queries that see no key do not count, but must be finite
  * (0 times NaN is NaN).  dQ, dK and dV must overlap neither the inputs nor one
  * another.  A stream-ordered temporary holds the row sums and intervals (about 8

@@ -165,7 +165,11 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     rp.intervals = reinterpret_cast<int32_t *>(at + rows_bytes);
     rp.ranges = reinterpret_cast<int4 *>(at + rows_bytes + interval_bytes);
     rp.next = reinterpret_cast<int32_t *>(at + rows_bytes + interval_bytes + range_bytes + 16);
-    rp.amax = dtype == TL_F16 ? reinterpret_cast<unsigned *>(at + rows_bytes + interval_bytes + range_bytes) : nullptr;
+    rp.norms = reinterpret_cast<float *>(at + rows_bytes + interval_bytes + range_bytes);
+    rp.Hk = static_cast<int32_t>(c.kv_heads);
+    rp.V = static_cast<const uint16_t *>(V);
+    rp.query_ctas = static_cast<int32_t>(nqb * batch * heads);
+    rp.nkb = static_cast<int32_t>(ceil_div(seq_k, kBwdCols));
     AttnBwdParams p{};
     p.mask = c.mask;
     p.score = score_params(c.scale, c.cap, c.slopes);
@@ -178,7 +182,7 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     p.rows = rp.rows;
     p.intervals = rp.intervals;
     p.ranges = rp.ranges;
-    p.amax = rp.amax;
+    p.norms = rp.norms;
     p.timeout_ns = kDefaultTimeoutNs;
     AttnBwdParams pk = p, pq = p;
     pq.next = rp.next;
@@ -197,11 +201,17 @@ tl_status attention_bwd_impl(const void *dO, const void *Q, const void *K, const
     for (int i = 0; i < 3; ++i) {
         rp.so[i] = c.o.s[i];
         rp.sdo[i] = sdo.s[i];
+        rp.sv[i] = c.v.s[i];
     }
-    if (rp.amax && cudaMemsetAsync(rp.amax, 0, sizeof(unsigned), stream) != cudaSuccess)
-        st = TL_ERR_CUDA;
+    // fp16: the norms that dX's factor comes from, those of V in CTAs behind the queries'
+    int64_t rows_grid = nqb * batch * heads;
+    if (dtype == TL_F16) {
+        rows_grid += rp.nkb * batch * c.kv_heads;
+        if (cudaMemsetAsync(rp.norms, 0, 2 * sizeof(float), stream) != cudaSuccess)
+            st = TL_ERR_CUDA;
+    }
     if (st == TL_OK)
-        st = launch_overlapped(e.rows[dtype], nqb * batch * heads, 256, 0, stream, rp);
+        st = launch_overlapped(e.rows[dtype], rows_grid, 256, 0, stream, rp);
     // persistent CTAs, one an SM; they take pieces from the passes' counters
     auto launch = [&](int dkv_pass, const CUtensorMap &x1, const CUtensorMap &x2, const CUtensorMap &y1,
                       const CUtensorMap &y2, const CUtensorMap &o0, const CUtensorMap &o1, int64_t items,

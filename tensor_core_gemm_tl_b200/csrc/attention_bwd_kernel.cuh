@@ -58,9 +58,12 @@
 // warps waiting for Tensor Memory loads and barriers.
 //
 // 16-bit range: bf16 takes P and dX as they are.  fp16 holds P times 2^10 and
-// dX times 2^4 over the power of two above the largest |dO| (P of long rows
-// and gradients of small losses lie below fp16's normal range); the factors
-// are powers of two and leave with the fp32 sums.
+// dX times 2^15 over a power of two that no |dX| exceeds (P of long rows and
+// gradients of small losses lie below fp16's normal range, dX of large values
+// above it).  O being a mean of rows of V, |dX_ij| <= |dO_i . (V_j - O_i)| <=
+// 2 max |dO_i| max |V_j|, 2-norms of the queries and keys that count: the rows
+// kernel takes them, those of V in CTAs of their own.  The factors are powers of
+// two and leave with the fp32 sums.
 #pragma once
 
 #include <type_traits>
@@ -84,7 +87,7 @@ struct AttnBwdParams {
                                // exponent of P's factor, -delta
     const int32_t *intervals;  // [B][nqb][3][64]: first and end key of each query; 0.0f where it sees one key, else 1.0f
     const int4 *ranges;        // [B][nqb]: least first, largest end, largest first, least end of the block's queries
-    const unsigned *amax;      // fp16: bits of the largest |dO| of queries that see some key, else null
+    const float *norms;        // fp16: the largest |dO_i|^2 of queries that see some key and |V_j|^2 of keys that some see
     int32_t *next;             // counter that pieces are taken from, 0 at the start
     int32_t chunk, splits;     // a piece is up to `chunk` blocks of a tile, a tile `splits` pieces at most
     int32_t *pieces;           // [tiles of all heads]: how many a tile has; null where every tile is one
@@ -115,19 +118,31 @@ __device__ __forceinline__ int2 bwd_tile(int i, int tiles, int BH, bool causal)
 
 struct AttnBwdRowsParams {
     MaskParams mask;
-    int32_t B, H, D, nqb;
-    const uint16_t *O, *dO;
-    int64_t so[3], sdo[3];
+    int32_t B, H, Hk, D, nqb;
+    int32_t query_ctas, nkb;   // CTAs for queries; blocks of 64 keys
+    const uint16_t *O, *dO, *V;
+    int64_t so[3], sdo[3], sv[3];
     const float *lse;          // [B][H][Sq]
     float *rows;
     int32_t *intervals;
     int4 *ranges;
-    unsigned *amax;
+    float *norms;              // fp16: as the passes', 0 at the start
     int32_t *next;             // the two passes' tile counters
 };
 
+// The largest of the warp's finite norms (inf and NaN spoil their own rows only) into `to`, of floats that are not
+// negative and so order like their bits
+__device__ __forceinline__ void raise_norm(float *to, float norm)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        norm = fmaxf(norm, __shfl_xor_sync(0xffffffffu, norm, off));
+    if ((threadIdx.x & 31) == 0)
+        atomicMax(reinterpret_cast<unsigned *>(to), __float_as_uint(norm));
+}
+
 // One CTA (256 threads) per 64 queries of a head: 8 lanes a row.  Bound by
-// reading O and dO once.
+// reading O and dO once.  fp16: then one per 64 keys of a head, for V's norms.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRowsParams p)
 {
@@ -135,6 +150,38 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
     __shared__ int red[4];
     grid_dependency_wait();
     grid_launch_dependents();
+    if (DT == 0 && static_cast<int>(blockIdx.x) >= p.query_ctas) {
+        const int at = static_cast<int>(blockIdx.x) - p.query_ctas;
+        const int bhk = at / p.nkb, b = bhk / p.Hk, hk = bhk - b * p.Hk, sub = threadIdx.x & 7;
+        const int32_t *docs = p.mask.doc_offsets
+                                  ? p.mask.doc_offsets + static_cast<int64_t>(b) * (p.mask.num_docs + 1) : nullptr;
+        float top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kBwdCols / 32; ++k) {
+            const int j = (at - bhk * p.nkb) * kBwdCols + (threadIdx.x >> 3) + 32 * k;
+            float norm = 0.0f;
+            if (key_is_seen(p.mask, docs, b, j)) {
+                const uint16_t *v = p.V + b * p.sv[0] + hk * p.sv[1] + static_cast<int64_t>(j) * p.sv[2];
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(v + 64 * c + 8 * sub));
+                    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v0 = to_float<DT>(static_cast<uint16_t>(a[e] & 0xFFFFu));
+                        const float v1 = to_float<DT>(static_cast<uint16_t>(a[e] >> 16));
+                        norm = fmaf(v0, v0, fmaf(v1, v1, norm));
+                    }
+                }
+            }
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1)
+                norm += __shfl_xor_sync(0xffffffffu, norm, off);
+            top = norm < INFINITY ? fmaxf(top, norm) : top;
+        }
+        raise_norm(p.norms + 1, top);
+        return;
+    }
     const int qb = static_cast<int>(blockIdx.x % p.nqb);
     const int bh = static_cast<int>(blockIdx.x / p.nqb);
     const int b = bh / p.H, h = bh % p.H;
@@ -198,9 +245,7 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
     }
 #pragma unroll
     for (int k = 0; k < RN; ++k) {
-        float sum = 0.0f;
-        // fp16: queries that see nothing have no part in the factor of dX
-        const bool counts = __shfl_sync(0xffffffffu, l[k], threadIdx.x & 24) != -INFINITY;
+        float sum = 0.0f, norm = 0.0f;
 #pragma unroll
         for (int c = 0; c < WN; ++c) {
             const uint32_t ao[4] = {wo[k][c].x, wo[k][c].y, wo[k][c].z, wo[k][c].w};
@@ -211,26 +256,26 @@ __global__ void __launch_bounds__(256) attention_bwd_rows_kernel(const AttnBwdRo
                 const float g1 = to_float<DT>(static_cast<uint16_t>(ag[e] >> 16));
                 sum = fmaf(g0, to_float<DT>(static_cast<uint16_t>(ao[e] & 0xFFFFu)), sum);
                 sum = fmaf(g1, to_float<DT>(static_cast<uint16_t>(ao[e] >> 16)), sum);
-                if (DT == 0 && counts)
-                    top = fmaxf(top, fmaxf(fabsf(g0), fabsf(g1)));
+                if constexpr (DT == 0)
+                    norm = fmaf(g0, g0, fmaf(g1, g1, norm));
             }
         }
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1)
+        for (int off = 4; off > 0; off >>= 1) {
             sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if constexpr (DT == 0)
+                norm += __shfl_xor_sync(0xffffffffu, norm, off);
+        }
         if (sub == 0) {
+            if (DT == 0 && l[k] != -INFINITY && norm < INFINITY)  // queries that see nothing have no part in it
+                top = fmaxf(top, norm);
             float *rows = p.rows + (static_cast<int64_t>(bh) * p.nqb + qb) * 2 * kBwdCols + (threadIdx.x >> 3) + 32 * k;
             rows[0] = l[k] == -INFINITY ? -INFINITY : kPShift<DT> - l[k] * 1.4426950408889634f;
             rows[kBwdCols] = l[k] == -INFINITY ? 0.0f : -sum;
         }
     }
-    if constexpr (DT == 0) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        if ((threadIdx.x & 31) == 0)
-            atomicMax(p.amax, __float_as_uint(top));  // non-negative floats order like their bits
-    }
+    if constexpr (DT == 0)
+        raise_norm(p.norms, top);
 }
 
 template <int D_>
@@ -620,12 +665,13 @@ __global__ void __launch_bounds__(640, 1)
         // fp16: dX times x_mul over P's factor; x_undo takes dX's factor out again
         float x_mul = 1.0f, x_undo = 1.0f;
         if constexpr (DT == 0) {
-            const unsigned bits = __ldg(p.amax);
-            // 2^-e with 2^(e-1) <= largest |dO| < 2^e, kept where both 2^e and 2^-e are normal; 1 for 0, inf, NaN
-            int e = static_cast<int>(bits >> 23) - 126;
-            e = bits == 0 || bits >= 0x7F800000u ? 0 : min(max(e, -100), 100);
-            x_mul = exp2f(static_cast<float>(-e) + 4.0f - kPShift<DT>);
-            x_undo = exp2f(static_cast<float>(e) - 4.0f);
+            // the least e with 4 |dO|^2 |V|^2 < 2^(2 e), so that |dX| < 2^e; 0 where one of them is 0.  The norms of
+            // finite fp16 rows keep e between -47 and 42.
+            const unsigned bits = __float_as_uint(4.0f * __ldg(p.norms) * __ldg(p.norms + 1));
+            const int e = bits == 0 ? 0 : (static_cast<int>(bits >> 23) - 126 + 1) >> 1;
+            auto power = [](int n) { return __uint_as_float(static_cast<unsigned>(n + 127) << 23); };
+            x_mul = power(15 - e - static_cast<int>(kPShift<DT>));
+            x_undo = power(e - 15);
         }
         constexpr float p_undo = DT == 0 ? 1.0f / 1024.0f : 1.0f;
         uint4 *out_buf = reinterpret_cast<uint4 *>(smem + CF::OFF_OUT + (warp - 4) * 1024);

@@ -90,6 +90,20 @@ struct MaskParams {
 // Document offsets kept in shared memory while rows look theirs up
 constexpr int kDocsInSmem = 512;
 
+// The last document that begins at or before `pos` (empty documents end where they begin), or -1
+__device__ __forceinline__ int last_document(const MaskParams &m, const int32_t *docs, int pos)
+{
+    int a = 0, n = m.num_docs;
+    while (a < n) {
+        const int mid = (a + n) >> 1;
+        if (docs[mid] <= pos)
+            a = mid + 1;
+        else
+            n = mid;
+    }
+    return a - 1;
+}
+
 // The keys query row `i` of batch entry `b` sees, [x, y); empty for rows past
 // the queries or outside every document.  `docs` are the batch entry's
 // offsets (shared or global memory).  Offsets out of order or out of range
@@ -101,16 +115,7 @@ __device__ __forceinline__ int2 visible_keys(const MaskParams &m, const int32_t 
     const int pos = m.q_offset + i;
     int lo = 0, hi = m.Sk, d = 0;
     if (m.doc_offsets) {
-        // the last document that begins at or before pos (empty documents end where they begin)
-        int a = 0, n = m.num_docs;
-        while (a < n) {
-            const int mid = (a + n) >> 1;
-            if (docs[mid] <= pos)
-                a = mid + 1;
-            else
-                n = mid;
-        }
-        d = a - 1;
+        d = last_document(m, docs, pos);
         if (d < 0)
             return make_int2(0, 0);
         lo = docs[d];
@@ -130,6 +135,27 @@ __device__ __forceinline__ int2 visible_keys(const MaskParams &m, const int32_t 
     lo = max(lo, 0);
     hi = min(hi, m.Sk);
     return hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// Whether some query sees key `j` of batch entry `b`: its document (the sequence) has queries and, causal, one of
+// them stands at or behind the key, or the prefix reaches it.
+__device__ __forceinline__ bool key_is_seen(const MaskParams &m, const int32_t *docs, int b, int j)
+{
+    if (j >= m.Sk)
+        return false;
+    int first = m.q_offset, end = m.q_offset + m.Sq, lo = 0, d = 0;  // the queries' places
+    if (m.doc_offsets) {
+        d = last_document(m, docs, j);
+        if (d < 0 || j >= docs[d + 1])
+            return false;
+        lo = docs[d];
+        first = max(first, lo);
+        end = min(end, docs[d + 1]);
+    }
+    if (end <= first)
+        return false;
+    return !m.causal || j < end ||
+           (m.prefix && j < static_cast<int64_t>(lo) + m.prefix[static_cast<int64_t>(b) * max(m.num_docs, 1) + d]);
 }
 
 struct ScoreParams {

@@ -1,5 +1,6 @@
 """The attention operators where their ranges end, on the GPU against the plain 64-bit
 forms."""
+import math
 import os
 import sys
 
@@ -45,6 +46,73 @@ def test_documents_that_begin_past_the_keys(name, dt):
 
 
 # ------------------------------------------------------------------ fp16 gradients
+def held_gradients(p, do):
+    """The gradients and bounds of `Plain`, with the step of what fp16 holds dX in.
+
+    |dX| <= |dP - delta| <= 2 m, m = max |dO_i| max |V_j| (2-norms; O is a mean of V rows), and dX is held
+    times 2^15 over the power of two above 2 m at least: half of fp16's smallest step 2^-24 is then at most
+    2^-25 2^-15 4 m = 2^-38 m of dX."""
+    want, (bq, bk, bv) = p.gradients(do)
+    m = do.double().norm(dim=-1).amax() * p.v.detach().norm(dim=-1).amax()
+    step = 2.0 ** -38 * m * (1 + 2.0 ** -6) * p.scale * p.see[:, None].double()
+    bq = bq + torch.einsum("bhij,bhjd->bhid", step.expand(-1, do.shape[1], -1, -1), p.kk.detach().abs())
+    by_head = torch.einsum("bhij,bhid->bhjd", step.expand(-1, do.shape[1], -1, -1), p.q.detach().abs())
+    bk = bk + by_head.view(by_head.shape[0], -1, p.G, *by_head.shape[2:]).sum(2)
+    return want, (bq, bk, bv)
+
+
+LARGE = {
+    # two values of opposite sign share the weight, gradients of a sum: dX is about 12, the sums behind it of order 1
+    "a_sum": dict(shape=(1, 1, 1, 130, 2, 128), v=100.0, do=1.9e-3, even=True),
+    "a_sum_64": dict(shape=(1, 2, 1, 130, 300, 64), v=100.0, do=1.9e-3, even=True, causal=True),
+    "values": dict(shape=(1, 4, 2, 333, 300, 128), v=300.0, do=1e-3, causal=True),
+    "small_values": dict(shape=(1, 2, 1, 200, 260, 64), v=1e-3, do=1.0, causal=True),
+    "largest_values": dict(shape=(1, 2, 2, 150, 270, 64), v=15000.0, do=1e-5),
+    "capped": dict(shape=(2, 2, 1, 140, 140, 128), v=500.0, do=1e-3, causal=True, cap=10.0, q_scale=3.0),
+    "pieces": dict(shape=(1, 3, 1, 900, 900, 64), v=400.0, do=1e-3, causal=True, bias=True),
+}
+
+
+@pytest.mark.parametrize("name", list(LARGE))
+def test_fp16_gradients_over_large_values(name):
+    """Values far from 1: dX would leave fp16's range where the gradients do not."""
+    import tensor_core_gemm_tl_b200 as tg
+    c = LARGE[name]
+    q, k, v, do, how, p = problem(c, "fp16", seed=3)
+    if c.get("even"):
+        sign = 1 - 2 * (torch.arange(v.shape[2], device="cuda") % 2)
+        v = (c["v"] * sign[:, None].half()).expand_as(v).contiguous()
+        do = torch.full_like(do, c["do"])
+    else:
+        v, do = (v.clamp(-4, 4) * c["v"]).half(), (do * c["do"]).half()
+    slopes = how.get("slopes")
+    at = [torch.arange(n, device="cuda").expand(q.shape[0], n) for n in (q.shape[2], k.shape[2])]
+    p = Plain(q, k, v, p.see.cpu(), p.scale, p.cap, slopes, *at)
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = tg.attention_ex(q, k, v, lse=lse, **how)
+    grads = tg.attention_backward(do, q, k, v, out, lse, **how)
+    want, bounds = held_gradients(p, do)
+    assert all(w.abs().max() < 60000 for w in want)  # the gradients themselves fit
+    for n, g, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(n, g, w, b)
+
+
+def test_an_infinite_gradient_spoils_its_own_query():
+    """fp16 dout with an infinite and a NaN row: dq of every other query as if those rows were 0."""
+    import tensor_core_gemm_tl_b200 as tg
+    q, k, v, do, how, _ = problem(dict(shape=(1, 2, 1, 300, 300, 64), causal=True), "fp16", seed=2)
+    do = (do * 40).half()
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = tg.attention_ex(q, k, v, lse=lse, **how)
+    do[0, 1, 50:52] = 0
+    want = tg.attention_backward(do, q, k, v, out, lse, **how)[0]
+    do[0, 1, 50, 3], do[0, 1, 51, 60] = math.inf, math.nan
+    dq = tg.attention_backward(do, q, k, v, out, lse, **how)[0]
+    bad = ~torch.isfinite(dq).all(-1)
+    assert bad[0, 1, 50:52].all() and int(bad.sum()) == 2
+    assert torch.equal(dq[~bad], want[~bad])
+
+
 @pytest.mark.parametrize("how", [dict(docs=[[20, 150, 260]]), dict(docs=[[20, 150, 260]], causal=True),
                                  dict(docs=[[20, 21, 150, 260]], causal=True, prefix=[[0, 30, 200]]),
                                  dict(causal=True, offset=5, queries=140)])
