@@ -492,8 +492,9 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str | No
     factor^(rot_dim / (rot_dim - 2)), so that only the slow pairs stretch;
     "yarn" divides the pairs that turn fewer than ``beta_slow`` times over
     ``original_length`` positions, keeps those that turn more than ``beta_fast``
-    times, blends linearly in the pair's index in between, and returns the scale
-    0.1 ln(factor) + 1 (else the scale is 1)."""
+    times, blends linearly in the pair's index in between (from the whole indices
+    around those two, 0 at least and rot_dim - 1 at most, which may lie behind the
+    last pair), and returns the scale 0.1 ln(factor) + 1 (else the scale is 1)."""
     import math
 
     import torch
@@ -509,16 +510,17 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str | No
     if scaling == "linear":
         freq = [f / factor for f in freq]
     elif scaling == "yarn":
-        if original_length < 1 or not beta_fast > beta_slow > 0:
-            raise ValueError("yarn needs original_length and beta_fast > beta_slow > 0")
+        if original_length < 1 or not beta_fast > beta_slow > 0 or not base > 1:
+            raise ValueError("yarn needs original_length, beta_fast > beta_slow > 0 and a base above 1")
 
         def index(turns):  # the pair that turns so many times over original_length positions
             return rot_dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
 
-        lo = min(max(math.floor(index(beta_fast)), 0), half - 1)
-        hi = min(max(math.ceil(index(beta_slow)), 0), half - 1)
+        # the upper end may lie behind the last pair: then no pair is divided whole
+        lo = max(math.floor(index(beta_fast)), 0)
+        hi = min(math.ceil(index(beta_slow)), rot_dim - 1)
         for i in range(half):
-            blend = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)  # 0: kept, 1: divided
+            blend = 1.0 if i >= hi else max((i - lo) / (hi - lo), 0.0) if hi > lo else 0.0  # 0: kept, 1: divided
             freq[i] = freq[i] * (1.0 - blend) + freq[i] / factor * blend
         scale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):
