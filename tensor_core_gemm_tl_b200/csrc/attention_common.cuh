@@ -203,14 +203,17 @@ __device__ __forceinline__ void odd_polynomial(uint32_t *v, float arg, const flo
 // leaves 1e-5.  (The polynomials' coefficients hold arg^13 at most: they are left to
 // arg <= 64, far above any cap in use, and where arg^13 underflows tanh x = x,
 // which the vanishing coefficients give.)
+//
+// The forms differ by 2^-22, so lanes whose scores belong to no row pass `counts`
+// false and have no say in the choice: what they hold must not reach the others.
 template <int N>
-__device__ __forceinline__ void tanh_scores(uint32_t *v, float arg)
+__device__ __forceinline__ void tanh_scores(uint32_t *v, float arg, bool counts = true)
 {
     float top = 0.0f;
 #pragma unroll
     for (int e = 0; e < N; e += 2)
         top = fmax3(top, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
-    top = arg <= 64.0f ? top * arg : INFINITY;
+    top = !counts ? 0.0f : arg <= 64.0f ? top * arg : INFINITY;
     if (__all_sync(0xffffffffu, top <= 0.5f)) {
         const float c[5] = {0.9999999869f, -0.3333306939f, 0.1332477932f, -0.05298607529f, 0.01713500663f};
         odd_polynomial<N>(v, arg, c);

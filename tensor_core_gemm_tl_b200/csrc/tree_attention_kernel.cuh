@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(384, 1)
                         if (cap) {
                             if (!context_only)
                                 hide(q, 0.0f);
-                            tanh_scores<32>(sv, p.score.cap_arg);
+                            tanh_scores<32>(sv, p.score.cap_arg, valid);
                         }
                         if constexpr (BIAS)
                             biased(q);

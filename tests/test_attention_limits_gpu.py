@@ -136,3 +136,56 @@ def test_fp16_gradients_beside_rows_that_do_not_count(how):
     grads = tg.attention_backward(do, q, k, v, out, lse, **how)
     for n, g, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
         close(n, g, w, b)
+
+
+# ------------------------------------------------------------------ tree attention
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bias", [False, True])
+def test_capped_tokens_do_not_depend_on_how_many_heads_share(D, dt, bias):
+    """One token of two query heads, and the same two among 32: bit for bit the same, whatever the tile's rows behind
+    them hold (the first leaves 30 lanes of a warp without a row; keys far larger than the queries take those lanes'
+    products past the cap, the rows' own lie well inside it)."""
+    import tensor_core_gemm_tl_b200 as tg
+    g = torch.Generator(device="cuda").manual_seed(D)
+    for contexts in ([5, 300, 1000], [4000]):
+        B, page = len(contexts), 16
+        per = (max(contexts) + page) // page
+        kc, vc = (torch.randn((B * per, page, 1, D), generator=g, device="cuda") * f for f in (10.0, 1.0))
+        kc, vc = kc.to(dt), vc.to(dt)
+        table = torch.randperm(B * per, generator=g, device="cuda").to(torch.int32).view(B, per)
+        context = torch.tensor(contexts, dtype=torch.int32, device="cuda")
+        two = (torch.randn((B, 2, 1, D), generator=g, device="cuda") * 0.2).to(dt)
+        many = two.repeat(1, 16, 1, 1)
+        slopes = torch.tensor([0.01, 0.002], device="cuda")
+        res = []
+        for q in (two, many, two):
+            lse = torch.empty(q.shape[:3], device="cuda")
+            how = dict(score_cap=50.0, slopes=slopes.repeat(q.shape[1] // 2) if bias else None)
+            res.append((tg.tree_attention(q, kc, vc, table, context, lse=lse, **how), lse))
+        assert tg.check_device() == 0
+        for out, lse in res[1:]:
+            for n in range(0, out.shape[1], 2):
+                assert torch.equal(out[:, n:n + 2], res[0][0]) and torch.equal(lse[:, n:n + 2], res[0][1])
+
+
+def test_capped_trees_repeat_bit_for_bit():
+    """Drafted trees with a cap, some rows of a warp without a token, run again and again among other calls."""
+    import tensor_core_gemm_tl_b200 as tg
+    g = torch.Generator(device="cuda").manual_seed(1)
+    B, T, H, Hk, D, page, keys = 8, 31, 16, 4, 128, 32, 4096
+    per = (keys + T + page - 1) // page
+    kc, vc = (torch.randn((B * per, page, Hk, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.randperm(B * per, generator=g, device="cuda").to(torch.int32).view(B, per)
+    context = torch.randint(keys // 4, keys + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(T // 2, T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    parents = (torch.rand((B, T), generator=g, device="cuda") * (torch.arange(T, device="cuda") + 1)).to(torch.int32) - 1
+    q = (torch.randn((B, T, H, D), generator=g, device="cuda") * 4).bfloat16().transpose(1, 2)
+    first = None
+    for n in range(12):
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+        tg.tree_attention(q, kc, vc, table, context, parents, tree_lens=lens, score_cap=30.0, out=out, lse=lse)
+        first = (out, lse) if first is None else first
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), n
+        tg.tree_attention((q * (n % 3)).contiguous(), vc, kc, table, context, score_cap=3.0)  # other bytes in shared memory
+    assert tg.check_device() == 0
