@@ -185,7 +185,11 @@ def _new_like(torch, t, stream):
     else:
         with torch.cuda.stream(stream):
             y = torch.empty_like(t)
-    s0, s1, s2, _ = y.stride()
+    s0, s1, s2, s3 = y.stride()
+    if s3 != 1:  # `t`'s rows overlap a value apart, which leaves open what is innermost: as of a contiguous tensor
+        n = y.shape
+        s0, s1, s2 = n[1] * n[2] * n[3], n[2] * n[3], n[3]
+        y = y.as_strided(n, (s0, s1, s2, 1))
     return y, (s0, s1, s2)
 
 

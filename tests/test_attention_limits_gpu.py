@@ -189,3 +189,18 @@ def test_capped_trees_repeat_bit_for_bit():
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), n
         tg.tree_attention((q * (n % 3)).contiguous(), vc, kc, table, context, score_cap=3.0)  # other bytes in shared memory
     assert tg.check_device() == 0
+
+
+# ------------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_of_windows_that_overlap(interleaved):
+    """Positive strides of any size, rows that lie inside one another among them: the output is laid out on its own."""
+    import tensor_core_gemm_tl_b200 as tg
+    x = torch.randn(4096, device="cuda", generator=torch.Generator("cuda").manual_seed(6)).bfloat16()
+    inv_freq, _ = tg.rotary_frequencies(8, device="cuda")
+    for shape, strides in (((1, 2, 4, 8), (100, 32, 1, 1)), ((2, 3, 4, 8), (1, 1, 1, 1)), ((2, 2, 5, 8), (40, 3, 8, 1))):
+        q = torch.as_strided(x, shape, strides)
+        pos = torch.arange(shape[2], device="cuda")
+        out, _ = tg.rotary(q, None, pos, inv_freq, interleaved=interleaved)
+        want, _ = tg.rotary(q.contiguous(), None, pos, inv_freq, interleaved=interleaved)
+        assert torch.equal(out, want)
