@@ -226,10 +226,14 @@ def _flat(name, t, device, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+# The smallest and largest positive float32: what the options hold scales and caps in
+_F32_MIN, _F32_MAX = 2.0 ** -149, (2.0 - 2.0 ** -23) * 2.0 ** 127
+
+
 def _score_arguments(scale, score_cap, slopes, heads, device):
     """The softmax scale, cap and bias slopes, checked; returns the slopes' pointer."""
-    if not 0.0 <= scale < float("inf") or not 0.0 <= score_cap < float("inf"):
-        raise ValueError("scale and score_cap must be finite and not negative")
+    if (scale != 0.0 and not _F32_MIN <= scale <= _F32_MAX) or (score_cap != 0.0 and not _F32_MIN <= score_cap <= _F32_MAX):
+        raise ValueError("scale and score_cap must be 0 or positive numbers that float32 holds")
     if slopes is None:
         return 0
     import torch
@@ -465,8 +469,8 @@ def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float
     _flat("inv_freq", inv_freq, dev, torch.float32, (half,))
     if not 2 <= 2 * half <= D:
         raise ValueError(f"inv_freq has {half} frequencies for heads of {D} values")
-    if not 0.0 < scale < float("inf"):
-        raise ValueError("scale must be positive and finite")
+    if not _F32_MIN <= scale <= _F32_MAX:
+        raise ValueError("scale must be a positive number that float32 holds")
     # every given tensor is checked before anything is allocated
     if out_q is not None:
         soq = _rotary_rows("out_q", out_q, dev, dtype, q.shape)
