@@ -245,13 +245,14 @@ TL_API tl_status tl_attention_fwd(const void *Q, const void *K, const void *V, v
  * head_dim is 64 or 128; seq_q, seq_k and q_offset + seq_q at most 2^31 - 257.
  * Pointers are 16-byte aligned; strides are positive multiples of 8 elements,
  * the last dimension is contiguous.  Rows of K and V that no query sees must
- * still be finite (a weight of 0 times NaN is NaN).  With a cap, raw scores
- * have to stay below 1e18; a cap is above 1e-30, softmax_scale / score_cap below
- * 1e38.  Sums and softmax statistics are fp32; the weights
- * are rounded to `dtype` before the product with V and O is rounded once.
- * Where the batch has few rows the keys are split over the SMs and joined from
- * a stream-ordered temporary, by a rule on the sizes: results repeat bit for
- * bit on the same kind of device.  Asynchronous on `stream`; bounded waits
+ * still be finite (a weight of 0 times NaN is NaN).  Scale and cap are below
+ * 1e38; with a cap, raw scores have to stay below 1e18, the cap is above 1e-30
+ * and softmax_scale / score_cap between 1e-37 and 1e38.  Sums and softmax
+ * statistics are fp32; the weights are rounded to `dtype` before the product
+ * with V and O is rounded once.  Where the batch has few rows the keys are split
+ * over the SMs and joined from a stream-ordered temporary, by a rule on the
+ * sizes: results repeat bit for bit on the same kind of device.  Asynchronous on
+ * `stream`; bounded waits
  * report through tl_check_device; O must not overlap an input.
  */
 typedef struct {

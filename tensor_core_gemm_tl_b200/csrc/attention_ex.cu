@@ -20,7 +20,7 @@ tl_status attention_call(const void *Q, const void *K, const void *V, const void
     const int64_t kv = o.kv_heads == 0 ? heads : o.kv_heads;
     if (kv < 1 || heads % kv != 0)
         return TL_ERR_INVALID_ARG;
-    if (!score_values_ok(o.softmax_scale, o.score_cap))
+    if (!score_values_ok(o.softmax_scale, o.score_cap, head_dim))
         return TL_ERR_INVALID_ARG;
     if ((o.causal != 0 && o.causal != 1) || o.q_offset < 0 || o.num_docs < 0)
         return TL_ERR_INVALID_ARG;
@@ -56,7 +56,7 @@ tl_status attention_call(const void *Q, const void *K, const void *V, const void
     c->seq_k = seq_k;
     c->head_dim = head_dim;
     c->dtype = dtype;
-    c->scale = o.softmax_scale > 0.0f ? o.softmax_scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+    c->scale = softmax_scale(o.softmax_scale, head_dim);
     c->cap = o.score_cap;
     c->slopes = o.slopes;
     c->mask = MaskParams{};

@@ -118,11 +118,19 @@ tl_status ready_kernel(DeviceState *d, Fn fn, int smem, int launch_regs)
     return raise_smem_limit(d, f, smem);
 }
 
-inline bool score_values_ok(float scale, float cap)
+// The scale of a call: the given one, or 1 / sqrt(head_dim) for 0
+inline float softmax_scale(float given, int64_t head_dim)
 {
-    // scale / cap is held in fp32 (times 2 log2 e)
-    return scale >= 0.0f && scale < INFINITY && cap >= 0.0f && cap < INFINITY && (cap == 0.0f || scale / cap < 1e38f) &&
-           (cap == 0.0f || cap > 1e-30f);
+    return given > 0.0f ? given : 1.0f / sqrtf(static_cast<float>(head_dim));
+}
+
+inline bool score_values_ok(float scale, float cap, int64_t head_dim)
+{
+    // both are held in fp32 times log2 e, and so is scale / cap, times 2 log2 e
+    if (!(scale >= 0.0f && scale < 1e38f && cap >= 0.0f && cap < 1e38f))
+        return false;
+    const float ratio = softmax_scale(scale, head_dim) / cap;
+    return cap == 0.0f || (cap > 1e-30f && ratio > 1e-37f && ratio < 1e38f);
 }
 
 inline ScoreParams score_params(float scale, float cap, const float *slopes)

@@ -58,7 +58,7 @@ tl_status tree_attention_impl(const void *Q, const void *K, const void *V, const
     if (batch < 1 || heads < 1 || kv_heads < 1 || tokens < 1 || num_pages < 1 || page_size < 1 || max_pages < 1)
         return TL_ERR_INVALID_ARG;
     if (heads % kv_heads != 0 || (dtype != TL_F16 && dtype != TL_BF16) ||
-        !score_values_ok(o.softmax_scale, o.score_cap) || o.table_stride < 0 ||
+        !score_values_ok(o.softmax_scale, o.score_cap, head_dim) || o.table_stride < 0 ||
         (o.table_stride != 0 && batch > 1 && o.table_stride < max_pages))
         return TL_ERR_INVALID_ARG;
     const int64_t group = heads / kv_heads;
@@ -92,7 +92,7 @@ tl_status tree_attention_impl(const void *Q, const void *K, const void *V, const
     if (d->cc_major != 10)
         return TL_ERR_UNSUPPORTED;
     const TreeEntry &e = head_dim == 64 ? kTree64 : kTree128;
-    const float scale = o.softmax_scale > 0.0f ? o.softmax_scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+    const float scale = softmax_scale(o.softmax_scale, head_dim);
     TreeFn fn = e.fn[dtype][o.score_cap > 0.0f][o.slopes != nullptr];
     if ((st = raise_smem_limit(d, reinterpret_cast<const void *>(fn), e.smem_max)) != TL_OK)
         return st;

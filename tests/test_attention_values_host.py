@@ -12,7 +12,7 @@ sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 import torch  # noqa: E402
 
 import tensor_core_gemm_tl_b200 as tg  # noqa: E402
-from test_attention_ops_host import Fake, I32, backward, forward  # noqa: E402
+from test_attention_ops_host import NO_GPU, Fake, I32, backward, call_attention, call_tree, forward  # noqa: E402
 
 OUT = (1e-46, 1e-300, 1e39, 1e300, math.inf, math.nan, -1e-46)
 SMALLEST, LARGEST = 2.0 ** -149, (2 - 2.0 ** -23) * 2.0 ** 127
@@ -76,3 +76,22 @@ def test_what_float32_holds_arrives(value, launches):
         assert o[at] == as_float32 > 0
     turned(value)
     assert tg.ROTARY_OPTIONS.unpack(launches.pop())[2] == as_float32 > 0
+
+
+# softmax_scale, score_cap: their product with log2 e, or their quotient, leaves fp32's normal range
+PAST_FP32 = [(2.4e38, 0.0), (1e38, 0.0), (0.0, 3e38), (1.0, 1.5e38), (1e-20, 1e30), (0.0, 9e37), (1e-38, 1.0)]
+
+
+@pytest.mark.parametrize("scale,cap", PAST_FP32)
+def test_the_library_refuses_scores_past_fp32(scale, cap):
+    o = dict(softmax_scale=scale, score_cap=cap)
+    for st in (call_attention({}, o, False), call_attention({}, o, True), call_tree({}, o)):
+        assert st == tg.Status.INVALID_ARG
+
+
+@NO_GPU
+@pytest.mark.parametrize("scale,cap", [(9e37, 0.0), (1e-38, 0.0), (0.0, 1e35), (1e-6, 1e-29), (1e30, 1e-7)])
+def test_scores_inside_fp32_reach_the_device(scale, cap):
+    o = dict(softmax_scale=scale, score_cap=cap)
+    for st in (call_attention({}, o, False), call_attention({}, o, True), call_tree({}, o)):
+        assert st == tg.Status.CUDA
