@@ -38,7 +38,7 @@ def sources():
 
 def inputs():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.inc"))
-                              + glob.glob(os.path.join(INCLUDE, "*.h")))
+                              + glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
 
 
 def stale(lib: str = LIB) -> bool:
@@ -49,22 +49,30 @@ def stale(lib: str = LIB) -> bool:
 
 
 def _compile(src: str, obj: str, force: bool, flags) -> None:
-    """One source to an object; kept when it is newer than everything the last
-    compile of it read (nvcc's own dependency list beside the object)."""
-    deps = obj + ".d"
-    if not force and os.path.exists(obj) and os.path.exists(deps):
+    """One source to an object; kept when the same command made it and it is newer
+    than everything that compile read (nvcc's own dependency list and the
+    command lie beside the object)."""
+    deps, made_by = obj + ".d", obj + ".cmd"
+    command = [NVCC, *flags, "-I", INCLUDE, "-I", CSRC, "-c", src]
+    if not force and all(os.path.exists(f) for f in (obj, deps, made_by)):
         with open(deps) as fh:
             read = fh.read().split(":", 1)[1].replace("\\\n", " ").split()
+        with open(made_by) as fh:
+            same = fh.read() == "\n".join(command)
         t = os.path.getmtime(obj)
-        if all(os.path.exists(f) and os.path.getmtime(f) <= t for f in read):
+        if same and all(os.path.exists(f) and os.path.getmtime(f) <= t for f in read):
             return
     tmp = obj + f".tmp{os.getpid()}"
-    subprocess.check_call([NVCC, *flags, "-MMD", "-MF", deps, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", tmp])
+    if os.path.exists(made_by):
+        os.remove(made_by)  # until the object is the new command's
+    subprocess.check_call([*command, "-MMD", "-MF", deps, "-o", tmp])
     os.replace(tmp, obj)
+    with open(made_by, "w") as fh:
+        fh.write("\n".join(command))
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, out: str = LIB, extra=()) -> str:
-    if not force and not stale(out):
+    if not force and not ptxas_verbose and not stale(out):
         return out
     objdir = os.path.join(ROOT, "build", os.path.basename(out))
     os.makedirs(objdir, exist_ok=True)
