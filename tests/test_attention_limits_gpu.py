@@ -12,8 +12,8 @@ torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
 
-from attention_plain import Plain, close  # noqa: E402
-from test_attention_ex_gpu import problem  # noqa: E402
+from attention_plain import Plain, close, rotate  # noqa: E402
+from test_attention_ex_gpu import CASES, problem  # noqa: E402
 
 # Documents that begin at or behind the last key: their queries see nothing, those before them in the same tile do
 PAST_THE_KEYS = {
@@ -191,7 +191,60 @@ def test_capped_trees_repeat_bit_for_bit():
     assert tg.check_device() == 0
 
 
+# ------------------------------------------------------------------ gradients against differences
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("name", ["prefix_documents", "capped", "biased"])
+def test_gradients_along_themselves_against_differences(name, dt):
+    """<gradient, d> against central differences of the 64-bit forward, d along the exact gradient, where nothing
+    cancels: the slope is many times what the roundings may add up to, so a gradient that is off shows."""
+    import tensor_core_gemm_tl_b200 as tg
+    q, k, v, do, how, p = problem(CASES[name], dt, seed=5)
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = tg.attention_ex(q, k, v, lse=lse, **how)
+    grads = tg.attention_backward(do, q, k, v, out, lse, **how)
+    want, bounds = p.gradients(do)
+    at = [torch.arange(n, device="cuda").expand(q.shape[0], n) for n in (q.shape[2], k.shape[2])]
+    see = p.see.cpu()
+    h = 1e-3
+    for n, (t, g, w, b) in enumerate(zip("qkv", grads, want, bounds)):
+        d = w / w.norm()
+        loss = []
+        for s in (h, -h):
+            x = [y.double() for y in (q, k, v)]
+            x[n] = x[n] + s * d
+            f = Plain(*x, see, p.scale, p.cap, how.get("slopes"), *at)
+            loss.append((f.out.detach() * do.double()).sum())
+        slope = (loss[0] - loss[1]) / (2 * h)
+        # the difference is off by h^2 / 6 of the third derivative along d: 2e-9 of the slope at most on such draws
+        # (h = 1e-2, 1e-3 and 1e-4 agree to that), 1e-6 of it holds that
+        slack = (b * d.abs()).sum() + 1e-6 * slope.abs()
+        assert slope > 20 * slack, t  # so neither 0 nor a gradient 5 % off passes
+        assert abs((g.double() * d).sum() - slope) <= slack, t
+
+
 # ------------------------------------------------------------------ rotary positions
+def rotary_bound(x, want):
+    """As in the rotary tests, for scale 1: one rounding, and fp32 before it."""
+    size = x.double().abs().amax(-1, keepdim=True)
+    return torch.finfo(x.dtype).eps / 2 * want.abs() * (1 + 2.0 ** -6) + size * 2.0 ** -20 + 1e-38
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_the_inverse_is_the_gradient_along_itself(interleaved):
+    """<rotate(d), g> = <d, inverse(g)> for d along the exact inverse, where nothing cancels."""
+    import tensor_core_gemm_tl_b200 as tg
+    g = torch.randn((1, 3, 200, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(4)).bfloat16()
+    inv_freq, _ = tg.rotary_frequencies(128, base=500000.0, device="cuda")
+    pos = torch.arange(200, device="cuda") + 70000
+    gx, _ = tg.rotary(g, None, pos, inv_freq, interleaved=interleaved, inverse=True)
+    want = rotate(g, pos[None], inv_freq, interleaved, inverse=True)
+    d = want / want.norm()
+    lhs, rhs = (rotate(d, pos[None], inv_freq, interleaved) * g.double()).sum(), (d * gx.double()).sum()
+    slack = (rotary_bound(g, want) * d.abs()).sum()
+    assert lhs > 100 * slack
+    assert abs(lhs - rhs) <= slack
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotary_of_windows_that_overlap(interleaved):
     """Positive strides of any size, rows that lie inside one another among them: the output is laid out on its own."""
