@@ -166,6 +166,10 @@ def attention(q, k, v, causal: bool = False, scale: float = 0.0, out=None, lse=N
     return out
 
 
+# None of the calls records anything for autograd: outputs carry no graph,
+# whatever the inputs ask for.  A training program calls the backward itself, from
+# a torch.autograd.Function or its own loop.
+#
 # The calls below run as often as a model has layers and tokens, so their checks
 # are written to cost little: each tensor's strides are read once, the option
 # structs are packed in one go, the device is only switched when it has to be.
@@ -310,8 +314,12 @@ def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap
     document (positions outside the first to the last offset see nothing);
     ``prefix`` (B, max(docs, 1)) int32 opens the first keys of each document (of
     the sequence) to causal queries.  Queries that see nothing give 0 and lse
-    -inf.  Returns out, shaped and by default laid out like q; fills ``lse``
-    (B, H, Sq) float32 if given (attention_backward needs it)."""
+    -inf.  Rows of k and v that no query sees -- a padded end, too -- must be
+    finite: a weight of 0 times NaN is NaN.  Returns out, shaped and by default
+    laid out like q; fills ``lse`` (B, H, Sq) float32 if given.
+
+    out carries no autograd graph; its gradients are attention_backward's, from
+    out and ``lse``."""
     import torch
     head, strides, dt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
     B, H, Sq, D = q.shape
@@ -337,7 +345,7 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: 
     ``lse`` and the gradient ``dout`` of out; the options are the forward's.
     dk and dv are summed over the heads that share them.  What no query sees, and
     queries that see nothing, do not count but must be finite.  Results repeat bit
-    for bit."""
+    for bit.  ``slopes`` are constants (a tensor that requires grad is refused)."""
     import torch
     head, strides, dt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
     B, H, Sq, D = q.shape
@@ -371,7 +379,8 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents=None,
     token, or -1; None: a chain).  ``tree_lens`` (B,) int32 gives shorter trees:
     out and lse of later tokens stay as they were.  Scale, cap and bias as in
     attention_ex, a new token standing at context_lens[b] plus its depth.
-    Returns out, like q; fills ``lse`` (B, H, T) float32 if given."""
+    Returns out, like q, without an autograd graph; fills ``lse`` (B, H, T) float32
+    if given."""
     import torch
     if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError(f"shapes q{tuple(q.shape)} k_cache{tuple(k_cache.shape)} v_cache{tuple(v_cache.shape)} "
@@ -444,7 +453,8 @@ def rotary(q, k, positions, inv_freq, *, interleaved: bool = False, scale: float
     2 * len(inv_freq) values of a head are rotated in pairs (i, i + half), or
     (2 i, 2 i + 1) when ``interleaved``, and multiplied by ``scale``; the rest is
     copied.  ``inverse`` turns back: it is the backward of the same call, on the
-    gradients.  ``out_q`` may be q and ``out_k`` may be k."""
+    gradients (the outputs carry no autograd graph).  ``out_q`` may be q and
+    ``out_k`` may be k."""
     import torch
     if q.dim() != 4 or not q.is_cuda:
         raise ValueError("q must be a 4-D CUDA tensor")

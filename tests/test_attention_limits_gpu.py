@@ -257,3 +257,25 @@ def test_rotary_of_windows_that_overlap(interleaved):
         out, _ = tg.rotary(q, None, pos, inv_freq, interleaved=interleaved)
         want, _ = tg.rotary(q.contiguous(), None, pos, inv_freq, interleaved=interleaved)
         assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ autograd
+def test_outputs_carry_no_graph():
+    """Inputs that require grad give the values they give otherwise, and outputs without a graph."""
+    import tensor_core_gemm_tl_b200 as tg
+    q, k, v, do, how, _ = problem(dict(shape=(1, 4, 2, 50, 50, 64), causal=True), "bf16", seed=1)
+    inv_freq, _ = tg.rotary_frequencies(64, device="cuda")
+    pos, table = torch.arange(50, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    context = torch.full((1,), 40, dtype=torch.int32, device="cuda")
+
+    def run(q, k, v):
+        lse = torch.empty(q.shape[:3], device="cuda")
+        out = tg.attention_ex(q, k, v, lse=lse, **how)
+        kc, vc = (t[0, :, :48].transpose(0, 1)[None] for t in (k, v))
+        return [out, lse, *tg.attention_backward(do, q, k, v, out, lse, **how), *tg.rotary(q, k, pos, inv_freq),
+                tg.tree_attention(q[:, :, :3], kc, vc, table, context)]
+
+    want = run(q, k, v)
+    got = run(*(t.requires_grad_() for t in (q, k, v)))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b) and not a.requires_grad
