@@ -461,7 +461,7 @@ TL_API tl_status tl_gemm_ex(const void *A, const void *B, const void *bias, void
  * accumulator, bit 3 epilogue warps, bit 4 final drain, bit 5 a part of a
  * split tile that could not record its arrival, bit 6 the row softmax waiting
  * for a row's copy into shared memory, bit 7 -- in the checked build
- * libtlgemm_checked.so only -- an index invariant of the GEMM kernel failed).
+ * libtlgemm_checked.so only -- an index invariant of a kernel failed).
  */
 TL_API tl_status tl_check_device(tl_stream stream, uint32_t *detail);
 

@@ -1,7 +1,7 @@
 """Build libtlgemm.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc,
-and its checked twin libtlgemm_checked.so (-DTL_CHECKED: the GEMM kernel tests
-its index invariants at run time and reports a violation in the device error
-word; used by the tests, never by the product path).
+and its checked twin libtlgemm_checked.so (-DTL_CHECKED: the kernels test their
+index invariants at run time and report a violation in the device error word;
+used by the tests, never by the product path).
 
     python tensor_core_gemm_tl_b200/build.py [--force] [--verbose-ptxas] [--checked]
 

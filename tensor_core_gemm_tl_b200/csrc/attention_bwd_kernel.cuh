@@ -468,6 +468,13 @@ __global__ void __launch_bounds__(640, 1)
                     pc = make_int4(n0, min(p.chunk, all - n0), all > p.chunk ? item : -1, 0);
                     if (p.pieces && s == 0 && lane == 0)
                         p.pieces[i] = (all + p.chunk - 1) / p.chunk;
+                    // checked build: heads, tiles, blocks and the place of partial sums
+                    const int limit = DKV ? p.nqb : (p.mask.Sk + CF::BN - 1) / CF::BN;
+                    if (!check_ok(tile >= 0 && tile < p.tiles && bh < BH && (blocks == 0 || (first >= 0 && end <= limit)) &&
+                                  pc.y >= 0 && n0 + pc.y <= all && s < p.splits && all <= static_cast<int64_t>(p.splits) * p.chunk)) {
+                        tl = make_int4(-1, 0, 0, 0);
+                        break;
+                    }
                     if (!DKV) {
                         tl.z += n0;
                         tl.w = pc.y;
@@ -986,7 +993,7 @@ __global__ void __launch_bounds__(256) attention_bwd_join_kernel(const AttnBwdJo
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int item = static_cast<int>(blockIdx.x >> 2);
     const int pieces = p.pieces[item];
-    if (pieces <= 1)
+    if (pieces <= 1 || !check_ok(pieces <= p.splits && item < p.tiles * p.BH))
         return;
     const int2 at = bwd_tile<DKV>(item, p.tiles, p.BH, p.mask.causal);
     const int r = 32 * static_cast<int>(blockIdx.x & 3) + lane, row = at.x * 128 + r;

@@ -298,8 +298,15 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
                         clip(x.z, x.w);
                         clip(y.x, y.y);
                     }
-                    *out = unpack(x, y);
-                    index = 0;
+                    // checked build: heads, tiles, steps and the place of partial sums
+                    const int steps = (p.mask.Sk + CF::BS - 1) / CF::BS;
+                    if (check_ok(x.x >= 0 && x.x < p.num_pairs && x.y >= 0 && x.y < BH && x.z >= 0 && x.w <= steps &&
+                                 y.x >= 0 && y.y <= steps && y.z < p.num_pairs * BH * p.splits)) {
+                        *out = unpack(x, y);
+                        index = 0;
+                    } else {
+                        x.x = index = -1;
+                    }
                 }
                 if (lane == 0) {
                     item_slots[2 * (t & 1)] = x;
@@ -810,6 +817,8 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnJoinParam
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bx = static_cast<int>(blockIdx.x);
     const int quarter = bx & 3, tile = (bx >> 2) & 1, item = bx >> 3;
+    if (!check_ok(item < p.num_pairs * p.BH))
+        return;
     // the item's pair and head, as the forward numbers them
     const int pair = p.causal ? p.num_pairs - 1 - item / p.BH : item % p.num_pairs;
     const int bh = p.causal ? item % p.BH : item / p.num_pairs;

@@ -88,11 +88,11 @@ __global__ void __launch_bounds__(256, 4) rotary_kernel(const RotaryParams p)
 
     for (int item0 = 0; item0 < items; item0 += 32) {
         const int item = item0 + lane - sub * lanes;
-        const bool mine = sub < warp_rows && item < items;
         const bool turns = item < turned;
         // value offsets of the one or two words
         const int at = turns ? (!VEC && p.interleaved ? 2 * item : W * item) : p.rot + (item - turned) * W;
         const int second = !turns || (VEC && p.interleaved) ? 0 : p.interleaved ? at + 1 : at + n;
+        const bool mine = sub < warp_rows && item < items && check_ok(at + W <= p.D && second + W <= p.D);
         uint4 va[AHEAD], vb[AHEAD];
         auto fetch = [&](int h, uint4 &a, uint4 &c) {
             if (!mine || h >= heads)

@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(384, 1)
                 // this lane's box of block j: its page and the row in it
                 auto page_of = [&](int j) {
                     const int k = j * CF::BN + lane * p.box_rows;
-                    return lane < boxes && k < rq.keys ? table[k / p.page_size] : -1;
+                    return lane < boxes && k < rq.keys && check_ok(k >= 0 && k < p.capacity && s.b < p.B)
+                               ? table[k / p.page_size] : -1;
                 };
                 int page = page_of(s.first);
                 const int qi = seg & 1;
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int a = 0; a < CF::D_ATOMS; ++a) {
                         uint4 *dst = reinterpret_cast<uint4 *>(smem + off_v + st * CF::TILE_BYTES + a * CF::ATOM_BYTES);
-                        for (int i = from * 8 + t; i < CF::BN * 8; i += 64)
+                        for (int i = from * 8 + t; i < CF::BN * 8 && check_ok(i >= 0 && st < KS); i += 64)
                             dst[i] = zero;
                     }
                     fence_proxy_async_smem();
@@ -516,7 +517,8 @@ __global__ void __launch_bounds__(384, 1)
             const TreeRequest rq = tree_request(p, s);
             const int hk = s.unit / p.row_tiles, rt = s.unit - hk * p.row_tiles;
             const int tok = rt * p.tile_tokens + r_token;
-            const bool valid = r_token < p.tile_tokens && tok < rq.tokens;
+            const bool valid = r_token < p.tile_tokens && tok < rq.tokens &&
+                               check_ok(tok < p.T && s.b < p.B && hk * p.group + r_head < p.H);
             const bool active = __any_sync(0xffffffffu, valid);  // warps without a row only keep the barriers going
             const int head = hk * p.group + r_head;
             const int buf = seg & 1;
@@ -562,6 +564,9 @@ __global__ void __launch_bounds__(384, 1)
                     };
                     // with a bias: the scores in log2 units, less slope2 times the distance
                     auto biased = [&](int q) {
+                        if (!context_only && !check_ok(key0 + 32 * q - rq.context >= -CF::PLACE0 &&
+                                                       key0 + 32 * q + 32 - rq.context <= CF::PLACES - CF::PLACE0))
+                            return;
                         const float dist0 = pos_f - static_cast<float>(key0 + 32 * q - rq.context);
                         const float *place = tree_place + buf * CF::PLACES + CF::PLACE0 + (key0 + 32 * q - rq.context);
 #pragma unroll
@@ -813,7 +818,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams p, i
     // the CTA whose run [c work / ctas, (c + 1) work / ctas) holds block g
     auto owner = [&](int g) { return static_cast<int>(((static_cast<int64_t>(g) + 1) * ctas - 1) / work); };
     const int c0 = owner(first), c1 = owner(first + blocks - 1);
-    if (c0 == c1)
+    if (c0 == c1 || !check_ok(b < p.B && c0 >= 0 && c0 < c1 && c1 < grid))
         return;
     const int hk = unit / p.row_tiles, rt = unit - hk * p.row_tiles;
     const int rows = min(p.tile_tokens, rq.tokens - rt * p.tile_tokens) * p.group;
