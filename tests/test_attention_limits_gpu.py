@@ -14,6 +14,7 @@ pytestmark = [pytest.mark.gpu,
 
 from attention_plain import Plain, close, rotate  # noqa: E402
 from test_attention_ex_gpu import CASES, problem  # noqa: E402
+from test_tree_attention_gpu import Cache  # noqa: E402
 
 # Documents that begin at or behind the last key: their queries see nothing, those before them in the same tile do
 PAST_THE_KEYS = {
@@ -35,6 +36,31 @@ def test_documents_that_begin_past_the_keys(name, dt):
     import tensor_core_gemm_tl_b200 as tg
     q, k, v, do, how, p = problem(PAST_THE_KEYS[name], dt, seed=len(name))
     lse = torch.full(q.shape[:3], 7.0, device="cuda")
+    out = tg.attention_ex(q, k, v, lse=lse, **how)
+    grads = tg.attention_backward(do, q, k, v, out, lse, **how)
+    assert tg.check_device() == 0
+    close("out", out, p.out, p.out_bound())
+    close("lse", lse, p.lse, p.lse_bound())
+    want, bounds = p.gradients(do)
+    for n, g, w, b in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(n, g, w, b)
+
+
+# ------------------------------------------------------------------ large counts
+LARGE_COUNTS = {
+    "heads": dict(shape=(300, 256, 128, 1, 3, 64), causal=True, offset=1),
+    "a_long_context": dict(shape=(1, 2, 1, 1, 150001, 64), causal=True, offset=150000, bias=True),
+    "a_long_context_128": dict(shape=(1, 3, 1, 5, 70003, 128), causal=True, offset=69998, cap=20.0, q_scale=3.0),
+    "many_queries": dict(shape=(1, 2, 1, 70001, 2, 64)),
+    "many_documents": dict(shape=(1, 1, 1, 6000, 6000, 64), docs=[list(range(0, 6001, 3))]),
+}
+
+
+@pytest.mark.parametrize("name", list(LARGE_COUNTS))
+def test_large_counts(name):
+    import tensor_core_gemm_tl_b200 as tg
+    q, k, v, do, how, p = problem(LARGE_COUNTS[name], "bf16", seed=len(name))
+    lse = torch.empty(q.shape[:3], device="cuda")
     out = tg.attention_ex(q, k, v, lse=lse, **how)
     grads = tg.attention_backward(do, q, k, v, out, lse, **how)
     assert tg.check_device() == 0
@@ -189,6 +215,35 @@ def test_capped_trees_repeat_bit_for_bit():
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), n
         tg.tree_attention((q * (n % 3)).contiguous(), vc, kc, table, context, score_cap=3.0)  # other bytes in shared memory
     assert tg.check_device() == 0
+
+
+@pytest.mark.parametrize("tokens,lens", [(1, False), (3, True)])
+def test_as_many_requests_as_are_allowed(tokens, lens):
+    import tensor_core_gemm_tl_b200 as tg
+    B = 4096
+    g = torch.Generator().manual_seed(tokens)
+    contexts = torch.randint(0, 300, (B,), generator=g).tolist()
+    live = torch.randint(0, tokens + 1, (B,), generator=g).tolist() if lens else [tokens] * B
+    c = Cache(contexts, tokens, 4, 2, 64, 16, "bf16", seed=B, live=live)
+    how = dict(tree_lens=torch.tensor(live, dtype=torch.int32, device="cuda")) if lens else {}
+    out, lse = torch.full_like(c.q, 3.0), torch.full(c.q.shape[:3], 3.0, device="cuda")
+    tg.tree_attention(c.q, c.k, c.v, c.table, c.context, out=out, lse=lse, **how)
+    assert tg.check_device() == 0
+    for b in range(B):
+        assert not lens or (out[b, :, live[b]:] == 3).all()
+    few = set(range(0, B, 67)) | {B - 1}
+    c.live = [n if b in few else 0 for b, n in enumerate(live)]
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("page", [8, 1000, 4096])
+def test_pages_of_many_rows_and_of_few(page):
+    import tensor_core_gemm_tl_b200 as tg
+    c = Cache([900, 2500, 5000, 0], 5, 8, 2, 128, page, "fp16", seed=page)
+    lse = torch.empty(c.q.shape[:3], device="cuda")
+    out = tg.tree_attention(c.q, c.k, c.v, c.table, c.context, lse=lse)
+    assert tg.check_device() == 0
+    c.check(out, lse)
 
 
 # ------------------------------------------------------------------ gradients against differences
