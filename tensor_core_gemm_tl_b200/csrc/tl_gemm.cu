@@ -73,10 +73,20 @@ tl_status ensure_pool(DeviceState *d)
     props.handleTypes = cudaMemHandleTypeNone;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
-    if (cudaMemPoolCreate(&d->pool, &props) != cudaSuccess)
+    // A stream capture, of this thread or another, forbids both calls below, though nothing of them enters its graph:
+    // the first call of a process may be a captured one.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess)
         return TL_ERR_CUDA;
+    cudaMemPool_t pool = nullptr;
+    const bool made = cudaMemPoolCreate(&pool, &props) == cudaSuccess;
     uint64_t keep = ~0ull;  // keep freed blocks for reuse by later calls
-    cudaMemPoolSetAttribute(d->pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (made)
+        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!made)
+        return TL_ERR_CUDA;
+    d->pool = pool;
     return TL_OK;
 }
 
