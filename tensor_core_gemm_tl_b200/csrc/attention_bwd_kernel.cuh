@@ -62,8 +62,10 @@
 // gradients of small losses lie below fp16's normal range, dX of large values
 // above it).  O being a mean of rows of V, |dX_ij| <= |dO_i . (V_j - O_i)| <=
 // 2 max |dO_i| max |V_j|, 2-norms of the queries and keys that count: the rows
-// kernel takes them, those of V in CTAs of their own.  The factors are powers of
-// two and leave with the fp32 sums.
+// kernel takes them, those of V in CTAs of their own (3 x 8 heads x 1001 x 1001 x
+// 64, with its forward: 70 -> 72 us; 4 x 16 heads on 4 x 4096 x 4096 x 128 with
+// documents: 552 -> 560).  The factors are powers of two and leave with the fp32
+// sums.
 #pragma once
 
 #include <type_traits>

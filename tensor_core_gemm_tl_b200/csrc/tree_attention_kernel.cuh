@@ -24,9 +24,9 @@
 // tree_combine_kernel joins.  A CTA prefetches across the ends of its pieces.
 //
 // Measured, 32 requests of 8192 keys, 8 key/value heads of 128, bf16, pages of 64:
-// 178 us, 6.0 TB/s (D = 64: 146 us, 3.7 TB/s: one warp holds the few rows, and its
-// latency bounds; capped, D = 128: 229 us); pages of 16: 204 us, with four times
-// the copies.  One request of 900 keys: 11 us,
+// 178 to 181 us, 6.0 TB/s (D = 64: 146 to 156 us, 3.4 to 3.7 TB/s: one warp holds
+// the few rows, and its latency bounds; capped, D = 128: 229 to 240 us); pages of
+// 16: 204 to 213 us, with four times the copies.  One request of 900 keys: 11 us,
 // of which its block takes 2; the rest is two launches and the reads of length,
 // table and page one after another.
 //
