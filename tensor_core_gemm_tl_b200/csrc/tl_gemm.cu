@@ -44,6 +44,7 @@ static std::unordered_map<int, DeviceState> g_dev;
 tl_status device_state(DeviceState **out)
 {
     int dev = 0;
+    cudaGetLastError();  // what an earlier call failed with (too little memory, say) is not this one's error
     if (cudaGetDevice(&dev) != cudaSuccess)
         return TL_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
