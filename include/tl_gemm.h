@@ -245,7 +245,9 @@ TL_API tl_status tl_attention_fwd(const void *Q, const void *K, const void *V, v
  * head_dim is 64 or 128; seq_q, seq_k and q_offset + seq_q at most 2^31 - 257.
  * Pointers are 16-byte aligned; strides are positive multiples of 8 elements,
  * the last dimension is contiguous.  Rows of K and V that no query sees must
- * still be finite (a weight of 0 times NaN is NaN).  Scale and cap are below
+ * still be finite, and so must their products with the rows of the others (a
+ * weight of 0 times NaN is NaN: NaN or infinity in a row of K or V may reach
+ * queries that do not see it).  Scale and cap are below
  * 1e38; with a cap, raw scores have to stay below 1e18, the cap is above 1e-30
  * and softmax_scale / score_cap between 1e-37 and 1e38.  Sums and softmax
  * statistics are fp32; the weights are rounded to `dtype` before the product
@@ -286,8 +288,8 @@ TL_API tl_status tl_attention_ex(const void *Q, const void *K, const void *V, vo
  * P and dX are rounded to `dtype` between the products (fp16 holds them scaled
  * by powers of two, dX by one that the largest rows of dO and V that count cannot
  * make too large); every sum is fp32 and has a fixed order, so results repeat bit for
- * bit.  Q and dO of queries that see no key do not count, but must be finite
- * (0 times NaN is NaN).  dQ, dK and dV must overlap neither the inputs nor one
+ * bit.  Q and dO of queries that see no key do not count, but must be finite, as
+ * must their products with rows of K and V (0 times NaN is NaN).  dQ, dK and dV must overlap neither the inputs nor one
  * another.  A stream-ordered temporary holds the row sums and intervals (about 8
  * bytes a query and head) and, where few tiles are cut into pieces, the pieces'
  * sums (at most eight pieces an SM, 1 KB a value of head_dim each).  Asynchronous
@@ -325,6 +327,7 @@ TL_API tl_status tl_attention_bwd(const void *dO, const void *Q, const void *K, 
  * 64 or 128.  Lengths on the device are held to what the table covers; a page
  * index outside the cache reads as zeros, table entries behind a request's last
  * key are not read, and rows of its last page behind that key may hold anything.
+ * NaN or infinity in the values of a request's new token may reach its others.
  * Works with any lengths for one captured graph: the host reads none of them.
  * Results repeat bit for bit on the same kind of device.  The joined pieces of
  * long requests live in a stream-ordered temporary (two an SM).  Lengths,

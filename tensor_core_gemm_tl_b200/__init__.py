@@ -315,8 +315,9 @@ def attention_ex(q, k, v, *, causal: bool = False, scale: float = 0.0, score_cap
     ``prefix`` (B, max(docs, 1)) int32 opens the first keys of each document (of
     the sequence) to causal queries.  Queries that see nothing give 0 and lse
     -inf.  Rows of k and v that no query sees -- a padded end, too -- must be
-    finite: a weight of 0 times NaN is NaN.  Returns out, shaped and by default
-    laid out like q; fills ``lse`` (B, H, Sq) float32 if given.
+    finite, and so must their products with the rows of the others: a weight of 0
+    times NaN is NaN.  Returns out, shaped and by default laid out like q; fills
+    ``lse`` (B, H, Sq) float32 if given.  ``out`` must not overlap an input.
 
     out carries no autograd graph; its gradients are attention_backward's, from
     out and ``lse``."""
@@ -344,8 +345,9 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False, scale: 
     """Gradients (dq, dk, dv) of attention_ex, from its inputs, its ``out`` and
     ``lse`` and the gradient ``dout`` of out; the options are the forward's.
     dk and dv are summed over the heads that share them.  What no query sees, and
-    queries that see nothing, do not count but must be finite.  Results repeat bit
-    for bit.  ``slopes`` are constants (a tensor that requires grad is refused)."""
+    queries that see nothing, do not count but must be finite, as must their
+    products with the other rows.  The gradients must overlap neither the inputs nor
+    one another.  Results repeat bit for bit.  ``slopes`` are constants (a tensor that requires grad is refused)."""
     import torch
     head, strides, dt = _attention_arguments(q, k, v, causal, scale, score_cap, slopes, doc_offsets, prefix, q_offset)
     B, H, Sq, D = q.shape
