@@ -247,15 +247,14 @@ TL_API tl_status tl_attention_fwd(const void *Q, const void *K, const void *V, v
  * the last dimension is contiguous.  Rows of K and V that no query sees must
  * still be finite, and so must their products with the rows of the others (a
  * weight of 0 times NaN is NaN: NaN or infinity in a row of K or V may reach
- * queries that do not see it).  Scale and cap are below
- * 1e38; with a cap, raw scores have to stay below 1e18, the cap is above 1e-30
- * and softmax_scale / score_cap between 1e-37 and 1e38.  Sums and softmax
- * statistics are fp32; the weights are rounded to `dtype` before the product
- * with V and O is rounded once.  Where the batch has few rows the keys are split
- * over the SMs and joined from a stream-ordered temporary, by a rule on the
- * sizes: results repeat bit for bit on the same kind of device.  Asynchronous on
- * `stream`; bounded waits
- * report through tl_check_device; O must not overlap an input.
+ * queries that do not see it).  Scale and cap are below 1e38; with a cap, raw
+ * scores have to stay below 1e18, the cap is above 1e-30 and softmax_scale /
+ * score_cap between 1e-37 and 1e38.  Sums and softmax statistics are fp32; the
+ * weights are rounded to `dtype` before the product with V and O is rounded once.
+ * Where the batch has few rows the keys are split over the SMs and joined from a
+ * stream-ordered temporary, by a rule on the sizes: results repeat bit for bit on
+ * the same kind of device.  Asynchronous on `stream`; bounded waits report through
+ * tl_check_device; O must not overlap an input.
  */
 typedef struct {
     int32_t causal;              /* 1: query i sees keys j <= q_offset + i            */
